@@ -35,11 +35,9 @@
 // streaming each expert's weights once bounds the GEMM anyway.)
 // Every mbarrier wait is bounded on the global timer; a time-out records
 // MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -101,32 +99,6 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-// 32 lanes x 32 consecutive fp32 columns of TMEM into registers.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
-        "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
-        "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
 // Drain one 128 x 256 fp32 accumulator to bf16 rows of Y.  Epilogue warp ew
 // owns TMEM lanes 32ew .. 32ew+31 (rows r0 + 32ew ..); 64 columns at a time,
 // each lane converts its row (nearest-even) into the warp's padded staging
@@ -223,73 +195,6 @@ constexpr int kPairRingBytes = kPairStages * kPairKB * (kSubA + kSubB);  // 192 
 constexpr int kPairSmemBytes = kPairRingBytes + kEpiBytes + 1024;
 constexpr int BM2 = 2 * BM;                     // rows of a pair block
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-// Address of the same shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-
-// 2-D tile into this CTA's shared memory; completion bytes counted on the
-// mbarrier at cluster address `mbar` (rank 0's barrier for both ranks).
-__device__ __forceinline__ void tma_load_2d_pair(void* sdst, const CUtensorMap* map, int x, int y,
-                                                 uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(sdst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t dtmem, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, int accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dtmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrive on the barrier at this offset in the CTAs of the pair that `mask`
-// names (bit c = rank c) once the issuing thread's earlier MMAs have
-// completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask = 0x3) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_addr(bar)),
-      "h"(mask)
-      : "memory");
-}
-
-// Bounded wait with cluster-scope acquire, for barriers that receive
-// arrivals from the other CTA of the pair.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
-  for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((it & 63) == 63 && globaltimer_ns() > deadline_ns) return false;
-  }
-}
-
 // 16 bytes from this CTA's shared memory to `dst` in another CTA of the
 // cluster, the bytes counted on the mbarrier `mbar` there: a signal that
 // travels through the async proxy (no cluster-scope release fence).
@@ -298,10 +203,6 @@ __device__ __forceinline__ void bulk_signal_s2s(uint32_t dst, const void* src, u
       "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
       "r"(smem_addr(src)), "r"(mbar)
       : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
 __device__ __forceinline__ uint32_t mma_idesc_pair() {
@@ -622,20 +523,6 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
                  "r"(kTmemCols)
                  : "memory");
   if (threadIdx.x == 0 && s_err) raise_status(p.status, MOE_DEV_TIMEOUT);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  // a function-local static initialises once, thread-safe
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
-  return fn;
 }
 
 // 2-D bf16 row-major [outer, inner] tensor, box (BK inner) x box_rows, 128-B swizzle.
