@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -27,7 +28,8 @@ MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_DEV_NONFINITE, MOE_DEV_BAD_ROUTE, MOE_DEV_TIMEOUT, MOE_DEV_ROWS_EXCEEDED = 0x1, 0x2, 0x4, 0x8
 KERNELS = ["topk_gate", "layout", "dispatch", "combine", "combine_bwd", "dispatch_bwd", "topk_gate_bwd",
            "grouped_gemm", "dispatch_gemm", "rank_slots", "combine_gate_bwd", "gate_layout", "ep_pack", "ep_unpack",
-           "ep_dispatch", "ep_combine"]
+           "ep_dispatch", "ep_combine", "layernorm", "layernorm_bwd", "balance", "balance_bwd", "linear",
+           "linear_bwd"]
 KERNEL_ID = {n: i for i, n in enumerate(KERNELS)}
 
 # every entry point the header declares (checked by the CPU test-suite)
@@ -38,6 +40,8 @@ EXPORTS = [
     "moe_dispatch_layout_noalloc", "moe_topk_gate_bwd", "moe_dispatch_layout_ex", "moe_grouped_gemm",
     "moe_dispatch_grouped_gemm", "moe_combine_gate_bwd", "moe_layout_create", "moe_layout_rebuild",
     "moe_topk_gate_layout", "moe_ep_pack", "moe_ep_dispatch", "moe_ep_combine", "moe_ep_unpack_dgate",
+    "moe_layernorm", "moe_layernorm_bwd", "moe_layernorm_bwd_workspace", "moe_balance_loss", "moe_balance_loss_bwd",
+    "moe_balance_loss_workspace", "moe_linear", "moe_linear_workspace", "moe_linear_bwd", "moe_linear_bwd_workspace",
 ]
 
 
@@ -65,6 +69,18 @@ class LayoutInfo(ctypes.Structure):
                                        "token_in_rank", "rank_counts", "status", "inv_row", "rank_slot")]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("s", "K", "N", "act", "out_dtype", "bias_dtype", "residual_dtype")] + [
+        (n, ctypes.c_int64) for n in ("ldx", "ldw", "ldres")]
+
+
+class LinearBwdDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("s", "K", "N", "act", "dy_dtype", "dx_dtype", "dw_dtype")] + [
+        (n, ctypes.c_int64) for n in ("lddy", "ldx", "ldw", "ldz")]
+
+
+ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
 _lib = None
 
 
@@ -77,6 +93,7 @@ def lib() -> ctypes.CDLL:
                                "g.build()\"` (nvcc, sm_103a); there is no CPU fallback")
         L = ctypes.CDLL(LIB_PATH)
         P, I, U = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64
+        I64, F, Z = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
         sig = {
             "moe_topk_gate": [P, I, I, I, I, P, P, P, P],
             "moe_topk_gate_bwd": [P, P, P, P, I, I, I, I, P, P],
@@ -101,11 +118,25 @@ def lib() -> ctypes.CDLL:
             "moe_handle_destroy": [P],
             "moe_debug_hold_layout_tile": [I, I],
             "moe_dispatch_layout_noalloc": [P, I, I, I, I, I] + [P] * 11,
+            "moe_layernorm": [I, I, I, P, I64, I, P, P, F, P, P, P, P],
+            "moe_layernorm_bwd": [I, I, I, P, I64, P, I64, I, P, P, P, P, I64, P, P, P, P, Z, P],
+            "moe_balance_loss": [P, P, P, P, I, I, I, I, P, P, P, P, P, P, P, Z, P, P],
+            "moe_balance_loss_bwd": [P] * 8 + [I, I, I, P, P],
+            "moe_linear": [ctypes.POINTER(LinearDesc)] + [P] * 7 + [Z, P, P],
+            "moe_linear_bwd": [ctypes.POINTER(LinearBwdDesc)] + [P] * 8 + [Z, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = I
+        for name in ("moe_layernorm_bwd_workspace", "moe_balance_loss_workspace"):
+            f = getattr(L, name)
+            f.argtypes = [I, I]
+            f.restype = Z
+        for name in ("moe_linear_workspace", "moe_linear_bwd_workspace"):
+            f = getattr(L, name)
+            f.argtypes = [I, I, I]
+            f.restype = Z
         L.moe_capacity.argtypes = [ctypes.c_double, I, I, I]
         L.moe_capacity.restype = I
         L.moe_status_string.argtypes = [I]
@@ -130,6 +161,20 @@ def _ptr(t: torch.Tensor | None):
     if not t.is_contiguous():
         raise ValueError("tensors passed to the MoE library must be contiguous")
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
+
+
+def _rows_ptr(t: torch.Tensor | None):
+    """Pointer and row stride (elements) of a 2-D tensor whose rows are contiguous; the rows may be apart."""
+    if t is None:
+        return None, 0
+    s, m = t.shape
+    if m > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of tensors passed to the MoE library must be contiguous")
+    # with at most one row the stride is never used
+    ld = t.stride(0) if s > 1 else m
+    if ld < m:
+        raise ValueError("rows that overlap (a broadcast or a negative stride) are not supported")
+    return (t.data_ptr() if t.numel() else None), ld
 
 
 def _stream(device: torch.device):
@@ -546,3 +591,221 @@ def moe_dispatch_grouped_gemm(h: Handle, x: torch.Tensor, W: torch.Tensor,
     _check(lib().moe_dispatch_grouped_gemm(h.raw, s, h.rows, K, N, _ptr(x), _ptr(W), _ptr(Y),
                                            _stream(x.device)), "moe_dispatch_grouped_gemm")
     return Y
+
+
+# ------------------------------------- layer norm, balance loss, products --
+
+def _same_device(where: str, dev: torch.device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise MoEError(1, where, "the tensors live on different devices")
+
+
+def _norm_weights(where: str, m: int, weight, bias):
+    wt = weight if weight is not None else bias
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (tuple(t.shape) != (m,) or t.dtype != wt.dtype):
+            raise MoEError(1, where, f"{name} must be [m], weight and bias of one dtype")
+    return MOE_F32 if wt is None else _dtype(wt)
+
+
+def moe_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                  eps: float = 1e-5, y: torch.Tensor | None = None, stats: bool = True):
+    """x [s,m] f32 or bf16 (rows may be strided), weight and bias [m] f32 or
+    bf16 -> (y [s,m], mean f32 [s], rstd f32 [s]); stats=False returns y alone."""
+    s, m = _rows2(x, "x")
+    dev = x.device
+    wd = _norm_weights("moe_layernorm", m, weight, bias)
+    _same_device("moe_layernorm", dev, weight, bias, y)
+    if y is None:
+        y = torch.empty(s, m, dtype=x.dtype, device=dev)
+    if tuple(y.shape) != (s, m) or y.dtype != x.dtype:
+        raise MoEError(1, "moe_layernorm", "output shape")
+    mean = torch.empty(s, dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(s, dtype=torch.float32, device=dev) if stats else None
+    px, ldx = _rows_ptr(x)
+    rc = lib().moe_layernorm(s, m, _dtype(x), px, ldx, wd, _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
+                             _ptr(rstd), _stream(dev))
+    _check(rc, "moe_layernorm")
+    return (y, mean, rstd) if stats else y
+
+
+def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                      rstd: torch.Tensor, dres: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                      need_dweight: bool = True, need_dbias: bool = True):
+    """(dy, x [s,m], weight [m] or None, mean, rstd f32 [s]) -> (dx [s,m],
+    dweight f32 [m] or None, dbias f32 [m] or None).  dres [s,m]: a gradient
+    that reaches x past the norm (the residual branch), added to dx."""
+    s, m = _rows2(x, "x")
+    dev = x.device
+    for t, name in ((dy, "dy"), (dres, "dres"), (dx, "dx")):
+        if t is not None and (tuple(t.shape) != (s, m) or t.dtype != x.dtype):
+            raise MoEError(1, "moe_layernorm_bwd", f"{name} must have x's shape and dtype")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if tuple(t.shape) != (s,) or t.dtype != torch.float32:
+            raise MoEError(1, "moe_layernorm_bwd", f"{name} must be float32 [s]")
+    wd = _norm_weights("moe_layernorm_bwd", m, weight, None)
+    _same_device("moe_layernorm_bwd", dev, dy, weight, mean, rstd, dres, dx)
+    if dx is None:
+        dx = torch.empty(s, m, dtype=x.dtype, device=dev)
+    dw = torch.empty(m, dtype=torch.float32, device=dev) if need_dweight else None
+    db = torch.empty(m, dtype=torch.float32, device=dev) if need_dbias else None
+    nbytes = lib().moe_layernorm_bwd_workspace(s, m) if need_dweight or need_dbias else 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    pdy, lddy = _rows_ptr(dy)
+    px, ldx = _rows_ptr(x)
+    pres, ldres = _rows_ptr(dres)
+    rc = lib().moe_layernorm_bwd(s, m, _dtype(x), pdy, lddy, px, ldx, wd, _ptr(weight), _ptr(mean), _ptr(rstd), pres,
+                                 ldres, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nbytes, _stream(dev))
+    _check(rc, "moe_layernorm_bwd")
+    return dx, dw, db
+
+
+class BalanceLoss(NamedTuple):
+    """What moe_balance_loss returns; lse, coef and norm feed its backward pass."""
+    loss: torch.Tensor       # f32 [2]: the balance loss, the z loss
+    counts: torch.Tensor     # i32 [num_seqs, e]: valid routes per expert
+    mean_prob: torch.Tensor  # f32 [num_seqs, e]: mean router probability
+    lse: torch.Tensor        # f32 [s]
+    coef: torch.Tensor       # f32 [num_seqs, e]
+    norm: torch.Tensor       # f32 [2]
+
+
+def _check_balance(where: str, s: int, e: int, logits, valid, seq_offsets) -> int:
+    if logits.dtype != torch.float32:
+        raise MoEError(3, where, "logits must be float32")
+    if valid is not None and (tuple(valid.shape) != (s,) or valid.dtype not in (torch.uint8, torch.bool)):
+        raise MoEError(1, where, "valid must be uint8 or bool [s]")
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.dtype != torch.int32 or seq_offsets.numel() < 2:
+        raise MoEError(1, where, "seq_offsets must be int32 [num_seqs + 1]")
+    return seq_offsets.numel() - 1
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Tensor | None = None,
+                     seq_offsets: torch.Tensor | None = None, device_status: torch.Tensor | None = None) -> BalanceLoss:
+    """logits f32 [s,e], topk_idx i32 [s,k] (-1: absent), valid u8/bool [s]
+    (padding is 0), seq_offsets i32 [num_seqs+1] -> BalanceLoss."""
+    s, e = _rows2(logits, "logits")
+    if topk_idx.dim() != 2 or topk_idx.dtype != torch.int32 or topk_idx.shape[0] != s:
+        raise MoEError(1, "moe_balance_loss", "topk_idx must be int32 [s, k]")
+    n = _check_balance("moe_balance_loss", s, e, logits, valid, seq_offsets)
+    dev = logits.device
+    _same_device("moe_balance_loss", dev, topk_idx, valid, seq_offsets, device_status)
+    f32 = dict(dtype=torch.float32, device=dev)
+    r = BalanceLoss(torch.empty(2, **f32), torch.empty(n, e, dtype=torch.int32, device=dev), torch.empty(n, e, **f32),
+                    torch.empty(s, **f32), torch.empty(n, e, **f32), torch.empty(2, **f32))
+    nbytes = lib().moe_balance_loss_workspace(e, n)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(seq_offsets), s, e,
+                                topk_idx.shape[1], n, _ptr(r.loss), _ptr(r.counts), _ptr(r.mean_prob), _ptr(r.lse),
+                                _ptr(r.coef), _ptr(r.norm), _ptr(ws), nbytes, _ptr(device_status), _stream(dev))
+    _check(rc, "moe_balance_loss")
+    return r
+
+
+def moe_balance_loss_bwd(logits: torch.Tensor, lse: torch.Tensor, coef: torch.Tensor, norm: torch.Tensor,
+                         dloss: torch.Tensor, valid: torch.Tensor | None = None,
+                         seq_offsets: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                         dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """dloss f32 [2] (the gradients reaching the two losses) -> dlogits f32
+    [s,e], plus add [s,e] (may be dlogits itself) where given."""
+    s, e = _rows2(logits, "logits")
+    n = _check_balance("moe_balance_loss_bwd", s, e, logits, valid, seq_offsets)
+    dev = logits.device
+    for t, name, shape in ((lse, "lse", (s,)), (coef, "coef", (n, e)), (norm, "norm", (2,)), (dloss, "dloss", (2,)),
+                           (add, "add", (s, e)), (dlogits, "dlogits", (s, e))):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32):
+            raise MoEError(1, "moe_balance_loss_bwd", f"{name} must be float32 {list(shape)}")
+    _same_device("moe_balance_loss_bwd", dev, lse, coef, norm, dloss, valid, seq_offsets, add, dlogits)
+    if dlogits is None:
+        dlogits = torch.empty(s, e, dtype=torch.float32, device=dev)
+    rc = lib().moe_balance_loss_bwd(_ptr(logits), _ptr(lse), _ptr(coef), _ptr(norm), _ptr(dloss), _ptr(valid),
+                                    _ptr(seq_offsets), _ptr(add), s, e, n, _ptr(dlogits), _stream(dev))
+    _check(rc, "moe_balance_loss_bwd")
+    return dlogits
+
+
+def _act(where: str, act: str) -> int:
+    if act not in ACT:
+        raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
+    return ACT[act]
+
+
+def _check_linear(where: str, x: torch.Tensor, W: torch.Tensor):
+    s, K = _rows2(x, "x")
+    N, KW = _rows2(W, "W")
+    if KW != K:
+        raise MoEError(1, where, "W must be [N, K]")
+    if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise MoEError(3, where, "x and W must be bf16")
+    return s, K, N
+
+
+def moe_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+               residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, save_z: bool = False,
+               y: torch.Tensor | None = None, device_status: torch.Tensor | None = None):
+    """y [s,N] = act(x W^T + bias) + residual on the tensor cores: x bf16
+    [s,K], W bf16 [N,K] (rows may be strided; K a multiple of 8), bias [N] and
+    residual [s,N] f32 or bf16, y f32 or bf16 (default bf16); act: none, relu,
+    gelu, gelu_tanh, silu.  save_z: return (y, z), z bf16 [s,N] the value
+    before the activation, for moe_linear_bwd."""
+    s, K, N = _check_linear("moe_linear", x, W)
+    dev = x.device
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if y is None else y.dtype
+    if bias is not None and tuple(bias.shape) != (N,):
+        raise MoEError(1, "moe_linear", "bias must be [N]")
+    if residual is not None and tuple(residual.shape) != (s, N):
+        raise MoEError(1, "moe_linear", "residual must be [s, N]")
+    _same_device("moe_linear", dev, W, bias, residual, y, device_status)
+    if y is None:
+        y = torch.empty(s, N, dtype=out_dtype, device=dev)
+    if tuple(y.shape) != (s, N) or y.dtype != out_dtype:
+        raise MoEError(1, "moe_linear", "output shape or dtype")
+    z = torch.empty(s, N, dtype=torch.bfloat16, device=dev) if save_z else None
+    nbytes = lib().moe_linear_workspace(s, K, N)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    px, ldx = _rows_ptr(x)
+    pw, ldw = _rows_ptr(W)
+    pres, ldres = _rows_ptr(residual)
+    d = LinearDesc(s, K, N, _act("moe_linear", act), _dtype(y), 0 if bias is None else _dtype(bias),
+                   0 if residual is None else _dtype(residual), ldx, ldw, ldres)
+    rc = lib().moe_linear(ctypes.byref(d), px, pw, _ptr(bias), pres, _ptr(y), _ptr(z), _ptr(ws), nbytes,
+                          _ptr(device_status), _stream(dev))
+    _check(rc, "moe_linear")
+    return (y, z) if save_z else y
+
+
+def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.Tensor | None = None,
+                   act: str = "none", need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                   dx_dtype: torch.dtype = torch.bfloat16, dw_dtype: torch.dtype = torch.bfloat16,
+                   device_status: torch.Tensor | None = None):
+    """(dy [s,N] f32 or bf16, x bf16 [s,K], W bf16 [N,K], z bf16 [s,N] with an
+    activation) -> (dx [s,K], dW [N,K], db f32 [N]), None for those not
+    needed.  The residual's gradient is dy itself."""
+    s, K, N = _check_linear("moe_linear_bwd", x, W)
+    dev = x.device
+    if tuple(dy.shape) != (s, N):
+        raise MoEError(1, "moe_linear_bwd", "dy must be [s, N]")
+    if act != "none" and (z is None or tuple(z.shape) != (s, N) or z.dtype != torch.bfloat16):
+        raise MoEError(1, "moe_linear_bwd", "z must be bf16 [s, N] with an activation")
+    if act == "none":
+        z = None
+    _same_device("moe_linear_bwd", dev, dy, W, z, device_status)
+    dx = torch.empty(s, K, dtype=dx_dtype, device=dev) if need_dx else None
+    dW = torch.empty(N, K, dtype=dw_dtype, device=dev) if need_dw else None
+    db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
+    nbytes = lib().moe_linear_bwd_workspace(s, K, N)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    pdy, lddy = _rows_ptr(dy)
+    px, ldx = _rows_ptr(x)
+    pw, ldw = _rows_ptr(W)
+    pz, ldz = _rows_ptr(z)
+    d = LinearBwdDesc(s, K, N, _act("moe_linear_bwd", act), _dtype(dy), 0 if dx is None else _dtype(dx),
+                      0 if dW is None else _dtype(dW), lddy, ldx, ldw, ldz)
+    rc = lib().moe_linear_bwd(ctypes.byref(d), pdy, px, pw, pz, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), nbytes,
+                              _ptr(device_status), _stream(dev))
+    _check(rc, "moe_linear_bwd")
+    return dx, dW, db

@@ -10,6 +10,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <unordered_set>
@@ -950,6 +951,246 @@ moe_status moe_dispatch_layout_noalloc(const int32_t* topk_idx, int s, int e, in
   if (err != cudaSuccess) return cuda_fail(err, "allocation-free layout launch");
   g_launches[MOE_KERNEL_LAYOUT]++;
   return MOE_OK;
+}
+
+namespace {
+
+moe_status check_dtype(moe_dtype dt, const char* name) {
+  if (dt == MOE_F32 || dt == MOE_BF16) return MOE_OK;
+  return fail(MOE_ERR_DTYPE, std::string(name) + " must be fp32 or bf16");
+}
+
+moe_status check_ld(int64_t ld, int m, const char* name) {
+  if (ld < m) return fail(MOE_ERR_INVALID_ARG, std::string(name) + " is shorter than a row");
+  if (ld > (int64_t)1 << 40) return fail(MOE_ERR_INVALID_ARG, std::string(name) + " is too large");
+  return MOE_OK;
+}
+
+// A call's pointers: those that must be there, then residency of all.
+struct PtrArg {
+  const void* p;
+  const char* name;
+  bool nullable;
+};
+moe_status check_ptrs(std::initializer_list<PtrArg> args, int* dev) {
+  for (const PtrArg& a : args) MOE_TRY(check_ptr(a.p, a.name, a.nullable));
+  MOE_TRY(current_device(dev));
+  for (const PtrArg& a : args) MOE_TRY(check_device_ptr(a.p, a.name, *dev));
+  return MOE_OK;
+}
+
+constexpr int kMaxNormM = 1 << 30;
+
+moe_status check_norm(int s, int m, moe_dtype dtype, moe_dtype weight_dtype) {
+  MOE_TRY(check_dtype(dtype, "dtype"));
+  MOE_TRY(check_dtype(weight_dtype, "weight_dtype"));
+  if (s < 0 || m < 1 || m > kMaxNormM) return fail(MOE_ERR_INVALID_ARG, "need s >= 0 and 1 <= m <= 2^30");
+  return MOE_OK;
+}
+
+moe_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (have < need)
+    return fail(MOE_ERR_INVALID_ARG, "the workspace has " + std::to_string(have) + " bytes, the call needs " + std::to_string(need));
+  return check_ptr(ws, "workspace", need == 0);
+}
+
+moe_status check_balance(int s, int e, int num_seqs, const void* seq_offsets) {
+  if (s < 0 || e < 1 || e > kMaxE) return fail(MOE_ERR_INVALID_ARG, "need s >= 0 and 1 <= e <= 256");
+  if ((long long)s * e > 2147483647LL) return fail(MOE_ERR_INVALID_ARG, "s*e must be < 2^31");
+  if (num_seqs < 1 || num_seqs > (1 << 24)) return fail(MOE_ERR_INVALID_ARG, "num_seqs must be in [1, 2^24]");
+  if (!seq_offsets && num_seqs != 1) return fail(MOE_ERR_INVALID_ARG, "num_seqs must be 1 without seq_offsets");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_layernorm(int s, int m, moe_dtype dtype, const void* x, int64_t ldx, moe_dtype weight_dtype,
+                         const void* weight, const void* bias, float eps, void* y, float* mean, float* rstd,
+                         void* stream) {
+  MOE_TRY(check_norm(s, m, dtype, weight_dtype));
+  MOE_TRY(check_ld(ldx, m, "ldx"));
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (s == 0) return MOE_OK;
+  int dev = 0;
+  MOE_TRY(check_ptrs({{x, "x", false}, {weight, "weight", true}, {bias, "bias", true}, {y, "y", false},
+                      {mean, "mean", true}, {rstd, "rstd", true}}, &dev));
+  const int wd = weight_dtype == MOE_F32 ? 0 : 1;
+  cudaError_t err = moe::launch_layernorm(x, ldx, s, m, dtype == MOE_F32 ? 0 : 1, weight, wd, bias, wd, eps, y, mean,
+                                          rstd, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "layernorm launch");
+  g_launches[MOE_KERNEL_LAYERNORM]++;
+  return MOE_OK;
+}
+
+size_t moe_layernorm_bwd_workspace(int s, int m) {
+  if (s < 1 || m < 1) return 0;
+  return 2 * sizeof(float) * (size_t)moe::layernorm_bwd_parts(s) * (size_t)m;
+}
+
+moe_status moe_layernorm_bwd(int s, int m, moe_dtype dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                             moe_dtype weight_dtype, const void* weight, const float* mean, const float* rstd,
+                             const void* dres, int64_t lddres, void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_TRY(check_norm(s, m, dtype, weight_dtype));
+  MOE_TRY(check_ld(lddy, m, "lddy"));
+  MOE_TRY(check_ld(ldx, m, "ldx"));
+  if (dres) MOE_TRY(check_ld(lddres, m, "lddres"));
+  const bool sums = dweight || dbias, rows = s > 0;
+  if (!rows && !sums) return MOE_OK;
+  MOE_TRY(check_workspace(workspace, workspace_bytes, sums ? moe_layernorm_bwd_workspace(s, m) : 0));
+  int dev = 0;
+  MOE_TRY(check_ptrs({{dy, "dy", !rows}, {x, "x", !rows}, {weight, "weight", true}, {mean, "mean", !rows},
+                      {rstd, "rstd", !rows}, {dres, "dres", true}, {dx, "dx", !rows}, {dweight, "dweight", true},
+                      {dbias, "dbias", true}, {workspace, "workspace", true}}, &dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
+  cudaError_t err = moe::launch_layernorm_bwd(dy, lddy, x, ldx, dres, lddres, s, m, dtype == MOE_F32 ? 0 : 1, weight,
+                                              weight_dtype == MOE_F32 ? 0 : 1, mean, rstd, dx, dweight, dbias,
+                                              static_cast<float*>(workspace), *di, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "layernorm_bwd launch");
+  g_launches[MOE_KERNEL_LAYERNORM_BWD]++;
+  return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace(int e, int num_seqs) {
+  if (e < 1 || e > kMaxE || num_seqs < 1) return 0;
+  return moe::balance_workspace(e, num_seqs);
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid,
+                            const int32_t* seq_offsets, int s, int e, int k, int num_seqs, float* loss,
+                            int32_t* counts, float* mean_prob, float* lse, float* coef, float* norm, void* workspace,
+                            size_t workspace_bytes, int32_t* device_status, void* stream) {
+  MOE_TRY(check_balance(s, e, num_seqs, seq_offsets));
+  if (k < 1 || k > kMaxK) return fail(MOE_ERR_INVALID_ARG, "need 1 <= k <= 16");
+  if ((long long)s * k > 2147483647LL) return fail(MOE_ERR_INVALID_ARG, "s*k must be < 2^31");
+  if (device_status && (reinterpret_cast<uintptr_t>(device_status) & 3u))
+    return fail(MOE_ERR_INVALID_ARG, "device_status is not 4-byte aligned");
+  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_balance_loss_workspace(e, num_seqs)));
+  const bool none = s == 0;
+  int dev = 0;
+  MOE_TRY(check_ptrs({{logits, "logits", none}, {topk_idx, "topk_idx", none}, {loss, "loss", false},
+                      {counts, "counts", false}, {mean_prob, "mean_prob", false}, {lse, "lse", none},
+                      {coef, "coef", false}, {norm, "norm", false}, {workspace, "workspace", false}}, &dev));
+  MOE_TRY(check_device_ptr(valid, "valid", dev));
+  MOE_TRY(check_device_ptr(seq_offsets, "seq_offsets", dev));
+  MOE_TRY(check_device_ptr(device_status, "device_status", dev));
+  if (reinterpret_cast<uintptr_t>(seq_offsets) & 3u) return fail(MOE_ERR_INVALID_ARG, "seq_offsets is not 4-byte aligned");
+  cudaError_t err = moe::launch_balance(logits, topk_idx, valid, seq_offsets, s, e, k, num_seqs, loss, counts,
+                                        mean_prob, lse, coef, norm, workspace, device_status,
+                                        static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "balance_loss launch");
+  g_launches[MOE_KERNEL_BALANCE]++;
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
+                                const float* dloss, const uint8_t* valid, const int32_t* seq_offsets,
+                                const float* add, int s, int e, int num_seqs, float* dlogits, void* stream) {
+  MOE_TRY(check_balance(s, e, num_seqs, seq_offsets));
+  if (s == 0) return MOE_OK;
+  int dev = 0;
+  MOE_TRY(check_ptrs({{logits, "logits", false}, {lse, "lse", false}, {coef, "coef", false}, {norm, "norm", false},
+                      {add, "add", true}, {dlogits, "dlogits", false}}, &dev));
+  if (!dloss || (reinterpret_cast<uintptr_t>(dloss) & 3u)) return fail(MOE_ERR_INVALID_ARG, "dloss is NULL or not 4-byte aligned");
+  if (reinterpret_cast<uintptr_t>(seq_offsets) & 3u) return fail(MOE_ERR_INVALID_ARG, "seq_offsets is not 4-byte aligned");
+  MOE_TRY(check_device_ptr(dloss, "dloss", dev));
+  MOE_TRY(check_device_ptr(valid, "valid", dev));
+  MOE_TRY(check_device_ptr(seq_offsets, "seq_offsets", dev));
+  cudaError_t err = moe::launch_balance_bwd(logits, lse, coef, norm, dloss, valid, seq_offsets, add, s, e, num_seqs,
+                                            dlogits, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "balance_loss_bwd launch");
+  g_launches[MOE_KERNEL_BALANCE_BWD]++;
+  return MOE_OK;
+}
+
+namespace {
+
+moe_status check_linear(int s, int K, int N, int act, int64_t ldx, int64_t ldw, bool need_x, bool need_w) {
+  if (s < 0 || K < 8 || K % 8 != 0 || N < 1)
+    return fail(MOE_ERR_INVALID_ARG, "need s >= 0, N >= 1 and K a positive multiple of 8");
+  if (s > (1 << 30) || K > (1 << 30) || N > (1 << 30)) return fail(MOE_ERR_INVALID_ARG, "s, K and N must be <= 2^30");
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID_ARG, "unknown activation");
+  if (need_x) MOE_TRY(check_ld(ldx, K, "ldx"));
+  if (need_w) MOE_TRY(check_ld(ldw, K, "ldw"));
+  if ((need_x && ldx % 8 != 0) || (need_w && ldw % 8 != 0))
+    return fail(MOE_ERR_INVALID_ARG, "ldx and ldw must be multiples of 8 (rows of whole 16 bytes)");
+  return MOE_OK;
+}
+
+moe_status check_status_ptr(const int32_t* status) {
+  if (reinterpret_cast<uintptr_t>(status) & 3u) return fail(MOE_ERR_INVALID_ARG, "device_status is not 4-byte aligned");
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_linear_workspace(int s, int K, int N) {
+  if (s < 1 || K < 1 || N < 1) return 0;
+  return moe::linear_workspace(s, K, N);
+}
+
+moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* W, const void* bias,
+                      const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
+                      int32_t* device_status, void* stream) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+  MOE_TRY(check_linear(d->s, d->K, d->N, d->act, d->ldx, d->ldw, true, true));
+  MOE_TRY(check_dtype((moe_dtype)d->out_dtype, "out_dtype"));
+  if (bias) MOE_TRY(check_dtype((moe_dtype)d->bias_dtype, "bias_dtype"));
+  if (residual) {
+    MOE_TRY(check_dtype((moe_dtype)d->residual_dtype, "residual_dtype"));
+    MOE_TRY(check_ld(d->ldres, d->N, "ldres"));
+  }
+  MOE_TRY(check_status_ptr(device_status));
+  if (d->s == 0) return MOE_OK;
+  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_workspace(d->s, d->K, d->N)));
+  int dev = 0;
+  MOE_TRY(check_ptrs({{x, "x", false}, {W, "W", false}, {bias, "bias", true}, {residual, "residual", true},
+                      {y, "y", false}, {z, "z", true}, {workspace, "workspace", true}}, &dev));
+  MOE_TRY(check_device_ptr(device_status, "device_status", dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
+  moe::LinearArgs a = {x, W, bias, residual, y, z, workspace, device_status, d->ldx, d->ldw, d->ldres, d->s, d->K, d->N,
+                       d->act, d->out_dtype == MOE_F32, d->bias_dtype == MOE_F32, d->residual_dtype == MOE_F32};
+  return gemm_result(moe::launch_linear(a, *di, static_cast<cudaStream_t>(stream)), "linear launch", MOE_KERNEL_LINEAR);
+}
+
+size_t moe_linear_bwd_workspace(int s, int K, int N) {
+  if (s < 1 || K < 1 || N < 1) return 0;
+  return moe::linear_bwd_workspace(s, K, N);
+}
+
+moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const void* x, const void* W,
+                          const void* z, void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
+                          int32_t* device_status, void* stream) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+  MOE_TRY(check_linear(d->s, d->K, d->N, d->act, d->ldx, d->ldw, dW != nullptr, dx != nullptr));
+  MOE_TRY(check_dtype((moe_dtype)d->dy_dtype, "dy_dtype"));
+  MOE_TRY(check_ld(d->lddy, d->N, "lddy"));
+  if (dx) MOE_TRY(check_dtype((moe_dtype)d->dx_dtype, "dx_dtype"));
+  if (dW) MOE_TRY(check_dtype((moe_dtype)d->dw_dtype, "dw_dtype"));
+  const bool need_z = d->act != MOE_ACT_NONE, none = d->s == 0;
+  if (need_z) MOE_TRY(check_ld(d->ldz, d->N, "ldz"));
+  MOE_TRY(check_status_ptr(device_status));
+  if (!dx && !dW && !db) return MOE_OK;
+  if (none && !dW && !db) return MOE_OK;
+  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_bwd_workspace(d->s, d->K, d->N)));
+  int dev = 0;
+  MOE_TRY(check_ptrs({{dy, "dy", none}, {x, "x", none || !dW}, {W, "W", none || !dx}, {z, "z", none || !need_z},
+                      {dx, "dx", true}, {dW, "dW", true}, {db, "db", true}, {workspace, "workspace", none}}, &dev));
+  MOE_TRY(check_device_ptr(device_status, "device_status", dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (none) {  // sums over no tokens
+    cudaError_t err = cudaSuccess;
+    if (dW) err = cudaMemsetAsync(dW, 0, (size_t)d->N * d->K * (d->dw_dtype == MOE_F32 ? 4 : 2), st);
+    if (err == cudaSuccess && db) err = cudaMemsetAsync(db, 0, (size_t)d->N * 4, st);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "linear_bwd zeroing");
+  }
+  moe::LinearBwdArgs a = {dy, x, W, z, dx, dW, db, workspace, device_status, d->lddy, d->ldx, d->ldw, d->ldz, d->s, d->K,
+                          d->N, d->act, d->dy_dtype == MOE_F32, d->dx_dtype == MOE_F32, d->dw_dtype == MOE_F32};
+  return gemm_result(moe::launch_linear_bwd(a, *di, st), "linear_bwd launch", MOE_KERNEL_LINEAR_BWD);
 }
 
 }  // extern "C"

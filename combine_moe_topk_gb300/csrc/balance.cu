@@ -1,0 +1,525 @@
+// balance.cu -- the router's balance loss with its per-expert counts, the z
+// loss from the same pass over the logits, and their gradient.
+//
+// The tokens are cut into B packed sequences by seq_offsets (one sequence of
+// all tokens without them).  With T_b the valid tokens of sequence b, n_bj its
+// routes to expert j, p = softmax(logits), P_bj = (1/T_b) sum_t p_tj, and B'
+// the sequences with T_b > 0:
+//   L = (1/B') sum_b e sum_j n_bj / (k T_b) P_bj,   Z = (1/T) sum_t lse_t^2
+//   dl_tj = dL/B' p_tj (c_bj - sum_i c_bi p_ti) + dZ 2 lse_t p_tj / T,
+//   c_bj = e n_bj / (k T_b^2)    (the counts are not differentiable)
+// Both directions read each logit once and are bound by device memory; the
+// forward pass keeps lse (one fp32 a token), so the backward pass needs no
+// reduction for the softmax, only the row's dot product with c.
+//
+// L lanes share a row (the smallest power of two that covers it with one
+// vector a lane), so a warp works on 32/L rows at once and few experts do
+// not leave lanes idle.  A block owns a run of consecutive tokens; the part of
+// a sequence inside a block (a piece) is summed in registers, then over the
+// block through shared memory, and written to slot (block + sequence), which
+// no other piece has.  join_kernel adds each sequence's pieces in block order:
+// no floating-point atomics, so the results are the same on every run.
+#include <float.h>
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kWarps = kBlock / 32;
+constexpr int kMaxExperts = 256;
+
+// A piece's sums, [slots][...] in the workspace.
+struct Pieces {
+  float* psum;    // [slots][e]
+  int* count;     // [slots][e]
+  float* zsum;    // [slots]
+  int* tokens;    // [slots]
+};
+
+struct BalanceFwd {
+  const float* logits;
+  const int32_t* idx;
+  const uint8_t* valid;
+  const int32_t* offsets;
+  int s, e, k, B, chunk;
+  float* lse;
+  Pieces pc;
+  unsigned* ticket;
+  int32_t* status;
+};
+
+// First sequence that ends after token t (B when none does).
+__device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int t) {
+  int lo = 0, hi = B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(offsets + mid + 1) <= t) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+// Bounds of sequence b inside [lo, hi); empty (x >= y) where they do not meet.
+__device__ __forceinline__ int2 piece_of(const int32_t* offsets, int s, int b, int lo, int hi) {
+  if (!offsets) return make_int2(lo, hi);
+  const int o0 = __ldg(offsets + b), o1 = __ldg(offsets + b + 1);
+  return make_int2(o0 > lo ? o0 : lo, o1 < hi ? o1 : hi);
+}
+
+// One row's columns held by this lane: V consecutive at V * (lane + L * i).
+template <int V>
+__device__ __forceinline__ void load_cols(const float* p, float* f) {
+  if (V == 4) {
+    const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+    Vec<float>::to_float(v, f);
+  } else {
+    f[0] = __ldg(p);
+  }
+}
+
+// The same by plain loads: `add` may be the buffer that is written.
+template <int V>
+__device__ __forceinline__ void load_add(const float* p, float* f) {
+  if (V == 4) Vec<float>::to_float(*reinterpret_cast<const uint4*>(p), f);
+  else f[0] = *p;
+}
+
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+template <int V, int L, int NI>
+__global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
+  constexpr int kRows = 32 / L;  // rows of a warp at once
+  __shared__ int s_count[kMaxExperts];
+  __shared__ float s_p[kWarps][V * L * NI];
+  __shared__ float s_z[kWarps];
+  __shared__ int s_t[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / L, col = lane % L;
+  const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the join, later in the stream
+  // tokens outside every sequence: nothing of theirs counts
+  const int first = p.offsets ? __ldg(p.offsets) : 0, last = p.offsets ? __ldg(p.offsets + p.B) : p.s;
+  for (int t = lo + threadIdx.x; t < hi; t += kBlock)
+    if (t < first || t >= last) p.lse[t] = 0.f;
+  int bad = 0;
+  for (int b = p.offsets ? sequence_of(p.offsets, p.B, lo) : 0; b < p.B; ++b) {
+    if (p.offsets && __ldg(p.offsets + b) >= hi) break;
+    const int2 r = piece_of(p.offsets, p.s, b, lo, hi);
+    if (r.x >= r.y) continue;  // the same for the whole block
+    for (int j = threadIdx.x; j < p.e; j += kBlock) s_count[j] = 0;
+    __syncthreads();
+    float acc[NI][V], zsum = 0.f;
+    int tokens = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[i][v] = 0.f;
+    for (int t0 = r.x + warp * kRows; t0 < r.y; t0 += kWarps * kRows) {
+      const int t = t0 + sub;
+      const bool in = t < r.y;
+      const bool live = in && (!p.valid || __ldg(p.valid + t) != 0);
+      float f[NI][V], top = -CUDART_INF_F;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int c = V * (col + L * i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[i][v] = -CUDART_INF_F;
+        if (live && c < p.e) load_cols<V>(p.logits + (size_t)t * p.e + c, f[i]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          if (!(f[i][v] < CUDART_INF_F)) bad = 1;  // NaN or +inf
+          if (f[i][v] == -FLT_MAX) f[i][v] = -CUDART_INF_F;  // a mask of the type's lowest value
+          top = fmaxf(top, f[i][v]);
+        }
+      }
+      top = lanes_max<L>(top);
+      const float base = top == -CUDART_INF_F ? 0.f : top;  // a row of masked experts: every exp below is 0
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          f[i][v] = expf(f[i][v] - base);
+          sum += f[i][v];
+        }
+      sum = lanes_sum<L>(sum);
+      const bool some = live && top != -CUDART_INF_F;
+      const float inv = some ? 1.f / sum : 0.f;
+      if (some) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[i][v] = fmaf(f[i][v], inv, acc[i][v]);
+      }
+      if (in && col == 0) {
+        const float lse = some ? base + logf(sum) : (live ? -CUDART_INF_F : 0.f);
+        p.lse[t] = lse;
+        if (some) zsum = fmaf(lse, lse, zsum);
+        tokens += live ? 1 : 0;
+      }
+    }
+    for (long long q = (long long)r.x * p.k + threadIdx.x; q < (long long)r.y * p.k; q += kBlock) {
+      if (p.valid && __ldg(p.valid + q / p.k) == 0) continue;
+      const int x = __ldg(p.idx + q);
+      if ((unsigned)x < (unsigned)p.e) atomicAdd(&s_count[x], 1);
+      else if (x != -1) bad |= 2;
+    }
+    // the warp's row groups, then the block's warps, in a fixed order
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int d = L; d < 32; d <<= 1) acc[i][v] += __shfl_xor_sync(0xffffffffu, acc[i][v], d);
+        if (sub == 0) s_p[warp][V * (col + L * i) + v] = acc[i][v];
+      }
+    zsum = lanes_sum<32>(zsum);
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
+    if (lane == 0) {
+      s_z[warp] = zsum;
+      s_t[warp] = tokens;
+    }
+    __syncthreads();
+    const size_t slot = (size_t)blockIdx.x + b;
+    for (int j = threadIdx.x; j < p.e; j += kBlock) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_p[w][j];
+      p.pc.psum[slot * p.e + j] = sum;
+      p.pc.count[slot * p.e + j] = s_count[j];
+    }
+    if (threadIdx.x == 0) {
+      float z = 0.f;
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        z += s_z[w];
+        n += s_t[w];
+      }
+      p.pc.zsum[slot] = z;
+      p.pc.tokens[slot] = n;
+    }
+    __syncthreads();  // the shared sums are rewritten by the next piece
+  }
+  if (bad & 1) raise_status(p.status, MOE_DEV_NONFINITE);
+  if (bad & 2) raise_status(p.status, MOE_DEV_BAD_ROUTE);
+}
+
+struct BalanceJoin {
+  const int32_t* offsets;
+  int s, e, k, B, chunk, cols;  // cols: blocks of 32 columns per sequence
+  Pieces pc;
+  int32_t* counts;
+  float* mean_prob;
+  float* coef;
+  float* part;    // [B * cols] this block's share of e sum_j f_j P_j
+  float* zpart;   // [B]
+  int* tpart;     // [B] valid tokens
+  unsigned* ticket;
+  float* loss;    // [2]
+  float* norm;    // [2] 1 / B', 1 / T
+};
+
+__device__ __forceinline__ float block_sum(float v, float* scratch) {
+  v = lanes_sum<32>(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sum += scratch[w];
+  return sum;
+}
+
+// One block per sequence and 32 columns: the pieces, 8 threads a column; the last block to finish adds the sequences' losses in order.
+__global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin p) {
+  __shared__ float s_f[8][32];
+  __shared__ int s_c[8][32];
+  __shared__ float scratch[kWarps];
+  __shared__ int s_last;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int b = (int)(blockIdx.x / (unsigned)p.cols), block = (int)(blockIdx.x - (unsigned)b * p.cols);
+  const int col = block * 32 + tx;
+  int lo = 0, hi = p.s;
+  if (p.offsets) {
+    lo = max(0, __ldg(p.offsets + b));
+    hi = min(p.s, __ldg(p.offsets + b + 1));
+  }
+  const int c0 = lo / p.chunk, c1 = lo < hi ? (hi - 1) / p.chunk + 1 : c0;  // the blocks that have a piece of it
+  float sum = 0.f;
+  int count = 0, tokens = 0;
+  for (int c = c0 + ty; c < c1; c += 8) {
+    const size_t slot = (size_t)c + b;
+    if (col < p.e) {
+      sum += __ldg(p.pc.psum + slot * p.e + col);
+      count += __ldg(p.pc.count + slot * p.e + col);
+    }
+  }
+  float z = 0.f;
+  for (int c = c0 + threadIdx.x; c < c1; c += kBlock) {
+    tokens += __ldg(p.pc.tokens + (size_t)c + b);
+    z += __ldg(p.pc.zsum + (size_t)c + b);
+  }
+  s_f[ty][tx] = sum;
+  s_c[ty][tx] = count;
+  z = block_sum(z, scratch);
+  // token counts as floats would stop being exact at 2^24: summed as integers
+  __shared__ int s_tok[kWarps];
+  tokens = __reduce_add_sync(0xffffffffu, tokens);
+  if (tx == 0) s_tok[ty] = tokens;
+  __syncthreads();
+  tokens = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) tokens += s_tok[w];
+  if (ty == 0) {
+    sum = 0.f;
+    count = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      sum += s_f[q][tx];
+      count += s_c[q][tx];
+    }
+    const float inv_t = tokens > 0 ? 1.f / (float)tokens : 0.f;
+    const float P = sum * inv_t, f = (float)count * inv_t / (float)p.k;
+    if (col < p.e) {
+      p.counts[(size_t)b * p.e + col] = count;
+      p.mean_prob[(size_t)b * p.e + col] = P;
+      p.coef[(size_t)b * p.e + col] = (float)p.e * f * inv_t;
+    }
+    const float share = lanes_sum<32>(col < p.e ? (float)p.e * f * P : 0.f);
+    if (tx == 0) {
+      p.part[(size_t)b * p.cols + block] = share;
+      if (block == 0) {
+        p.zpart[b] = z;
+        p.tpart[b] = tokens;
+      }
+      __threadfence();
+      s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  float loss = 0.f, zall = 0.f, live = 0.f, total = 0.f;
+  for (int q = threadIdx.x; q < p.B; q += kBlock) {
+    for (int c = 0; c < p.cols; ++c) loss += __ldcg(p.part + (size_t)q * p.cols + c);
+    zall += __ldcg(p.zpart + q);
+    const int n = __ldcg(p.tpart + q);
+    live += n > 0 ? 1.f : 0.f;
+    total += (float)n;
+  }
+  loss = block_sum(loss, scratch);
+  zall = block_sum(zall, scratch);
+  live = block_sum(live, scratch);
+  total = block_sum(total, scratch);
+  if (threadIdx.x == 0) {
+    const float per_seq = 1.f / fmaxf(live, 1.f), per_token = 1.f / fmaxf(total, 1.f);
+    p.loss[0] = loss * per_seq;
+    p.loss[1] = zall * per_token;
+    p.norm[0] = per_seq;
+    p.norm[1] = per_token;
+  }
+}
+
+struct BalanceBwd {
+  const float* logits;
+  const float* lse;
+  const float* coef;
+  const float* norm;
+  const float* dloss;
+  const uint8_t* valid;
+  const int32_t* offsets;
+  const float* add;
+  float* dlogits;
+  int s, e, B, chunk;
+};
+
+template <int V>
+__device__ __forceinline__ void store_cols(float* p, const float* f) {
+  if (V == 4) st_stream(reinterpret_cast<uint4*>(p), Vec<float>::from_float(f));
+  else *p = f[0];
+}
+
+// Rows [lo, hi) get `add` or zeros: tokens outside every sequence.
+template <int V>
+__device__ __forceinline__ void copy_rows(const BalanceBwd& p, int lo, int hi) {
+  for (long long q = (long long)lo * p.e + V * threadIdx.x; q < (long long)hi * p.e; q += V * kBlock) {
+    float f[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) f[v] = 0.f;
+    if (p.add) load_add<V>(p.add + q, f);
+    store_cols<V>(p.dlogits + q, f);
+  }
+}
+
+template <int V, int L, int NI>
+__global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p) {
+  constexpr int kRows = 32 / L;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / L, col = lane % L;
+  const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  const float wl = __ldg(p.dloss) * __ldg(p.norm), wz = 2.f * __ldg(p.dloss + 1) * __ldg(p.norm + 1);
+  if (p.offsets) {
+    copy_rows<V>(p, lo, min(hi, max(lo, __ldg(p.offsets))));
+    copy_rows<V>(p, max(lo, min(hi, __ldg(p.offsets + p.B))), hi);
+  }
+  for (int b = p.offsets ? sequence_of(p.offsets, p.B, lo) : 0; b < p.B; ++b) {
+    if (p.offsets && __ldg(p.offsets + b) >= hi) break;
+    const int2 r = piece_of(p.offsets, p.s, b, lo, hi);
+    if (r.x >= r.y) continue;
+    float c[NI][V];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int j = V * (col + L * i) + v;
+        c[i][v] = j < p.e ? wl * __ldg(p.coef + (size_t)b * p.e + j) : 0.f;
+      }
+    for (int t0 = r.x + warp * kRows; t0 < r.y; t0 += kWarps * kRows) {
+      const int t = t0 + sub;
+      const bool in = t < r.y;
+      const bool live = in && (!p.valid || __ldg(p.valid + t) != 0);
+      const float lse = live ? __ldg(p.lse + t) : 0.f;
+      const bool some = live && lse != -CUDART_INF_F;  // a row of masked experts has no probabilities
+      float f[NI][V], g[NI][V], dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int q = V * (col + L * i);
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[i][v] = -CUDART_INF_F, g[i][v] = 0.f;
+        if (some && q < p.e) load_cols<V>(p.logits + (size_t)t * p.e + q, f[i]);
+        if (p.add && in && q < p.e) load_add<V>(p.add + (size_t)t * p.e + q, g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          f[i][v] = expf(f[i][v] - lse);
+          dot = fmaf(c[i][v], f[i][v], dot);
+        }
+      dot = lanes_sum<L>(dot);
+      const float zt = wz * lse;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int q = V * (col + L * i);
+        if (some) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) g[i][v] = fmaf(f[i][v], c[i][v] - dot + zt, g[i][v]);
+        }
+        if (in && q < p.e) store_cols<V>(p.dlogits + (size_t)t * p.e + q, g[i]);
+      }
+    }
+  }
+}
+
+struct Shape {
+  int V, L, NI;
+};
+
+// Lanes of a row: the fewest (a power of two) that hold it with one vector or
+// element each; past 32 lanes each holds NI of them.
+Shape shape_of(int e) {
+  Shape h;
+  h.V = e % 4 == 0 ? 4 : 1;
+  const int n = e / h.V;
+  h.L = 1;
+  while (h.L < 32 && h.L < n) h.L *= 2;
+  h.NI = 1;
+  while (h.L * h.NI < n) h.NI *= 2;
+  return h;
+}
+
+// Tokens of a block: at least one round of every warp, and not much more
+// than four blocks an SM.
+int chunk_of(int s, const Shape& h) {
+  const int round = kWarps * (32 / h.L);
+  long long c = ((long long)s + kBalanceBlocks - 1) / kBalanceBlocks;
+  c = (c + round - 1) / round * round;
+  return (int)c;
+}
+
+#define MOE_BALANCE_SHAPES(X)                                                                                  \
+  X(4, 1, 1) X(4, 2, 1) X(4, 4, 1) X(4, 8, 1) X(4, 16, 1) X(4, 32, 1) X(4, 32, 2) X(1, 1, 1) X(1, 2, 1)        \
+  X(1, 4, 1) X(1, 8, 1) X(1, 16, 1) X(1, 32, 1) X(1, 32, 2) X(1, 32, 4) X(1, 32, 8)
+
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
+
+struct Plan {
+  size_t psum, count, zsum, tokens, part, zpart, tpart, ticket, total;
+};
+Plan plan_of(int e, int B) {
+  const size_t slots = (size_t)kBalanceBlocks + B, cols = (e + 31) / 32;
+  Plan q;
+  size_t at = 0;
+  q.psum = at, at += up(slots * e * 4);
+  q.count = at, at += up(slots * e * 4);
+  q.zsum = at, at += up(slots * 4);
+  q.tokens = at, at += up(slots * 4);
+  q.part = at, at += up((size_t)B * cols * 4);
+  q.zpart = at, at += up((size_t)B * 4);
+  q.tpart = at, at += up((size_t)B * 4);
+  q.ticket = at, at += up(4);
+  q.total = at;
+  return q;
+}
+
+}  // namespace
+
+size_t balance_workspace(int e, int B) { return plan_of(e, B).total; }
+
+cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* valid, const int32_t* offsets,
+                           int s, int e, int k, int B, float* loss, int32_t* counts, float* mean_prob, float* lse,
+                           float* coef, float* norm, void* workspace, int32_t* status, cudaStream_t st) {
+  char* ws = static_cast<char*>(workspace);
+  const Plan q = plan_of(e, B);
+  const Shape h = shape_of(e);
+  const int chunk = s > 0 ? chunk_of(s, h) : 1;
+  Pieces pc = {reinterpret_cast<float*>(ws + q.psum), reinterpret_cast<int*>(ws + q.count),
+               reinterpret_cast<float*>(ws + q.zsum), reinterpret_cast<int*>(ws + q.tokens)};
+  unsigned* ticket = reinterpret_cast<unsigned*>(ws + q.ticket);
+  BalanceFwd p = {logits, idx, valid, offsets, s, e, k, B, chunk, lse, pc, ticket, status};
+  const unsigned grid = s > 0 ? (unsigned)((s + chunk - 1) / chunk) : 1u;  // no tokens: one block clears the ticket
+#define MOE_RUN(v, l, n) \
+  if (h.V == v && h.L == l && h.NI == n) balance_kernel<v, l, n><<<grid, kBlock, 0, st>>>(p);
+  MOE_BALANCE_SHAPES(MOE_RUN)
+#undef MOE_RUN
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const int cols = (e + 31) / 32;
+  BalanceJoin j = {offsets, s, e, k, B, chunk, cols, pc, counts, mean_prob, coef,
+                   reinterpret_cast<float*>(ws + q.part), reinterpret_cast<float*>(ws + q.zpart),
+                   reinterpret_cast<int*>(ws + q.tpart), ticket, loss, norm};
+  balance_join_kernel<<<(unsigned)cols * (unsigned)B, kBlock, 0, st>>>(j);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_balance_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
+                               const float* dloss, const uint8_t* valid, const int32_t* offsets, const float* add,
+                               int s, int e, int B, float* dlogits, cudaStream_t st) {
+  const Shape h = shape_of(e);
+  const int chunk = chunk_of(s, h);
+  BalanceBwd p = {logits, lse, coef, norm, dloss, valid, offsets, add, dlogits, s, e, B, chunk};
+  const unsigned grid = (unsigned)((s + chunk - 1) / chunk);
+#define MOE_RUN(v, l, n) \
+  if (h.V == v && h.L == l && h.NI == n) balance_bwd_kernel<v, l, n><<<grid, kBlock, 0, st>>>(p);
+  MOE_BALANCE_SHAPES(MOE_RUN)
+#undef MOE_RUN
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -158,4 +158,59 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
                                  int e, int rows, int s, int K, int N, const void* x, const void* W,
                                  void* Y, int32_t* status, const DeviceInfo& di, cudaStream_t st);
 
+// --- layer norm ------------------------------------------------------------
+// dtype / w_dtype: 0 = f32, 1 = bf16.  w, b, mean, rstd may be NULL.  ld*:
+// elements between rows of the inputs (outputs are contiguous).
+cudaError_t launch_layernorm(const void* x, long long ldx, int s, int m, int dtype, const void* w, int w_dtype,
+                             const void* b, int b_dtype, float eps, void* y, float* mean, float* rstd,
+                             cudaStream_t st);
+
+// Partial rows of the weight gradients: at most this many blocks write one.
+inline int layernorm_bwd_parts(int s) { return s < 640 ? s : 640; }
+// part: f32 [2][layernorm_bwd_parts(s)][m] scratch, needed when dw or db is wanted.
+cudaError_t launch_layernorm_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* dres,
+                                 long long lddres, int s, int m, int dtype, const void* w, int w_dtype,
+                                 const float* mean, const float* rstd, void* dx, float* dw, float* db, float* part,
+                                 const DeviceInfo& di, cudaStream_t st);
+
+// --- balance loss ------------------------------------------------------------
+constexpr int kBalanceBlocks = 608;  // most blocks of its kernels (four for each of 152 SMs)
+size_t balance_workspace(int e, int B);
+// offsets == NULL: one sequence of all tokens (B = 1).
+cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* valid, const int32_t* offsets,
+                           int s, int e, int k, int B, float* loss, int32_t* counts, float* mean_prob, float* lse,
+                           float* coef, float* norm, void* workspace, int32_t* status, cudaStream_t st);
+cudaError_t launch_balance_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
+                               const float* dloss, const uint8_t* valid, const int32_t* offsets, const float* add,
+                               int s, int e, int B, float* dlogits, cudaStream_t st);
+
+// out[c] = sum over q < parts of part[q][c] for two arrays (part, then
+// part + stride_parts * m), [m] f32 each, either may be NULL; fixed order.
+cudaError_t launch_sum_parts(const float* part, int parts, int stride_parts, int m, float* out0, float* out1,
+                             cudaStream_t st);
+
+// --- dense products with an epilogue ------------------------------------------
+struct LinearArgs {
+  const void *x, *W, *bias, *res;  // bf16 [s][ldx], bf16 [N][ldw], [N], [s][ldres]
+  void *y, *z;                     // [s][N]; z bf16 [s][N] or NULL
+  void* workspace;
+  int32_t* status;
+  long long ldx, ldw, ldres;
+  int s, K, N, act, out_f32, bias_f32, res_f32;
+};
+size_t linear_workspace(int s, int K, int N);
+cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_t st);
+
+struct LinearBwdArgs {
+  const void *dy, *x, *W, *z;
+  void *dx, *dW;
+  float* db;
+  void* workspace;
+  int32_t* status;
+  long long lddy, ldx, ldw, ldz;
+  int s, K, N, act, dy_f32, dx_f32, dw_f32;
+};
+size_t linear_bwd_workspace(int s, int K, int N);
+cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,808 @@
+// linear.cu -- dense products beside the token path (the router's projection,
+// a shared expert): a product with bias, activation and residual in its
+// epilogue, and its backward pass.
+//
+//   z = x W^T + b;  y = act(z) + residual
+//   dz = dy act'(z);  db = sum_rows dz;  dx = dz W;  dW = dz^T x
+//
+// Three matrix products of one form, D[m,n] = sum_k A[m,k] B[n,k], which
+// differ in which axis of each operand is contiguous in memory:
+//   y   A = x  [m][k]          B = W [n][k]
+//   dx  A = dz [m][k]          B = W [k][n] (contracts over W's rows)
+//   dW  A = dz [k][m]          B = x [k][n] (contracts over the tokens)
+// The tensor cores read either order from shared memory, so no operand is
+// transposed in memory: TMA writes 64-element rows of 128 bytes with the
+// 128-byte swizzle, and the matrix descriptors say which axis those rows run
+// along.  Accumulation is fp32 in TMEM.
+//
+// gemm_kernel: persistent; work units are output tiles (times parts of the
+// contracted axis), each CTA or pair of CTAs taking every gridDim-th:
+//   warp 0 lane 0   TMA producer of a shared-memory ring
+//   warp 1 lane 0   MMA issuer (of the pair's first CTA)
+//   warp 2          TMEM allocation
+//   warps 4..11     epilogue, two warps for each quarter of the TMEM lanes,
+//                   from one of two accumulators while the other fills
+// Every mbarrier wait is bounded on the global timer; a time-out records
+// MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
+#include "common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+namespace {
+
+typedef __nv_bfloat16 bf16;
+
+// ---- activations -------------------------------------------------------------
+
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;  // 1 / sqrt(2 pi)
+constexpr float kTanhA = 0.79788456080286536f;       // sqrt(2 / pi)
+constexpr float kTanhB = 0.044715f;
+
+template <int N>
+__device__ __forceinline__ void activate(float* f, int act) {
+  switch (act) {  // uniform over the grid
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = f[j] > 0.f ? f[j] : (f[j] != f[j] ? f[j] : 0.f);  // NaN stays
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = 0.5f * f[j] * (1.f + erff(f[j] * kSqrtHalf));
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        f[j] = 0.5f * f[j] * (1.f + tanhf(kTanhA * (f[j] + kTanhB * f[j] * f[j] * f[j])));
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = f[j] / (1.f + expf(-f[j]));
+      break;
+    default: break;
+  }
+}
+
+__device__ __forceinline__ float slope(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_GELU: return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    case MOE_ACT_GELU_TANH: {
+      // past 16 the slope is 0 or 1 in fp32; z's square there would overflow beside 1 - t^2 = 0
+      z = fabsf(z) > 16.f ? copysignf(16.f, z) : z;
+      const float t = tanhf(kTanhA * (z + kTanhB * z * z * z));
+      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * kTanhA * (1.f + 3.f * kTanhB * z * z);
+    }
+    case MOE_ACT_SILU: {
+      const float sg = 1.f / (1.f + expf(-z));
+      return sg * (1.f + z * (1.f - sg));
+    }
+    default: return 1.f;
+  }
+}
+
+// ---- epilogue ------------------------------------------------------------------
+
+struct Epi {
+  void* out;
+  bf16* z;          // the value before the activation, or NULL
+  const void* bias;
+  const void* res;
+  float* part;      // split contraction: fp32 partial tiles [splits][M][ldpart], else NULL
+  long long ldres;
+  int ldpart;
+  int act, out_f32, bias_f32, res_f32;
+  int wide;         // N and the residual's stride are multiples of 8: 16-byte accesses
+};
+
+__device__ __forceinline__ float load_any(const void* p, int is_f32, long long i) {
+  return is_f32 ? __ldg(static_cast<const float*>(p) + i) : __bfloat162float(__ldg(static_cast<const bf16*>(p) + i));
+}
+
+// Eight consecutive values of fp32 or bf16 memory, 16-byte aligned.
+__device__ __forceinline__ void load8(const void* p, int is_f32, long long i, float* f) {
+  if (is_f32) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    Vec<float>::to_float(__ldg(q), f);
+    Vec<float>::to_float(__ldg(q + 1), f + 4);
+  } else {
+    Vec<bf16>::to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + i)), f);
+  }
+}
+
+__device__ __forceinline__ void load_bias8(const Epi& e, int col, int N, float* b) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = 0.f;
+  if (!e.bias || col >= N) return;
+  if (e.wide) {
+    load8(e.bias, e.bias_f32, col, b);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < N) b[j] = load_any(e.bias, e.bias_f32, col + j);
+  }
+}
+
+// Bias, activation and residual of row `row`, columns col .. col+7 (those below
+// N); each output is rounded once, from fp32.
+__device__ __forceinline__ void finish8(const Epi& e, long long row, int col, int N, float* f, const float* bias) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] += bias[j];
+  const long long at = row * N + col;
+  if (e.z) {
+    if (e.wide) {
+      *reinterpret_cast<uint4*>(e.z + at) = Vec<bf16>::from_float(f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (col + j < N) e.z[at + j] = __float2bfloat16_rn(f[j]);
+    }
+  }
+  activate<8>(f, e.act);
+  if (e.wide) {
+    if (e.res) {
+      float r[8];
+      load8(e.res, e.res_f32, row * e.ldres + col, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += r[j];
+    }
+    if (e.out_f32) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(e.out) + at);
+      o[0] = Vec<float>::from_float(f);
+      o[1] = Vec<float>::from_float(f + 4);
+    } else {
+      *reinterpret_cast<uint4*>(static_cast<bf16*>(e.out) + at) = Vec<bf16>::from_float(f);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (col + j < N) {
+        const float v = e.res ? f[j] + load_any(e.res, e.res_f32, row * e.ldres + col + j) : f[j];
+        if (e.out_f32) static_cast<float*>(e.out)[at + j] = v;
+        else static_cast<bf16*>(e.out)[at + j] = __float2bfloat16_rn(v);
+      }
+    }
+  }
+}
+
+// ---- the product ----------------------------------------------------------------
+
+struct GemmArgs {
+  int M, N, K;
+  int tiles_m, tiles_n, splits, blocks_per_split, kblocks;  // K blocks of 128
+  Epi epi;
+  int32_t* status;
+  long long timeout_ns;
+};
+
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kEpiBytes = kEpiWarps * 32 * 128;  // a warp: 32 rows x 32 fp32 columns
+constexpr int kKB = 2;                           // 64-wide K blocks per ring stage
+constexpr int kSubA = 128 * 128;                 // 16 KB: 128 rows x 64 of A
+
+// Per variant: CG CTAs (1 or 2) make a tile of 128 CG x BN.
+template <int CG, int BN>
+struct Shape {
+  static constexpr int kRowsB = BN / CG;               // rows of B held by one CTA
+  static constexpr int kSubB = kRowsB * 128;
+  static constexpr int kStage = kKB * (kSubA + kSubB);
+  static constexpr int kStages = (192 * 1024) / kStage;  // 3 at 64 KB a stage, 4 at 48 KB
+  static constexpr int kSmem = kStages * kStage + kEpiBytes + 1024;
+  static constexpr int kTmemCols = 2 * BN;
+};
+
+// Matrix descriptor of a tile in shared memory, 128-byte swizzle, base on 1024
+// bytes.  Rows of 128 bytes along the contracted axis: groups of 8 rows 1024
+// bytes apart.  Rows along the other axis (kMN): 8 steps of the contracted axis
+// are 1024 bytes, the next 64 elements of the other axis 8192 bytes on.
+template <bool kMN>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3ffffu) >> 4);
+  d |= (uint64_t)(kMN ? 8192 >> 4 : 1) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Descriptor step of one MMA (16 of the contracted axis), in 16-byte units.
+template <bool kMN>
+constexpr uint64_t kstep() { return kMN ? 2048 >> 4 : 32 >> 4; }
+
+template <int CG, int BN, bool AT, bool BT>
+__device__ __forceinline__ uint32_t instr_desc() {
+  uint32_t d = 0;
+  d |= 1u << 4;                             // fp32 accumulator
+  d |= 1u << 7;                             // A bf16
+  d |= 1u << 10;                            // B bf16
+  d |= (AT ? 1u : 0u) << 15;                // A's rows run along m
+  d |= (BT ? 1u : 0u) << 16;                // B's rows run along n
+  d |= (uint32_t)(BN >> 3) << 17;
+  d |= (uint32_t)((128 * CG) >> 4) << 24;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_2d(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(sdst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+      : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_tile(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  if constexpr (CG == 2) tma_load_2d_pair(sdst, map, x, y, mbar);
+  else tma_load_2d(sdst, map, x, y, mbar);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t idesc, int accumulate) {
+  if constexpr (CG == 2) {
+    mma_bf16_pair(dt, ad, bd, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 2) {
+    mma_commit_pair(bar);
+  } else {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+  }
+}
+
+struct Unit {
+  int m0, n0, split, kb0, kb1;
+};
+
+// Units run over tiles in bands of 8 rows of tiles (the m index fastest), so
+// that the tiles in flight share operands in L2; splits outermost.
+template <int CG, int BN>
+__device__ __forceinline__ Unit unit_of(int u, const GemmArgs& p) {
+  constexpr int kBand = 8;
+  const int tiles = p.tiles_m * p.tiles_n;
+  Unit t;
+  t.split = u / tiles;
+  const int i = u - t.split * tiles;
+  const int band = i / (kBand * p.tiles_n);
+  const int rows = min(kBand, p.tiles_m - band * kBand);
+  const int r = i - band * kBand * p.tiles_n;
+  const int n = r / rows;
+  t.m0 = (band * kBand + r - n * rows) * 128 * CG;
+  t.n0 = n * BN;
+  t.kb0 = t.split * p.blocks_per_split;
+  t.kb1 = min(p.kblocks, t.kb0 + p.blocks_per_split);
+  return t;
+}
+
+template <int CG, int BN, bool AT, bool BT>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ GemmArgs p) {
+  typedef Shape<CG, BN> S;
+  constexpr int kStages = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+  __shared__ uint32_t tmem_base;
+  __shared__ int s_err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    s_err = 0;
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], CG * kEpiWarps);
+    }
+    mbar_init(&drain, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (warp == 2) {
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                   "r"(S::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
+                   "r"(S::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any remote signal
+  tc_fence_after();
+  const uint32_t tbase = tmem_base;
+
+  const int units = p.tiles_m * p.tiles_n * p.splits;
+  const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+
+  if (warp == 0 && lane == 0) {
+    // ---- TMA producer ------------------------------------------------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = worker; u < units && ok; u += workers) {
+      const Unit t = unit_of<CG, BN>(u, p);
+      const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + S::kRowsB * (int)rank;
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * S::kStage;
+        const uint32_t fb = CG == 2 ? mapa_shared(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
+        if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * S::kStage);
+#pragma unroll
+        for (int q = 0; q < kKB; ++q) {
+          const int k = (kb * kKB + q) * 64;
+          if constexpr (AT) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) load_tile<CG>(sa + q * kSubA + g * 8192, &tmA, m0 + 64 * g, k, fb);
+          } else {
+            load_tile<CG>(sa + q * kSubA, &tmA, k, m0, fb);
+          }
+          uint8_t* sb = sa + kKB * kSubA + q * S::kSubB;
+          if constexpr (BT) {
+#pragma unroll
+            for (int g = 0; g < S::kRowsB / 64; ++g) load_tile<CG>(sb + g * 8192, &tmB, n0 + 64 * g, k, fb);
+          } else {
+            load_tile<CG>(sb, &tmB, k, n0, fb);
+          }
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // every stage's last fill consumed: nothing still arrives at this CTA's
+    // barriers or shared memory when it leaves
+    for (int i = 0; i < kStages && ok; ++i) {
+      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) ok = false;
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (!ok) atomicOr(&s_err, 1);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- MMA issuer ----------------------------------------------------------
+    const uint32_t idesc = instr_desc<CG, BN, AT, BT>();
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, tphase[2] = {0u, 0u};
+    bool ok = true;
+    for (int u = worker; u < units && ok; u += workers) {
+      const Unit t = unit_of<CG, BN>(u, p);
+      if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
+        ok = false;
+        break;
+      }
+      tphase[acc] ^= 1u;
+      tc_fence_after();
+      const uint32_t dt = tbase + (uint32_t)(acc * BN);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        if (!mbar_wait_cluster(&full[stage], phase, deadline)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_addr(smem + stage * S::kStage);
+#pragma unroll
+        for (int q = 0; q < kKB; ++q) {
+          const uint64_t ad = tile_desc<AT>(sa + q * kSubA);
+          const uint64_t bd = tile_desc<BT>(sa + kKB * kSubA + q * S::kSubB);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma<CG>(dt, ad + kk * kstep<AT>(), bd + kk * kstep<BT>(), idesc, (kb > t.kb0) | (q | kk) != 0);
+        }
+        commit<CG>(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      commit<CG>(&tfull[acc]);
+      acc ^= 1;
+    }
+    if (!ok) {
+      // a wait ran out: let the MMAs issued so far finish reading shared
+      // memory before the CTAs leave (one more commit, to this CTA only)
+      if constexpr (CG == 2) mma_commit_pair(&drain, 0x1);
+      else commit<CG>(&drain);
+      mbar_wait_bounded(&drain, 0, globaltimer_ns() + (uint64_t)p.timeout_ns);
+      atomicOr(&s_err, 1);
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue --------------------------------------------------------------
+    const int ew = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* stage_buf = smem + kStages * S::kStage + (warp - 4) * 32 * 128;
+    const uint32_t te[2] = {CG == 2 ? mapa_shared(smem_addr(&tempty[0]), 0) : smem_addr(&tempty[0]),
+                            CG == 2 ? mapa_shared(smem_addr(&tempty[1]), 0) : smem_addr(&tempty[1])};
+    const int sub = lane >> 2, c8 = (lane & 3) * 8;
+    int acc = 0;
+    uint32_t tphase[2] = {0u, 0u};
+    bool ok = true;
+    for (int u = worker; u < units && ok; u += workers) {
+      const Unit t = unit_of<CG, BN>(u, p);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+        ok = false;
+        break;
+      }
+      tphase[acc] ^= 1u;
+      tc_fence_after();
+      const int r0 = t.m0 + 128 * (int)rank + 32 * ew;
+      const uint32_t tcol = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2));
+      float* part = p.epi.part ? p.epi.part + (size_t)t.split * p.M * p.epi.ldpart : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < BN / 64; ++c) {
+        const int col = t.n0 + half * (BN / 2) + 32 * c + c8;
+        float bias[8];
+        if (!part) load_bias8(p.epi, col, p.N, bias);
+        uint32_t v[32];
+        tmem_ld32(tcol + (uint32_t)(32 * c), v);
+        if (c == BN / 64 - 1) {  // the accumulator is in registers: the next product may have it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 1 || rank == 0) mbar_arrive(&tempty[acc]);
+            else mbar_arrive_cluster(te[acc]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<uint4*>(stage_buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+              make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + sub, row = r0 + r;
+          if (row < p.M && col < p.N) {
+            float f[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              Vec<float>::to_float(
+                  *reinterpret_cast<const uint4*>(stage_buf + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4)), f + 4 * h);
+            if (part) {
+              uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * p.epi.ldpart + col);
+              o[0] = Vec<float>::from_float(f);
+              o[1] = Vec<float>::from_float(f + 4);
+            } else {
+              finish8(p.epi, row, col, p.N, f, bias);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      acc ^= 1;
+    }
+    if (!ok) atomicOr(&s_err, 1);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (s_err) {  // let copies in flight land before shared memory goes
+    const uint64_t until = globaltimer_ns() + 200000;
+    while (globaltimer_ns() < until) {
+    }
+  }
+  if constexpr (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  if (warp == 2) {
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(S::kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(S::kTmemCols) : "memory");
+  }
+  if (threadIdx.x == 0 && s_err) raise_status(p.status, MOE_DEV_TIMEOUT);
+}
+
+// Adds the partial products of a split contraction in order and finishes them.
+__global__ void __launch_bounds__(256) gemm_join_kernel(const Epi e, int M, int N, int splits) {
+  const int per_row = e.ldpart / 8;
+  const long long all = (long long)M * per_row;
+  for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
+    const long long row = q / per_row;
+    const int col = (int)(q - row * per_row) * 8;
+    float f[8], bias[8];
+    load_bias8(e, col, N, bias);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.f;
+    const float* src = e.part + row * e.ldpart + col;
+    for (int sp = 0; sp < splits; ++sp) {
+      float g[8];
+      const uint4* s4 = reinterpret_cast<const uint4*>(src + (size_t)sp * M * e.ldpart);
+      Vec<float>::to_float(__ldg(s4), g);
+      Vec<float>::to_float(__ldg(s4 + 1), g + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += g[j];
+    }
+    finish8(e, row, col, N, f, bias);
+  }
+}
+
+// ---- dz and the bias' gradient --------------------------------------------------
+
+struct SlopeArgs {
+  const void* dy;
+  const bf16* z;
+  bf16* dz;        // [s][lddz], or NULL: only the column sums
+  float* part;     // [gridDim.y][N] column sums, or NULL
+  long long lddy, ldz, lddz;
+  int s, N, act, dy_f32, wide;
+};
+
+// dz = dy act'(z) and its column sums: a warp walks rows of 256 columns (8 a
+// lane), a block's eight warps add up through shared memory, each block one
+// partial row.  dz is rounded to bf16 for the tensor cores; the sums are taken
+// before that.
+__global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs p) {
+  __shared__ float acc[8][256 + 8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * 256 + lane * 8;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+  if (col < p.N) {
+#pragma unroll 2
+    for (long long row = (long long)blockIdx.y * 8 + warp; row < p.s; row += (long long)gridDim.y * 8) {
+      float d[8], z[8];
+      if (p.wide) {
+        load8(p.dy, p.dy_f32, row * p.lddy + col, d);
+        if (p.z) load8(p.z, 0, row * p.ldz + col, z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          d[j] = col + j < p.N ? load_any(p.dy, p.dy_f32, row * p.lddy + col + j) : 0.f;
+          z[j] = p.z && col + j < p.N ? load_any(p.z, 0, row * p.ldz + col + j) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (p.z) d[j] *= slope(z[j], p.act);
+        sum[j] += d[j];
+      }
+      if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = Vec<bf16>::from_float(d);
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[warp][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c < p.N) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += acc[w][threadIdx.x];
+    p.part[(size_t)blockIdx.y * p.N + c] = v;
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+// 2-D bf16 [outer][inner], rows ld elements apart, 128-byte swizzle.
+bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estride[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product's plan.  kind: index into the four tile shapes.
+struct Plan {
+  int kind, tiles_m, tiles_n, splits, per_split, kblocks;
+  size_t part_bytes;
+};
+constexpr int kKinds = 4;
+constexpr int kKindCG[kKinds] = {2, 2, 1, 1};
+constexpr int kKindBN[kKinds] = {256, 128, 128, 64};
+constexpr int kPlanSms = 152;  // plans (and workspaces) are made for a whole GB300
+
+Plan plan_gemm(int M, int N, int K) {
+  // relative time of a K block on one tile of each shape
+  const double cost[kKinds] = {1.0, 0.6, 0.6, 0.42};
+  Plan best = {};
+  double best_t = 0;
+  const int kblocks = (K + 127) / 128;
+  for (int k = 0; k < kKinds; ++k) {
+    Plan q;
+    q.kind = k;
+    q.kblocks = kblocks;
+    q.tiles_m = (M + 128 * kKindCG[k] - 1) / (128 * kKindCG[k]);
+    q.tiles_n = (N + kKindBN[k] - 1) / kKindBN[k];
+    const long long tiles = (long long)q.tiles_m * q.tiles_n;
+    const int workers = kPlanSms / kKindCG[k];
+    // a contraction is split only where one wave does not fill the machine,
+    // and keeps at least four K blocks (512 terms) a part
+    int splits = 1;
+    if (tiles * 2 <= workers) splits = (int)(workers / tiles);
+    if (splits > kblocks / 4) splits = kblocks / 4;
+    if (splits < 1) splits = 1;
+    q.per_split = (kblocks + splits - 1) / splits;
+    q.splits = (kblocks + q.per_split - 1) / q.per_split;
+    const long long waves = (tiles * q.splits + workers - 1) / workers;
+    const double t = (double)waves * (q.per_split * cost[k] + 3.0) + (q.splits > 1 ? 12.0 : 0.0);
+    q.part_bytes = q.splits > 1 ? (size_t)q.splits * M * ((N + 7) / 8 * 8) * 4 : 0;
+    if (k == 0 || t < best_t) {
+      best = q;
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+template <int CG, int BN, bool AT, bool BT>
+cudaError_t run_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& p, const DeviceInfo& di,
+                     cudaStream_t st) {
+  typedef Shape<CG, BN> S;
+  static OncePerDevice once;
+  cudaError_t err = once.run([] {
+    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  });
+  if (err != cudaSuccess) return err;
+  long long workers = di.sms / CG;
+  const long long units = (long long)p.tiles_m * p.tiles_n * p.splits;
+  if (units < workers) workers = units;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(workers * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT>, ma, mb, p);
+}
+
+// D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).
+template <bool AT, bool BT>
+cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
+                    void* workspace, int32_t* status, const DeviceInfo& di, cudaStream_t st) {
+  const Plan q = plan_gemm(M, N, K);
+  CUtensorMap ma, mb;
+  const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
+  if (!(AT ? make_map(&ma, A, M, K, lda, 64) : make_map(&ma, A, K, M, lda, 128)) ||
+      !(BT ? make_map(&mb, B, N, K, ldb, box_b) : make_map(&mb, B, K, N, ldb, box_b)))
+    return cudaErrorInvalidValue;
+  epi.part = q.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  epi.ldpart = (N + 7) / 8 * 8;
+  epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
+  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
+  cudaError_t err;
+  switch (q.kind) {
+    case 0: err = run_gemm<2, 256, AT, BT>(ma, mb, p, di, st); break;
+    case 1: err = run_gemm<2, 128, AT, BT>(ma, mb, p, di, st); break;
+    case 2: err = run_gemm<1, 128, AT, BT>(ma, mb, p, di, st); break;
+    default: err = run_gemm<1, 64, AT, BT>(ma, mb, p, di, st); break;
+  }
+  if (err != cudaSuccess || q.splits == 1) return err;
+  const long long work = ((long long)M * (epi.ldpart / 8) + 255) / 256;
+  const unsigned grid = (unsigned)(work < 8LL * di.sms ? work : 8LL * di.sms);
+  gemm_join_kernel<<<grid, 256, 0, st>>>(epi, M, N, q.splits);
+  return cudaGetLastError();
+}
+
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
+
+int slope_rows(int s, int N) {  // blocks along the rows: enough to fill the machine, at least 32 rows each
+  const int cols = (N + 255) / 256;
+  int rows = (4 * kPlanSms + cols - 1) / cols;
+  const int most = (s + 31) / 32;
+  if (rows > most) rows = most;
+  return rows < 1 ? 1 : rows;
+}
+
+struct BwdPlan {
+  size_t dz, part, gemm, total;
+};
+BwdPlan plan_bwd(int s, int K, int N) {
+  BwdPlan q;
+  size_t at = 0;
+  q.dz = at, at += up((size_t)s * ((N + 7) / 8 * 8) * 2);
+  q.part = at, at += up((size_t)slope_rows(s, N) * N * 4);
+  q.gemm = at;
+  const size_t a = plan_gemm(s, K, N).part_bytes, b = plan_gemm(N, K, s).part_bytes;
+  q.total = at + (a > b ? a : b);
+  return q;
+}
+
+}  // namespace
+
+size_t linear_workspace(int s, int K, int N) { return plan_gemm(s, N, K).part_bytes; }
+size_t linear_bwd_workspace(int s, int K, int N) { return plan_bwd(s, K, N).total; }
+
+cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  Epi e = {};
+  e.out = a.y;
+  e.z = static_cast<bf16*>(a.z);
+  e.bias = a.bias;
+  e.res = a.res;
+  e.ldres = a.ldres;
+  e.act = a.act;
+  e.out_f32 = a.out_f32;
+  e.bias_f32 = a.bias_f32;
+  e.res_f32 = a.res_f32;
+  return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.workspace, a.status, di, st);
+}
+
+cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  const BwdPlan q = plan_bwd(a.s, a.K, a.N);
+  char* ws = static_cast<char*>(a.workspace);
+  // without an activation a bf16 dy with whole 16-byte rows is dz itself
+  const bool own_dz = (a.dx || a.dW) && (a.act != MOE_ACT_NONE || a.dy_f32 || a.lddy % 8 != 0);
+  const int lddz = (a.N + 7) / 8 * 8;
+  if (own_dz || a.db) {
+    SlopeArgs p = {};
+    p.dy = a.dy;
+    p.z = a.act != MOE_ACT_NONE ? static_cast<const bf16*>(a.z) : nullptr;
+    p.dz = own_dz ? reinterpret_cast<bf16*>(ws + q.dz) : nullptr;
+    p.part = a.db ? reinterpret_cast<float*>(ws + q.part) : nullptr;
+    p.lddy = a.lddy;
+    p.ldz = a.ldz;
+    p.lddz = lddz;
+    p.s = a.s;
+    p.N = a.N;
+    p.act = a.act;
+    p.dy_f32 = a.dy_f32;
+    p.wide = a.N % 8 == 0 && a.lddy % 8 == 0 && (!p.z || a.ldz % 8 == 0);
+    const int rows = slope_rows(a.s, a.N);
+    slope_kernel<<<dim3((unsigned)((a.N + 255) / 256), (unsigned)rows), 256, 0, st>>>(p);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    if (a.db) {
+      err = launch_sum_parts(p.part, rows, 0, a.N, a.db, nullptr, st);
+      if (err != cudaSuccess) return err;
+    }
+  }
+  const void* dz = own_dz ? ws + q.dz : a.dy;
+  const long long ld = own_dz ? lddz : a.lddy;
+  if (a.dx) {
+    Epi e = {};
+    e.out = a.dx;
+    e.out_f32 = a.dx_f32;
+    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, e, ws + q.gemm, a.status, di, st);
+    if (err != cudaSuccess) return err;
+  }
+  if (a.dW) {
+    Epi e = {};
+    e.out = a.dW;
+    e.out_f32 = a.dw_f32;
+    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, e, ws + q.gemm, a.status, di, st);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace moe

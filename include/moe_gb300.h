@@ -48,6 +48,7 @@
 #ifndef MOE_GB300_H
 #define MOE_GB300_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -93,7 +94,13 @@ enum {
   MOE_KERNEL_EP_UNPACK = 13,
   MOE_KERNEL_EP_DISPATCH = 14,
   MOE_KERNEL_EP_COMBINE = 15,
-  MOE_KERNEL_COUNT = 16
+  MOE_KERNEL_LAYERNORM = 16,
+  MOE_KERNEL_LAYERNORM_BWD = 17,
+  MOE_KERNEL_BALANCE = 18,
+  MOE_KERNEL_BALANCE_BWD = 19,
+  MOE_KERNEL_LINEAR = 20,
+  MOE_KERNEL_LINEAR_BWD = 21,
+  MOE_KERNEL_COUNT = 22
 };
 
 /* Opaque layout handle [P1 "How"; P3 description].  Owned by the library:
@@ -432,6 +439,142 @@ moe_status moe_grouped_gemm(moe_handle h, int rows, int K, int N, const void* X,
  * (the GShard-like capacity layout). */
 moe_status moe_dispatch_grouped_gemm(moe_handle h, int s, int rows, int K, int N, const void* x,
                                      const void* W, void* Y, void* stream);
+
+/* ---- around the token path: norm, balance loss, products -------------------
+ * The pages have no counterpart: these complete a transformer block around
+ * the path above (the norm in front of it, the router's projection and loss,
+ * a shared expert).  They need no handle.  Row strides (ld*) count elements, are at least the row's length,
+ * and apply to inputs; outputs are contiguous.  Any row length is taken; rows
+ * and strides of whole 16 bytes are read with wide loads.  Workspaces are
+ * caller-owned device memory, 16-byte aligned, of the size the _workspace
+ * call names (a host computation), needed only until the call's work on
+ * `stream` is done; their contents need no initialisation. */
+
+/* Layer norm over the last axis:
+ *   mu = mean(x[t]), r = 1 / sqrt(mean((x[t] - mu)^2) + eps),
+ *   y[t] = (x[t] - mu) * r * weight + bias.
+ * x, y [s,m] of dtype (f32 or bf16); weight and bias [m] of weight_dtype, each
+ * nullable (1 and 0); mean and rstd f32 [s], nullable (the backward pass needs
+ * them).  fp32 statistics, the variance around the mean; y rounded once.
+ * eps > 0.  s = 0 is a no-op.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
+ * MOE_ERR_CUDA. */
+moe_status moe_layernorm(int s, int m, moe_dtype dtype, const void* x, int64_t ldx, moe_dtype weight_dtype,
+                         const void* weight, const void* bias, float eps, void* y, float* mean, float* rstd,
+                         void* stream);
+
+/* Bytes of moe_layernorm_bwd's workspace (0 when neither dweight nor dbias is
+ * wanted, or s = 0). */
+size_t moe_layernorm_bwd_workspace(int s, int m);
+
+/* Layer norm backward, from the forward pass's mean and rstd.  With
+ * xh = (x - mean) * rstd and g = dy * weight (weight NULL: 1):
+ *   dx = rstd * (g - mean_m(g) - xh * mean_m(g * xh)) [+ dres],
+ *   dweight = sum_t dy * xh, dbias = sum_t dy   (f32 [m], each nullable).
+ * dres [s,m] (nullable): the gradient that reaches x past the norm, e.g. along
+ * the residual branch, added before dx is rounded.  dx must not overlap an
+ * input.  The sums over tokens are fp32 in a fixed order: the same bits on
+ * every run.  With s = 0, dweight and dbias are zeroed. */
+moe_status moe_layernorm_bwd(int s, int m, moe_dtype dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                             moe_dtype weight_dtype, const void* weight, const float* mean, const float* rstd,
+                             const void* dres, int64_t lddres, void* dx, float* dweight, float* dbias,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of moe_balance_loss's workspace for e experts and B sequences. */
+size_t moe_balance_loss_workspace(int e, int num_seqs);
+
+/* The router's balance loss, the z loss and the per-expert counts.
+ * logits f32 [s,e], topk_idx i32 [s,k] (-1: an absent route, not counted);
+ * valid u8 [s] (nullable): tokens with 0 (padding) take no part, whatever their
+ * logits hold; seq_offsets i32 [num_seqs+1] (nullable, then num_seqs = 1 and
+ * the sequence is all s tokens): non-decreasing starts of packed sequences and
+ * the end of the last, in [0, s]; tokens outside take no part, sequences may
+ * be empty.  With T_b the valid tokens of sequence b, n_bj its routes to
+ * expert j, p = softmax(logits), P_bj = (1/T_b) sum_t p_tj and B' the
+ * sequences with T_b > 0:
+ *   loss[0] = (1/B') sum_b e * sum_j n_bj / (k T_b) * P_bj,
+ *   loss[1] = (1/T) sum_t lse_t^2,  lse_t = log sum_j exp(logits_tj),
+ * both 0 when no token is valid.  Also written: counts i32 [num_seqs,e] (n),
+ * mean_prob f32 [num_seqs,e] (P), lse f32 [s] (0 for tokens that take no
+ * part), and for the backward pass coef f32 [num_seqs,e] = e n_bj / (k T_b^2)
+ * and norm f32 [2] = (1/B', 1/T).  Logits of -inf or of fp32's
+ * lowest value (-FLT_MAX) are experts masked out (p = 0); a row that a mask
+ * leaves nothing of has no probabilities, is left out of the z loss, and its
+ * lse is -inf.  device_status (nullable): MOE_DEV_NONFINITE for a NaN or +inf logit
+ * of a valid token (it reaches the losses), MOE_DEV_BAD_ROUTE for an expert
+ * id outside [-1, e) (not counted).  fp32 sums in a fixed order. */
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* valid,
+                            const int32_t* seq_offsets, int s, int e, int k, int num_seqs, float* loss,
+                            int32_t* counts, float* mean_prob, float* lse, float* coef, float* norm, void* workspace,
+                            size_t workspace_bytes, int32_t* device_status, void* stream);
+
+/* Gradient of the two losses in the logits, the counts held fixed.  dloss f32
+ * [2] (device memory): the gradients that reach loss[0] and loss[1];
+ *   dlogits_tj = add_tj + dloss[0] norm[0] p_tj (coef_bj - sum_i coef_bi p_ti)
+ *                       + dloss[1] norm[1] 2 lse_t p_tj,
+ * p_tj = exp(logits_tj - lse_t); tokens that take no part get add alone.  add
+ * f32 [s,e] (nullable: 0) is typically the gradient from moe_topk_gate_bwd and
+ * may be dlogits itself. */
+moe_status moe_balance_loss_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
+                                const float* dloss, const uint8_t* valid, const int32_t* seq_offsets,
+                                const float* add, int s, int e, int num_seqs, float* dlogits, void* stream);
+
+/* Activations of moe_linear. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_GELU = 2,      /* z Phi(z), by the error function                          */
+  MOE_ACT_GELU_TANH = 3, /* its tanh form: z/2 (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3))) */
+  MOE_ACT_SILU = 4       /* z / (1 + exp(-z))                                        */
+};
+
+typedef struct {
+  int32_t s, K, N;        /* x [s,K], W [N,K], y [s,N]                               */
+  int32_t act;            /* MOE_ACT_*                                              */
+  int32_t out_dtype;      /* of y: MOE_F32 or MOE_BF16                              */
+  int32_t bias_dtype;     /* of bias                                                */
+  int32_t residual_dtype; /* of residual                                            */
+  int64_t ldx, ldw, ldres; /* elements between rows; ldx and ldw multiples of 8     */
+} moe_linear_desc;
+
+/* Bytes of moe_linear's workspace (partial products where the contracted axis is split over SMs);
+ * 0 is common, and then the workspace may be NULL. */
+size_t moe_linear_workspace(int s, int K, int N);
+
+/* A dense product with bias, activation and residual in its epilogue:
+ *   z = x W^T + bias,  y = act(z) + residual.
+ * x bf16 [s,K], W bf16 [N,K] (K a multiple of 8, so that rows are whole 16
+ * bytes; any s >= 0 and N >= 1); bias [N] and residual [s,N] nullable, fp32 or
+ * bf16; y [s,N] fp32 or bf16.  z bf16 [s,N] (nullable): what the backward pass
+ * of an activation needs, rounded to bf16 to halve what is kept.  Products of
+ * bf16 are exact, sums fp32 on the tensor cores (tcgen05), the epilogue fp32;
+ * y and z are each rounded once.  device_status (nullable): MOE_DEV_TIMEOUT if
+ * a bounded device wait ran out.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
+ * MOE_ERR_CUDA. */
+moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* W, const void* bias,
+                      const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
+                      int32_t* device_status, void* stream);
+
+typedef struct {
+  int32_t s, K, N;
+  int32_t act;
+  int32_t dy_dtype;       /* MOE_F32 or MOE_BF16                                    */
+  int32_t dx_dtype;       /* of dx                                                  */
+  int32_t dw_dtype;       /* of dW                                                  */
+  int64_t lddy, ldx, ldw, ldz;
+} moe_linear_bwd_desc;
+
+size_t moe_linear_bwd_workspace(int s, int K, int N);
+
+/* Backward of moe_linear (the residual's gradient is dy itself):
+ *   dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum_t dz.
+ * dy [s,N] fp32 or bf16, z bf16 [s,N] (may be NULL without an activation);
+ * dx [s,K] and dW [N,K] fp32 or bf16, db f32 [N], each nullable.  dz is
+ * rounded to bf16 for the two products (2^-9 of each term, averaged over the
+ * sums) unless it is a bf16 dy itself; db sums it in fp32 before that.  All sums run in a
+ * fixed order: the same bits on every run.  With s = 0, dW and db are zeroed. */
+moe_status moe_linear_bwd(const moe_linear_bwd_desc* desc, const void* dy, const void* x, const void* W,
+                          const void* z, void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
+                          int32_t* device_status, void* stream);
 
 /* Fill *info with the handle's sizes and device pointers (valid until the
  * handle is destroyed). */

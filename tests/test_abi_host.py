@@ -227,3 +227,36 @@ def test_recorder_keys_on_layout_options():
     # same call position, but token priority this time: rebuilt, not replayed
     assert rec.layout(FakeIdx((8, 2), "c"), 4, pad_multiple=1) == "c"
     assert rec.replayed == 1 and rec.fallbacks == 1
+
+
+def test_block_calls_reject_bad_arguments_without_a_gpu(lib):
+    fake = P(0x10000)
+    # layer norm: sizes, dtypes, strides, eps
+    ln = lambda s=4, m=8, dt=0, ldx=8, wd=0, eps=1e-5, x=fake: rc_name(
+        lib.moe_layernorm(s, m, dt, x, ldx, wd, fake, fake, eps, fake, None, None, None))
+    assert ln(s=-1) == ln(m=0) == ln(ldx=7) == ln(eps=0.0) == ln(eps=float("nan")) == ln(x=None) == "MOE_ERR_INVALID_ARG"
+    assert ln(dt=2) == ln(wd=2) == ln(dt=-1) == "MOE_ERR_DTYPE"
+    assert ln(s=0) == "MOE_OK"
+    assert lib.moe_layernorm_bwd_workspace(0, 64) == 0
+    assert lib.moe_layernorm_bwd_workspace(5, 64) == 5 * 64 * 8
+    bwd = lambda ws: rc_name(lib.moe_layernorm_bwd(4, 8, 0, fake, 8, fake, 8, 0, fake, fake, fake, None, 0, fake, fake, fake,
+                                                   fake, ws, None))
+    assert bwd(4 * 8 * 8 - 1) == "MOE_ERR_INVALID_ARG" and "workspace" in lib.moe_last_error().decode()
+    # balance loss
+    bl = lambda s=4, e=8, k=2, n=1, off=None, ws=1 << 30: rc_name(
+        lib.moe_balance_loss(fake, fake, None, off, s, e, k, n, fake, fake, fake, fake, fake, fake, fake, ws, None, None))
+    assert bl(s=-1) == bl(e=0) == bl(e=257) == bl(k=0) == bl(k=17) == bl(n=0) == bl(n=2) == bl(ws=8) == "MOE_ERR_INVALID_ARG"
+    assert lib.moe_balance_loss_workspace(300, 1) == 0 and lib.moe_balance_loss_workspace(8, 4) > 0
+    # products
+    d = B.LinearDesc(4, 64, 8, 0, 1, 1, 1, 64, 64, 8)
+    call = lambda dd: rc_name(lib.moe_linear(ctypes.byref(dd), fake, fake, None, None, fake, None, None, 0, None, None))
+    for field, value in (("s", -1), ("K", 4), ("K", 12), ("N", 0), ("act", 5), ("act", -1), ("ldx", 32), ("ldx", 68), ("ldw", 60)):
+        bad = B.LinearDesc(*[value if f == field else getattr(d, f) for f, _ in B.LinearDesc._fields_])
+        assert call(bad) == "MOE_ERR_INVALID_ARG", field
+    assert call(B.LinearDesc(4, 64, 8, 0, 2, 1, 1, 64, 64, 8)) == "MOE_ERR_DTYPE"
+    assert call(B.LinearDesc(0, 64, 8, 0, 1, 1, 1, 64, 64, 8)) == "MOE_OK"
+    assert rc_name(lib.moe_linear(None, fake, fake, None, None, fake, None, None, 0, None, None)) == "MOE_ERR_INVALID_ARG"
+    b = B.LinearBwdDesc(4, 64, 8, 0, 2, 1, 1, 8, 64, 64, 8)
+    assert rc_name(lib.moe_linear_bwd(ctypes.byref(b), fake, fake, fake, None, fake, fake, fake, fake, 1 << 30, None,
+                                      None)) == "MOE_ERR_DTYPE"
+    assert lib.moe_linear_workspace(0, 64, 8) == 0 and lib.moe_linear_bwd_workspace(16, 64, 8) > 0
