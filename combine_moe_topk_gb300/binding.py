@@ -167,6 +167,8 @@ def _rows_ptr(t: torch.Tensor | None):
     """Pointer and row stride (elements) of a 2-D tensor whose rows are contiguous; the rows may be apart."""
     if t is None:
         return None, 0
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[1]
     s, m = t.shape
     if m > 1 and t.stride(1) != 1:
         raise ValueError("the rows of tensors passed to the MoE library must be contiguous")
@@ -174,7 +176,21 @@ def _rows_ptr(t: torch.Tensor | None):
     ld = t.stride(0) if s > 1 else m
     if ld < m:
         raise ValueError("rows that overlap (a broadcast or a negative stride) are not supported")
-    return (t.data_ptr() if t.numel() else None), ld
+    return t.data_ptr(), ld
+
+
+def _addr(t: torch.Tensor | None):
+    """Address of a contiguous tensor, as an int (a cheaper _ptr)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the MoE library must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(t: torch.Tensor):
+    """The current stream of a CUDA tensor's device; a host tensor goes to the library, which rejects it."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
 
 
 def _stream(device: torch.device):
@@ -594,19 +610,11 @@ def moe_dispatch_grouped_gemm(h: Handle, x: torch.Tensor, W: torch.Tensor,
 
 
 # ------------------------------------- layer norm, balance loss, products --
+# Small calls are bound by the host, so these marshal with as few Python
+# operations as they can; which device a pointer lives on is checked by the
+# library alone.
 
-def _same_device(where: str, dev: torch.device, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise MoEError(1, where, "the tensors live on different devices")
-
-
-def _norm_weights(where: str, m: int, weight, bias):
-    wt = weight if weight is not None else bias
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None and (tuple(t.shape) != (m,) or t.dtype != wt.dtype):
-            raise MoEError(1, where, f"{name} must be [m], weight and bias of one dtype")
-    return MOE_F32 if wt is None else _dtype(wt)
+_DTYPE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 
 
 def moe_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -614,19 +622,24 @@ def moe_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: tor
     """x [s,m] f32 or bf16 (rows may be strided), weight and bias [m] f32 or
     bf16 -> (y [s,m], mean f32 [s], rstd f32 [s]); stats=False returns y alone."""
     s, m = _rows2(x, "x")
-    dev = x.device
-    wd = _norm_weights("moe_layernorm", m, weight, bias)
-    _same_device("moe_layernorm", dev, weight, bias, y)
+    dev, dt = x.device, x.dtype
+    wt = weight if weight is not None else bias
+    for t in (weight, bias):
+        if t is not None and (t.shape != (m,) or t.dtype != wt.dtype):
+            raise MoEError(1, "moe_layernorm", "weight and bias must be [m], of one dtype")
     if y is None:
-        y = torch.empty(s, m, dtype=x.dtype, device=dev)
-    if tuple(y.shape) != (s, m) or y.dtype != x.dtype:
+        y = torch.empty(s, m, dtype=dt, device=dev)
+    elif y.shape != (s, m) or y.dtype != dt:
         raise MoEError(1, "moe_layernorm", "output shape")
-    mean = torch.empty(s, dtype=torch.float32, device=dev) if stats else None
-    rstd = torch.empty(s, dtype=torch.float32, device=dev) if stats else None
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(s, dtype=torch.float32, device=dev)
+        rstd = torch.empty(s, dtype=torch.float32, device=dev)
     px, ldx = _rows_ptr(x)
-    rc = lib().moe_layernorm(s, m, _dtype(x), px, ldx, wd, _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
-                             _ptr(rstd), _stream(dev))
-    _check(rc, "moe_layernorm")
+    rc = lib().moe_layernorm(s, m, _DTYPE.get(dt, -1), px, ldx, 0 if wt is None else _DTYPE.get(wt.dtype, -1),
+                             _addr(weight), _addr(bias), eps, _addr(y), _addr(mean), _addr(rstd), _raw_stream(x))
+    if rc:
+        _check(rc, "moe_layernorm")
     return (y, mean, rstd) if stats else y
 
 
@@ -637,27 +650,31 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | 
     dweight f32 [m] or None, dbias f32 [m] or None).  dres [s,m]: a gradient
     that reaches x past the norm (the residual branch), added to dx."""
     s, m = _rows2(x, "x")
-    dev = x.device
-    for t, name in ((dy, "dy"), (dres, "dres"), (dx, "dx")):
-        if t is not None and (tuple(t.shape) != (s, m) or t.dtype != x.dtype):
-            raise MoEError(1, "moe_layernorm_bwd", f"{name} must have x's shape and dtype")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if tuple(t.shape) != (s,) or t.dtype != torch.float32:
-            raise MoEError(1, "moe_layernorm_bwd", f"{name} must be float32 [s]")
-    wd = _norm_weights("moe_layernorm_bwd", m, weight, None)
-    _same_device("moe_layernorm_bwd", dev, dy, weight, mean, rstd, dres, dx)
+    dev, dt = x.device, x.dtype
+    for t in (dy, dres, dx):
+        if t is not None and (t.shape != (s, m) or t.dtype != dt):
+            raise MoEError(1, "moe_layernorm_bwd", "dy, dres and dx must have x's shape and dtype")
+    if mean.shape != (s,) or rstd.shape != (s,) or mean.dtype != torch.float32 or rstd.dtype != torch.float32:
+        raise MoEError(1, "moe_layernorm_bwd", "mean and rstd must be float32 [s]")
+    if weight is not None and weight.shape != (m,):
+        raise MoEError(1, "moe_layernorm_bwd", "weight must be [m]")
     if dx is None:
-        dx = torch.empty(s, m, dtype=x.dtype, device=dev)
+        dx = torch.empty(s, m, dtype=dt, device=dev)
     dw = torch.empty(m, dtype=torch.float32, device=dev) if need_dweight else None
     db = torch.empty(m, dtype=torch.float32, device=dev) if need_dbias else None
-    nbytes = lib().moe_layernorm_bwd_workspace(s, m) if need_dweight or need_dbias else 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    L, nbytes, ws = lib(), 0, None
+    if need_dweight or need_dbias:
+        nbytes = L.moe_layernorm_bwd_workspace(s, m)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)
     pres, ldres = _rows_ptr(dres)
-    rc = lib().moe_layernorm_bwd(s, m, _dtype(x), pdy, lddy, px, ldx, wd, _ptr(weight), _ptr(mean), _ptr(rstd), pres,
-                                 ldres, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nbytes, _stream(dev))
-    _check(rc, "moe_layernorm_bwd")
+    rc = L.moe_layernorm_bwd(s, m, _DTYPE.get(dt, -1), pdy, lddy, px, ldx,
+                             0 if weight is None else _DTYPE.get(weight.dtype, -1), _addr(weight), _addr(mean),
+                             _addr(rstd), pres, ldres, _addr(dx), _addr(dw), _addr(db), _addr(ws), nbytes,
+                             _raw_stream(x))
+    if rc:
+        _check(rc, "moe_layernorm_bwd")
     return dx, dw, db
 
 
@@ -671,10 +688,10 @@ class BalanceLoss(NamedTuple):
     norm: torch.Tensor       # f32 [2]
 
 
-def _check_balance(where: str, s: int, e: int, logits, valid, seq_offsets) -> int:
+def _check_balance(where: str, s: int, logits, valid, seq_offsets) -> int:
     if logits.dtype != torch.float32:
         raise MoEError(3, where, "logits must be float32")
-    if valid is not None and (tuple(valid.shape) != (s,) or valid.dtype not in (torch.uint8, torch.bool)):
+    if valid is not None and (valid.shape != (s,) or valid.dtype not in (torch.uint8, torch.bool)):
         raise MoEError(1, where, "valid must be uint8 or bool [s]")
     if seq_offsets is None:
         return 1
@@ -690,19 +707,23 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.
     s, e = _rows2(logits, "logits")
     if topk_idx.dim() != 2 or topk_idx.dtype != torch.int32 or topk_idx.shape[0] != s:
         raise MoEError(1, "moe_balance_loss", "topk_idx must be int32 [s, k]")
-    n = _check_balance("moe_balance_loss", s, e, logits, valid, seq_offsets)
-    dev = logits.device
-    _same_device("moe_balance_loss", dev, topk_idx, valid, seq_offsets, device_status)
-    f32 = dict(dtype=torch.float32, device=dev)
-    r = BalanceLoss(torch.empty(2, **f32), torch.empty(n, e, dtype=torch.int32, device=dev), torch.empty(n, e, **f32),
-                    torch.empty(s, **f32), torch.empty(n, e, **f32), torch.empty(2, **f32))
-    nbytes = lib().moe_balance_loss_workspace(e, n)
+    n = _check_balance("moe_balance_loss", s, logits, valid, seq_offsets)
+    dev, f32, L = logits.device, torch.float32, lib()
+    loss = torch.empty(2, dtype=f32, device=dev)
+    counts = torch.empty(n, e, dtype=torch.int32, device=dev)
+    mean_prob = torch.empty(n, e, dtype=f32, device=dev)
+    lse = torch.empty(s, dtype=f32, device=dev)
+    coef = torch.empty(n, e, dtype=f32, device=dev)
+    norm = torch.empty(2, dtype=f32, device=dev)
+    nbytes = L.moe_balance_loss_workspace(e, n)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    rc = lib().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(valid), _ptr(seq_offsets), s, e,
-                                topk_idx.shape[1], n, _ptr(r.loss), _ptr(r.counts), _ptr(r.mean_prob), _ptr(r.lse),
-                                _ptr(r.coef), _ptr(r.norm), _ptr(ws), nbytes, _ptr(device_status), _stream(dev))
-    _check(rc, "moe_balance_loss")
-    return r
+    rc = L.moe_balance_loss(_addr(logits), _addr(topk_idx), _addr(valid), _addr(seq_offsets), s, e, topk_idx.shape[1],
+                            n, loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(), lse.data_ptr(),
+                            coef.data_ptr(), norm.data_ptr(), ws.data_ptr(), nbytes, _addr(device_status),
+                            _raw_stream(logits))
+    if rc:
+        _check(rc, "moe_balance_loss")
+    return BalanceLoss(loss, counts, mean_prob, lse, coef, norm)
 
 
 def moe_balance_loss_bwd(logits: torch.Tensor, lse: torch.Tensor, coef: torch.Tensor, norm: torch.Tensor,
@@ -712,34 +733,30 @@ def moe_balance_loss_bwd(logits: torch.Tensor, lse: torch.Tensor, coef: torch.Te
     """dloss f32 [2] (the gradients reaching the two losses) -> dlogits f32
     [s,e], plus add [s,e] (may be dlogits itself) where given."""
     s, e = _rows2(logits, "logits")
-    n = _check_balance("moe_balance_loss_bwd", s, e, logits, valid, seq_offsets)
-    dev = logits.device
+    n = _check_balance("moe_balance_loss_bwd", s, logits, valid, seq_offsets)
+    f32 = torch.float32
     for t, name, shape in ((lse, "lse", (s,)), (coef, "coef", (n, e)), (norm, "norm", (2,)), (dloss, "dloss", (2,)),
                            (add, "add", (s, e)), (dlogits, "dlogits", (s, e))):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.float32):
+        if t is not None and (t.shape != shape or t.dtype != f32):
             raise MoEError(1, "moe_balance_loss_bwd", f"{name} must be float32 {list(shape)}")
-    _same_device("moe_balance_loss_bwd", dev, lse, coef, norm, dloss, valid, seq_offsets, add, dlogits)
     if dlogits is None:
-        dlogits = torch.empty(s, e, dtype=torch.float32, device=dev)
-    rc = lib().moe_balance_loss_bwd(_ptr(logits), _ptr(lse), _ptr(coef), _ptr(norm), _ptr(dloss), _ptr(valid),
-                                    _ptr(seq_offsets), _ptr(add), s, e, n, _ptr(dlogits), _stream(dev))
-    _check(rc, "moe_balance_loss_bwd")
+        dlogits = torch.empty(s, e, dtype=f32, device=logits.device)
+    rc = lib().moe_balance_loss_bwd(_addr(logits), _addr(lse), _addr(coef), _addr(norm), _addr(dloss), _addr(valid),
+                                    _addr(seq_offsets), _addr(add), s, e, n, _addr(dlogits), _raw_stream(logits))
+    if rc:
+        _check(rc, "moe_balance_loss_bwd")
     return dlogits
 
 
-def _act(where: str, act: str) -> int:
-    if act not in ACT:
-        raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
-    return ACT[act]
-
-
-def _check_linear(where: str, x: torch.Tensor, W: torch.Tensor):
+def _check_linear(where: str, x: torch.Tensor, W: torch.Tensor, act: str):
     s, K = _rows2(x, "x")
     N, KW = _rows2(W, "W")
     if KW != K:
         raise MoEError(1, where, "W must be [N, K]")
     if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
         raise MoEError(3, where, "x and W must be bf16")
+    if act not in ACT:
+        raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
     return s, K, N
 
 
@@ -751,30 +768,29 @@ def moe_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     residual [s,N] f32 or bf16, y f32 or bf16 (default bf16); act: none, relu,
     gelu, gelu_tanh, silu.  save_z: return (y, z), z bf16 [s,N] the value
     before the activation, for moe_linear_bwd."""
-    s, K, N = _check_linear("moe_linear", x, W)
+    s, K, N = _check_linear("moe_linear", x, W, act)
     dev = x.device
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if y is None else y.dtype
-    if bias is not None and tuple(bias.shape) != (N,):
+    if bias is not None and bias.shape != (N,):
         raise MoEError(1, "moe_linear", "bias must be [N]")
-    if residual is not None and tuple(residual.shape) != (s, N):
+    if residual is not None and residual.shape != (s, N):
         raise MoEError(1, "moe_linear", "residual must be [s, N]")
-    _same_device("moe_linear", dev, W, bias, residual, y, device_status)
     if y is None:
-        y = torch.empty(s, N, dtype=out_dtype, device=dev)
-    if tuple(y.shape) != (s, N) or y.dtype != out_dtype:
+        y = torch.empty(s, N, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+    elif y.shape != (s, N) or (out_dtype is not None and y.dtype != out_dtype):
         raise MoEError(1, "moe_linear", "output shape or dtype")
     z = torch.empty(s, N, dtype=torch.bfloat16, device=dev) if save_z else None
-    nbytes = lib().moe_linear_workspace(s, K, N)
+    L = lib()
+    nbytes = L.moe_linear_workspace(s, K, N)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
     pres, ldres = _rows_ptr(residual)
-    d = LinearDesc(s, K, N, _act("moe_linear", act), _dtype(y), 0 if bias is None else _dtype(bias),
-                   0 if residual is None else _dtype(residual), ldx, ldw, ldres)
-    rc = lib().moe_linear(ctypes.byref(d), px, pw, _ptr(bias), pres, _ptr(y), _ptr(z), _ptr(ws), nbytes,
-                          _ptr(device_status), _stream(dev))
-    _check(rc, "moe_linear")
+    d = LinearDesc(s, K, N, ACT[act], _DTYPE.get(y.dtype, -1), 0 if bias is None else _DTYPE.get(bias.dtype, -1),
+                   0 if residual is None else _DTYPE.get(residual.dtype, -1), ldx, ldw, ldres)
+    rc = L.moe_linear(d, px, pw, _addr(bias), pres, _addr(y), _addr(z), _addr(ws), nbytes, _addr(device_status),
+                      _raw_stream(x))
+    if rc:
+        _check(rc, "moe_linear")
     return (y, z) if save_z else y
 
 
@@ -785,27 +801,28 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     """(dy [s,N] f32 or bf16, x bf16 [s,K], W bf16 [N,K], z bf16 [s,N] with an
     activation) -> (dx [s,K], dW [N,K], db f32 [N]), None for those not
     needed.  The residual's gradient is dy itself."""
-    s, K, N = _check_linear("moe_linear_bwd", x, W)
+    s, K, N = _check_linear("moe_linear_bwd", x, W, act)
     dev = x.device
-    if tuple(dy.shape) != (s, N):
+    if dy.shape != (s, N):
         raise MoEError(1, "moe_linear_bwd", "dy must be [s, N]")
-    if act != "none" and (z is None or tuple(z.shape) != (s, N) or z.dtype != torch.bfloat16):
-        raise MoEError(1, "moe_linear_bwd", "z must be bf16 [s, N] with an activation")
     if act == "none":
         z = None
-    _same_device("moe_linear_bwd", dev, dy, W, z, device_status)
+    elif z is None or z.shape != (s, N) or z.dtype != torch.bfloat16:
+        raise MoEError(1, "moe_linear_bwd", "z must be bf16 [s, N] with an activation")
     dx = torch.empty(s, K, dtype=dx_dtype, device=dev) if need_dx else None
     dW = torch.empty(N, K, dtype=dw_dtype, device=dev) if need_dw else None
     db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
-    nbytes = lib().moe_linear_bwd_workspace(s, K, N)
+    L = lib()
+    nbytes = L.moe_linear_bwd_workspace(s, K, N)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
     pz, ldz = _rows_ptr(z)
-    d = LinearBwdDesc(s, K, N, _act("moe_linear_bwd", act), _dtype(dy), 0 if dx is None else _dtype(dx),
-                      0 if dW is None else _dtype(dW), lddy, ldx, ldw, ldz)
-    rc = lib().moe_linear_bwd(ctypes.byref(d), pdy, px, pw, pz, _ptr(dx), _ptr(dW), _ptr(db), _ptr(ws), nbytes,
-                              _ptr(device_status), _stream(dev))
-    _check(rc, "moe_linear_bwd")
+    d = LinearBwdDesc(s, K, N, ACT[act], _DTYPE.get(dy.dtype, -1), _DTYPE.get(dx_dtype, -1), _DTYPE.get(dw_dtype, -1),
+                      lddy, ldx, ldw, ldz)
+    rc = L.moe_linear_bwd(d, pdy, px, pw, pz, _addr(dx), _addr(dW), _addr(db), _addr(ws), nbytes, _addr(device_status),
+                          _raw_stream(x))
+    if rc:
+        _check(rc, "moe_linear_bwd")
     return dx, dW, db

@@ -52,14 +52,14 @@ __device__ __forceinline__ void activate(float* f, int act) {
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] = 0.5f * f[j] * (1.f + erff(f[j] * kSqrtHalf));
       break;
-    case MOE_ACT_GELU_TANH:
+    case MOE_ACT_GELU_TANH:  // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u))
 #pragma unroll
       for (int j = 0; j < N; ++j)
-        f[j] = 0.5f * f[j] * (1.f + tanhf(kTanhA * (f[j] + kTanhB * f[j] * f[j] * f[j])));
+        f[j] = __fdividef(f[j], 1.f + __expf(-2.f * kTanhA * (f[j] + kTanhB * f[j] * f[j] * f[j])));
       break;
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = f[j] / (1.f + expf(-f[j]));
+      for (int j = 0; j < N; ++j) f[j] = __fdividef(f[j], 1.f + __expf(-f[j]));
       break;
     default: break;
   }
@@ -94,7 +94,8 @@ struct Epi {
   long long ldres;
   int ldpart;
   int act, out_f32, bias_f32, res_f32;
-  int wide;         // N and the residual's stride are multiples of 8: 16-byte accesses
+  int wide;         // N and the residual's stride are multiples of 8: 16-byte accesses,
+                    // else each lane takes one column and walks down the rows
 };
 
 __device__ __forceinline__ float load_any(const void* p, int is_f32, long long i) {
@@ -115,56 +116,41 @@ __device__ __forceinline__ void load8(const void* p, int is_f32, long long i, fl
 __device__ __forceinline__ void load_bias8(const Epi& e, int col, int N, float* b) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) b[j] = 0.f;
-  if (!e.bias || col >= N) return;
-  if (e.wide) {
-    load8(e.bias, e.bias_f32, col, b);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (col + j < N) b[j] = load_any(e.bias, e.bias_f32, col + j);
-  }
+  if (e.bias && col < N) load8(e.bias, e.bias_f32, col, b);
 }
 
-// Bias, activation and residual of row `row`, columns col .. col+7 (those below
-// N); each output is rounded once, from fp32.
+// Bias, activation and residual of columns col .. col+7 of row `row`, by
+// 16-byte accesses (e.wide); each output is rounded once, from fp32.
 __device__ __forceinline__ void finish8(const Epi& e, long long row, int col, int N, float* f, const float* bias) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] += bias[j];
   const long long at = row * N + col;
-  if (e.z) {
-    if (e.wide) {
-      *reinterpret_cast<uint4*>(e.z + at) = Vec<bf16>::from_float(f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (col + j < N) e.z[at + j] = __float2bfloat16_rn(f[j]);
-    }
-  }
+  if (e.z) *reinterpret_cast<uint4*>(e.z + at) = Vec<bf16>::from_float(f);
   activate<8>(f, e.act);
-  if (e.wide) {
-    if (e.res) {
-      float r[8];
-      load8(e.res, e.res_f32, row * e.ldres + col, r);
+  if (e.res) {
+    float r[8];
+    load8(e.res, e.res_f32, row * e.ldres + col, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += r[j];
-    }
-    if (e.out_f32) {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(e.out) + at);
-      o[0] = Vec<float>::from_float(f);
-      o[1] = Vec<float>::from_float(f + 4);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<bf16*>(e.out) + at) = Vec<bf16>::from_float(f);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (col + j < N) {
-        const float v = e.res ? f[j] + load_any(e.res, e.res_f32, row * e.ldres + col + j) : f[j];
-        if (e.out_f32) static_cast<float*>(e.out)[at + j] = v;
-        else static_cast<bf16*>(e.out)[at + j] = __float2bfloat16_rn(v);
-      }
-    }
+    for (int j = 0; j < 8; ++j) f[j] += r[j];
   }
+  if (e.out_f32) {
+    uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(e.out) + at);
+    o[0] = Vec<float>::from_float(f);
+    o[1] = Vec<float>::from_float(f + 4);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<bf16*>(e.out) + at) = Vec<bf16>::from_float(f);
+  }
+}
+
+// The same for one value.
+__device__ __forceinline__ void finish1(const Epi& e, long long row, int col, int N, float f) {
+  const long long at = row * N + col;
+  if (e.bias) f += load_any(e.bias, e.bias_f32, col);
+  if (e.z) e.z[at] = __float2bfloat16_rn(f);
+  activate<1>(&f, e.act);
+  if (e.res) f += load_any(e.res, e.res_f32, row * e.ldres + col);
+  if (e.out_f32) static_cast<float*>(e.out)[at] = f;
+  else static_cast<bf16*>(e.out)[at] = __float2bfloat16_rn(f);
 }
 
 // ---- the product ----------------------------------------------------------------
@@ -263,6 +249,49 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   }
 }
 
+// 32 rows x 32 columns (lane = row, v = its columns) starting at (r0, n0),
+// through the warp's staging tile (16-byte pieces XOR-swizzled by the row, so
+// that neither side has bank conflicts) to coalesced stores: four lanes take a
+// row's 32 columns, or each lane a column where rows are not of 16 bytes.
+__device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* stage, const uint32_t (&v)[32], int r0,
+                                            int n0, int M, int N, int lane) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+        make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+  if (part || e.wide) {
+    const int sub = lane >> 2, c8 = (lane & 3) * 8, col = n0 + c8;
+    float bias[8];
+    if (!part) load_bias8(e, col, N, bias);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + sub, row = r0 + r;
+      if (row < M && col < N) {
+        float f[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          Vec<float>::to_float(*reinterpret_cast<const uint4*>(stage + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4)),
+                               f + 4 * h);
+        if (part) {
+          uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * e.ldpart + col);
+          o[0] = Vec<float>::from_float(f);
+          o[1] = Vec<float>::from_float(f + 4);
+        } else {
+          finish8(e, row, col, N, f, bias);
+        }
+      }
+    }
+  } else if (n0 + lane < N) {
+    const int rows = min(32, M - r0);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      finish1(e, r0 + r, n0 + lane, N,
+              *reinterpret_cast<const float*>(stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))));
+  }
+  __syncwarp();
+}
+
 struct Unit {
   int m0, n0, split, kb0, kb1;
 };
@@ -287,7 +316,13 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs& p) {
   return t;
 }
 
-template <int CG, int BN, bool AT, bool BT>
+// kExact (fp32 outputs): the tensor cores' accumulator drops the bits below
+// its last place at every step (measured: 4.4e-6 of the result over 4096
+// terms, against 6e-7 for fp32 additions), so a product hands its sum over
+// every kExactBlocks K blocks, and the epilogue adds these up in registers.
+constexpr int kExactBlocks = 4;
+
+template <int CG, int BN, bool AT, bool BT, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ GemmArgs p) {
@@ -396,37 +431,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int u = worker; u < units && ok; u += workers) {
       const Unit t = unit_of<CG, BN>(u, p);
-      if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
-        ok = false;
-        break;
-      }
-      tphase[acc] ^= 1u;
-      tc_fence_after();
-      const uint32_t dt = tbase + (uint32_t)(acc * BN);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!mbar_wait_cluster(&full[stage], phase, deadline)) {
+      for (int kb0 = t.kb0; kb0 < t.kb1 && ok;) {
+        const int kb1 = kExact ? min(t.kb1, kb0 + kExactBlocks) : t.kb1;
+        if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
           ok = false;
           break;
         }
+        tphase[acc] ^= 1u;
         tc_fence_after();
-        const uint32_t sa = smem_addr(smem + stage * S::kStage);
+        const uint32_t dt = tbase + (uint32_t)(acc * BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_cluster(&full[stage], phase, deadline)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_addr(smem + stage * S::kStage);
 #pragma unroll
-        for (int q = 0; q < kKB; ++q) {
-          const uint64_t ad = tile_desc<AT>(sa + q * kSubA);
-          const uint64_t bd = tile_desc<BT>(sa + kKB * kSubA + q * S::kSubB);
+          for (int q = 0; q < kKB; ++q) {
+            const uint64_t ad = tile_desc<AT>(sa + q * kSubA);
+            const uint64_t bd = tile_desc<BT>(sa + kKB * kSubA + q * S::kSubB);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma<CG>(dt, ad + kk * kstep<AT>(), bd + kk * kstep<BT>(), idesc, (kb > t.kb0) | (q | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk)
+              mma<CG>(dt, ad + kk * kstep<AT>(), bd + kk * kstep<BT>(), idesc, (kb > kb0) | (q | kk) != 0);
+          }
+          commit<CG>(&empty[stage]);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
-        commit<CG>(&empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (!ok) break;
+        commit<CG>(&tfull[acc]);
+        acc ^= 1;
+        kb0 = kb1;
       }
-      if (!ok) break;
-      commit<CG>(&tfull[acc]);
-      acc ^= 1;
     }
     if (!ok) {
       // a wait ran out: let the MMAs issued so far finish reading shared
@@ -442,62 +481,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stage_buf = smem + kStages * S::kStage + (warp - 4) * 32 * 128;
     const uint32_t te[2] = {CG == 2 ? mapa_shared(smem_addr(&tempty[0]), 0) : smem_addr(&tempty[0]),
                             CG == 2 ? mapa_shared(smem_addr(&tempty[1]), 0) : smem_addr(&tempty[1])};
-    const int sub = lane >> 2, c8 = (lane & 3) * 8;
+    constexpr int kChunks = BN / 64;  // of 32 columns, this warp's half of the tile
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
+    // this warp's reads of the accumulator are done: the next product may have it
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 1 || rank == 0) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_cluster(te[acc]);
+      }
+    };
     for (int u = worker; u < units && ok; u += workers) {
       const Unit t = unit_of<CG, BN>(u, p);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
-        ok = false;
-        break;
-      }
-      tphase[acc] ^= 1u;
-      tc_fence_after();
-      const int r0 = t.m0 + 128 * (int)rank + 32 * ew;
-      const uint32_t tcol = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2));
+      const int r0 = t.m0 + 128 * (int)rank + 32 * ew, n0 = t.n0 + half * (BN / 2);
       float* part = p.epi.part ? p.epi.part + (size_t)t.split * p.M * p.epi.ldpart : nullptr;
+      auto lanes_of = [&]() { return tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2)); };
+      if constexpr (kExact) {
+        uint32_t sum[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c][j] = 0u;
+        for (int kb = t.kb0; kb < t.kb1; kb += kExactBlocks) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+            ok = false;
+            break;
+          }
+          tphase[acc] ^= 1u;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t v[32];
+            tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c][j] = __float_as_uint(__uint_as_float(sum[c][j]) + __uint_as_float(v[j]));
+          }
+          release();
+          acc ^= 1;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+          ok = false;
+          break;
+        }
+        tphase[acc] ^= 1u;
+        tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < BN / 64; ++c) {
-        const int col = t.n0 + half * (BN / 2) + 32 * c + c8;
-        float bias[8];
-        if (!part) load_bias8(p.epi, col, p.N, bias);
-        uint32_t v[32];
-        tmem_ld32(tcol + (uint32_t)(32 * c), v);
-        if (c == BN / 64 - 1) {  // the accumulator is in registers: the next product may have it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 1 || rank == 0) mbar_arrive(&tempty[acc]);
-            else mbar_arrive_cluster(te[acc]);
-          }
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t v[32];
+          tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
+          if (c == kChunks - 1) release();
+          store_chunk(p.epi, part, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
         }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<uint4*>(stage_buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-              make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + sub, row = r0 + r;
-          if (row < p.M && col < p.N) {
-            float f[8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              Vec<float>::to_float(
-                  *reinterpret_cast<const uint4*>(stage_buf + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4)), f + 4 * h);
-            if (part) {
-              uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * p.epi.ldpart + col);
-              o[0] = Vec<float>::from_float(f);
-              o[1] = Vec<float>::from_float(f + 4);
-            } else {
-              finish8(p.epi, row, col, p.N, f, bias);
-            }
-          }
-        }
-        __syncwarp();
+        acc ^= 1;
       }
-      acc ^= 1;
     }
     if (!ok) atomicOr(&s_err, 1);
   }
@@ -522,25 +566,122 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds the partial products of a split contraction in order and finishes them.
 __global__ void __launch_bounds__(256) gemm_join_kernel(const Epi e, int M, int N, int splits) {
-  const int per_row = e.ldpart / 8;
-  const long long all = (long long)M * per_row;
-  for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
-    const long long row = q / per_row;
-    const int col = (int)(q - row * per_row) * 8;
-    float f[8], bias[8];
-    load_bias8(e, col, N, bias);
+  const size_t step = (size_t)M * e.ldpart;
+  if (e.wide) {
+    const int per_row = N / 8;
+    const long long all = (long long)M * per_row;
+    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
+      const long long row = q / per_row;
+      const int col = (int)(q - row * per_row) * 8;
+      float f[8], bias[8];
+      load_bias8(e, col, N, bias);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 0.f;
-    const float* src = e.part + row * e.ldpart + col;
-    for (int sp = 0; sp < splits; ++sp) {
-      float g[8];
-      const uint4* s4 = reinterpret_cast<const uint4*>(src + (size_t)sp * M * e.ldpart);
-      Vec<float>::to_float(__ldg(s4), g);
-      Vec<float>::to_float(__ldg(s4 + 1), g + 4);
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      const float* src = e.part + row * e.ldpart + col;
+      for (int sp = 0; sp < splits; ++sp) {
+        float g[8];
+        load8(src + sp * step, 1, 0, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += g[j];
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+      }
+      finish8(e, row, col, N, f, bias);
     }
-    finish8(e, row, col, N, f, bias);
+  } else {
+    const long long all = (long long)M * N;
+    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
+      const long long row = q / N;
+      const int col = (int)(q - row * N);
+      const float* src = e.part + row * e.ldpart + col;
+      float f = 0.f;
+      for (int sp = 0; sp < splits; ++sp) f += __ldg(src + sp * step);
+      finish1(e, row, col, N, f);
+    }
+  }
+}
+
+// ---- few rows -------------------------------------------------------------------
+
+constexpr int kFewRows = 16;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+struct FewArgs {
+  const bf16* x;
+  const bf16* W;
+  long long ldx, ldw;
+  int s, K, N;
+  Epi epi;
+};
+
+// Up to 16 rows of x (decoded tokens): bound by reading W once, so W goes from
+// memory straight into the registers of warp-level MMAs, 16 bytes a lane, with
+// kUnroll loads in flight, and nothing is staged or shared before the end.  A
+// block makes 8 NT columns of y, its eight warps take every eighth 32 of the
+// contracted axis.  The order of the terms is free, so lane c of a row's four
+// feeds its 8 consecutive elements to two MMAs as their k pairs, the same for
+// x and W.  The warps' sums are added in order through shared memory.
+template <int NT, bool kHigh>
+__global__ void __launch_bounds__(256) few_rows_kernel(const FewArgs p) {
+  constexpr int kUnroll = 8 / NT;
+  __shared__ float red[8][16][8 * NT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int n0 = blockIdx.x * 8 * NT;
+  const bf16* w[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) w[t] = p.W + (long long)min(n0 + 8 * t + g, p.N - 1) * p.ldw + c * 8;
+  const bf16* x0 = p.x + (long long)g * p.ldx + c * 8;
+  const bf16* x1 = p.x + (long long)(g + 8) * p.ldx + c * 8;
+  const bool in0 = g < p.s, in1 = kHigh && g + 8 < p.s;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+  const int blocks = (p.K + 31) / 32;
+  for (int kb0 = warp; kb0 < blocks; kb0 += 8 * kUnroll) {
+    uint4 wv[kUnroll][NT], xa[kUnroll], xb[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int k = (kb0 + 8 * i) * 32;
+      const bool in = k + c * 8 < p.K;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) wv[i][t] = in ? ld_stream(reinterpret_cast<const uint4*>(w[t] + k)) : make_uint4(0, 0, 0, 0);
+      xa[i] = in && in0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : make_uint4(0, 0, 0, 0);
+      xb[i] = in && in1 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const uint32_t a0[4] = {xa[i].x, xb[i].x, xa[i].y, xb[i].y}, a1[4] = {xa[i].z, xb[i].z, xa[i].w, xb[i].w};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma16816(acc[t], a0, wv[i][t].x, wv[i][t].y);
+        mma16816(acc[t], a1, wv[i][t].z, wv[i][t].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    red[warp][g][8 * t + 2 * c] = acc[t][0];
+    red[warp][g][8 * t + 2 * c + 1] = acc[t][1];
+    if (kHigh) {
+      red[warp][g + 8][8 * t + 2 * c] = acc[t][2];
+      red[warp][g + 8][8 * t + 2 * c + 1] = acc[t][3];
+    }
+  }
+  __syncthreads();
+  for (int o = threadIdx.x; o < p.s * 8 * NT; o += 256) {
+    const int row = o / (8 * NT), j = o - row * 8 * NT;
+    if (n0 + j >= p.N) continue;
+    float f = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f += red[q][row][j];
+    finish1(p.epi, row, n0 + j, p.N, f);
   }
 }
 
@@ -626,13 +767,15 @@ constexpr int kKindCG[kKinds] = {2, 2, 1, 1};
 constexpr int kKindBN[kKinds] = {256, 128, 128, 64};
 constexpr int kPlanSms = 152;  // plans (and workspaces) are made for a whole GB300
 
-Plan plan_gemm(int M, int N, int K) {
+Plan plan_gemm(int M, int N, int K, bool exact) {
   // relative time of a K block on one tile of each shape
   const double cost[kKinds] = {1.0, 0.6, 0.6, 0.42};
   Plan best = {};
   double best_t = 0;
   const int kblocks = (K + 127) / 128;
+  bool first = true;
   for (int k = 0; k < kKinds; ++k) {
+    if (exact && k != 1 && k != 3) continue;  // its running sums need registers: the narrower tiles
     Plan q;
     q.kind = k;
     q.kblocks = kblocks;
@@ -651,7 +794,8 @@ Plan plan_gemm(int M, int N, int K) {
     const long long waves = (tiles * q.splits + workers - 1) / workers;
     const double t = (double)waves * (q.per_split * cost[k] + 3.0) + (q.splits > 1 ? 12.0 : 0.0);
     q.part_bytes = q.splits > 1 ? (size_t)q.splits * M * ((N + 7) / 8 * 8) * 4 : 0;
-    if (k == 0 || t < best_t) {
+    if (first || t < best_t) {
+      first = false;
       best = q;
       best_t = t;
     }
@@ -659,13 +803,13 @@ Plan plan_gemm(int M, int N, int K) {
   return best;
 }
 
-template <int CG, int BN, bool AT, bool BT>
+template <int CG, int BN, bool AT, bool BT, bool kExact>
 cudaError_t run_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& p, const DeviceInfo& di,
                      cudaStream_t st) {
   typedef Shape<CG, BN> S;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (err != cudaSuccess) return err;
   long long workers = di.sms / CG;
@@ -683,14 +827,14 @@ cudaError_t run_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArg
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact>, ma, mb, p);
 }
 
 // D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).
 template <bool AT, bool BT>
 cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
                     void* workspace, int32_t* status, const DeviceInfo& di, cudaStream_t st) {
-  const Plan q = plan_gemm(M, N, K);
+  const Plan q = plan_gemm(M, N, K, epi.out_f32);
   CUtensorMap ma, mb;
   const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
   if (!(AT ? make_map(&ma, A, M, K, lda, 64) : make_map(&ma, A, K, M, lda, 128)) ||
@@ -701,16 +845,34 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
   epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
   cudaError_t err;
-  switch (q.kind) {
-    case 0: err = run_gemm<2, 256, AT, BT>(ma, mb, p, di, st); break;
-    case 1: err = run_gemm<2, 128, AT, BT>(ma, mb, p, di, st); break;
-    case 2: err = run_gemm<1, 128, AT, BT>(ma, mb, p, di, st); break;
-    default: err = run_gemm<1, 64, AT, BT>(ma, mb, p, di, st); break;
+  if (epi.out_f32) {
+    err = q.kind == 1 ? run_gemm<2, 128, AT, BT, true>(ma, mb, p, di, st) : run_gemm<1, 64, AT, BT, true>(ma, mb, p, di, st);
+  } else {
+    switch (q.kind) {
+      case 0: err = run_gemm<2, 256, AT, BT, false>(ma, mb, p, di, st); break;
+      case 1: err = run_gemm<2, 128, AT, BT, false>(ma, mb, p, di, st); break;
+      case 2: err = run_gemm<1, 128, AT, BT, false>(ma, mb, p, di, st); break;
+      default: err = run_gemm<1, 64, AT, BT, false>(ma, mb, p, di, st); break;
+    }
   }
   if (err != cudaSuccess || q.splits == 1) return err;
-  const long long work = ((long long)M * (epi.ldpart / 8) + 255) / 256;
+  const long long work = ((long long)M * (epi.wide ? N / 8 : N) + 255) / 256;
   const unsigned grid = (unsigned)(work < 8LL * di.sms ? work : 8LL * di.sms);
   gemm_join_kernel<<<grid, 256, 0, st>>>(epi, M, N, q.splits);
+  return cudaGetLastError();
+}
+
+// Whichever output type the call will ask for.
+size_t part_bytes(int M, int N, int K) {
+  const size_t a = plan_gemm(M, N, K, false).part_bytes, b = plan_gemm(M, N, K, true).part_bytes;
+  return a > b ? a : b;
+}
+
+cudaError_t few_rows(const LinearArgs& a, const Epi& e, cudaStream_t st) {
+  FewArgs p = {static_cast<const bf16*>(a.x), static_cast<const bf16*>(a.W), a.ldx, a.ldw, a.s, a.K, a.N, e};
+  const unsigned grid = (unsigned)((a.N + 7) / 8);
+  if (a.s <= 8) few_rows_kernel<1, false><<<grid, 256, 0, st>>>(p);
+  else few_rows_kernel<1, true><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -733,14 +895,14 @@ BwdPlan plan_bwd(int s, int K, int N) {
   q.dz = at, at += up((size_t)s * ((N + 7) / 8 * 8) * 2);
   q.part = at, at += up((size_t)slope_rows(s, N) * N * 4);
   q.gemm = at;
-  const size_t a = plan_gemm(s, K, N).part_bytes, b = plan_gemm(N, K, s).part_bytes;
+  const size_t a = part_bytes(s, K, N), b = part_bytes(N, K, s);
   q.total = at + (a > b ? a : b);
   return q;
 }
 
 }  // namespace
 
-size_t linear_workspace(int s, int K, int N) { return plan_gemm(s, N, K).part_bytes; }
+size_t linear_workspace(int s, int K, int N) { return s <= kFewRows ? 0 : part_bytes(s, N, K); }
 size_t linear_bwd_workspace(int s, int K, int N) { return plan_bwd(s, K, N).total; }
 
 cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_t st) {
@@ -754,6 +916,7 @@ cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_
   e.out_f32 = a.out_f32;
   e.bias_f32 = a.bias_f32;
   e.res_f32 = a.res_f32;
+  if (a.s <= kFewRows) return few_rows(a, e, st);
   return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.workspace, a.status, di, st);
 }
 
