@@ -36,30 +36,61 @@ typedef __nv_bfloat16 bf16;
 
 // ---- activations -------------------------------------------------------------
 
-constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;  // 1 / sqrt(2 pi)
 constexpr float kTanhA = 0.79788456080286536f;       // sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
 
+// 1 / (1 + exp(-v)); exp overflows to inf and the quotient to 0.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and e = exp(-z^2 / 2), by Abramowitz and
+// Stegun 7.1.26: erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + p x),
+// x >= 0, to 1.5e-7.  It shares its exponential with gelu's slope, and it
+// keeps the relative precision of the tail, where 1 + erf cancels.  (With
+// erff and expf the backward pass' kernel was bound by instructions.)
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  e = __expf(-x * x);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q *= 0.5f * t * e;
+  return z < 0.f ? q : 1.f - q;
+}
+
+__device__ __forceinline__ float activated(float z, int act) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);  // NaN stays
+    case MOE_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, e);
+    }
+    case MOE_ACT_GELU_TANH: return z * sigmoid(2.f * kTanhA * (z + kTanhB * z * z * z));  // (1 + tanh(u)) / 2 = sigmoid(2u)
+    case MOE_ACT_SILU: return z * sigmoid(z);
+    default: return z;
+  }
+}
+
 template <int N>
 __device__ __forceinline__ void activate(float* f, int act) {
-  switch (act) {  // uniform over the grid
+  switch (act) {  // uniform over the grid; one loop for each, so that the code that runs is short
     case MOE_ACT_RELU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = f[j] > 0.f ? f[j] : (f[j] != f[j] ? f[j] : 0.f);  // NaN stays
+      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_RELU);
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = 0.5f * f[j] * (1.f + erff(f[j] * kSqrtHalf));
+      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_GELU);
       break;
-    case MOE_ACT_GELU_TANH:  // (1 + tanh(u)) / 2 = 1 / (1 + exp(-2u))
+    case MOE_ACT_GELU_TANH:
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        f[j] = __fdividef(f[j], 1.f + __expf(-2.f * kTanhA * (f[j] + kTanhB * f[j] * f[j] * f[j])));
+      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_GELU_TANH);
       break;
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = __fdividef(f[j], 1.f + __expf(-f[j]));
+      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_SILU);
       break;
     default: break;
   }
@@ -68,16 +99,21 @@ __device__ __forceinline__ void activate(float* f, int act) {
 __device__ __forceinline__ float slope(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MOE_ACT_GELU: return 0.5f * (1.f + erff(z * kSqrtHalf)) + z * kInvSqrt2Pi * expf(-0.5f * z * z);
+    case MOE_ACT_GELU: {
+      float e;
+      const float cdf = normal_cdf(z, e);
+      return fmaf(z * kInvSqrt2Pi, e, cdf);
+    }
     case MOE_ACT_GELU_TANH: {
-      // past 16 the slope is 0 or 1 in fp32; z's square there would overflow beside 1 - t^2 = 0
+      // s + z s' with s = sigmoid(2u); past 16 the slope is 0 or 1 in fp32, and z's
+      // square there would overflow beside s (1 - s) = 0
       z = fabsf(z) > 16.f ? copysignf(16.f, z) : z;
-      const float t = tanhf(kTanhA * (z + kTanhB * z * z * z));
-      return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * kTanhA * (1.f + 3.f * kTanhB * z * z);
+      const float s = sigmoid(2.f * kTanhA * (z + kTanhB * z * z * z));
+      return fmaf(z * s * (1.f - s), 2.f * kTanhA * (1.f + 3.f * kTanhB * z * z), s);
     }
     case MOE_ACT_SILU: {
-      const float sg = 1.f / (1.f + expf(-z));
-      return sg * (1.f + z * (1.f - sg));
+      const float s = sigmoid(z);
+      return s * (1.f + z * (1.f - s));
     }
     default: return 1.f;
   }
@@ -94,8 +130,7 @@ struct Epi {
   long long ldres;
   int ldpart;
   int act, out_f32, bias_f32, res_f32;
-  int wide;         // N and the residual's stride are multiples of 8: 16-byte accesses,
-                    // else each lane takes one column and walks down the rows
+  int wide;         // N and the residual's stride are multiples of 8: rows of 16-byte pieces
 };
 
 __device__ __forceinline__ float load_any(const void* p, int is_f32, long long i) {
@@ -249,10 +284,96 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   }
 }
 
-// 32 rows x 32 columns (lane = row, v = its columns) starting at (r0, n0),
-// through the warp's staging tile (16-byte pieces XOR-swizzled by the row, so
-// that neither side has bank conflicts) to coalesced stores: four lanes take a
-// row's 32 columns, or each lane a column where rows are not of 16 bytes.
+// 32 rows x 32 columns starting at (r0, n0), lane = row, v its columns.  The
+// usual way out (bulk): bias, activation and residual in that layout, then
+// the rounded rows into the warp's staging tile, which a TMA store writes,
+// clipped at the tensor's edge.  The tile is two pieces of 32 rows x 64 bytes,
+// used in turn, so one store drains while the next piece is filled; 64-byte
+// swizzle (the 16-byte piece's index XOR half the row), free of bank conflicts.
+// Against four lanes a row and 16-byte stores this took a quarter of the
+// instructions: dx of 16384 x 4096 from 128 columns 75.7 -> @DX@ us.
+struct Bulk {
+  uint8_t* stage;  // this warp's 2 x 2 KB
+  int piece;
+};
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_addr(src))
+               : "memory");
+}
+
+// One piece: 16 words of each lane's row to columns starting at x.
+__device__ __forceinline__ void put_piece(Bulk& b, const CUtensorMap* map, const uint32_t (&w)[16], int x, int y, int lane) {
+  uint8_t* dst = b.stage + b.piece * 2048;
+  if (lane == 0) bulk_wait_read<1>();  // the store before last, from this piece
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, dst, x, y);
+    bulk_commit();
+  }
+  b.piece ^= 1;
+}
+
+__device__ __forceinline__ void put_bf16(Bulk& b, const CUtensorMap* map, const float (&f)[32], int x, int y, int lane) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  put_piece(b, map, w, x, y, lane);
+}
+
+__device__ __forceinline__ void put_f32(Bulk& b, const CUtensorMap* map, const float (&f)[32], int x, int y, int N, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (x + 16 * h < N) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(f[16 * h + j]);
+      put_piece(b, map, w, x + 16 * h, y, lane);
+    }
+  }
+}
+
+__device__ __forceinline__ void add32(const void* p, int is_f32, long long at, int n, float (&f)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (8 * q < n) {
+      float t[8];
+      load8(p, is_f32, at + 8 * q, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[8 * q + j] += t[j];
+    }
+  }
+}
+
+__device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtensorMap* tmY, const CUtensorMap* tmZ,
+                                            const uint32_t (&v)[32], int r0, int n0, int M, int N, int lane) {
+  if (r0 >= M || n0 >= N) return;  // the whole warp
+  float f[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+  if (e.bias) add32(e.bias, e.bias_f32, n0, N - n0, f);
+  if (e.z) put_bf16(b, tmZ, f, n0, r0, lane);
+  if (e.act != MOE_ACT_NONE) activate<32>(f, e.act);
+  if (e.res && r0 + lane < M) add32(e.res, e.res_f32, (long long)(r0 + lane) * e.ldres + n0, N - n0, f);
+  if (e.out_f32) put_f32(b, tmY, f, n0, r0, N, lane);
+  else put_bf16(b, tmY, f, n0, r0, lane);
+}
+
+// The same block as fp32 through the staging tile (16-byte pieces
+// XOR-swizzled by the row), then read along rows: partial products of a split
+// contraction (four lanes a row), or, where rows are not of 16 bytes and TMA
+// cannot write them, each lane a column walking down the rows.
 __device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* stage, const uint32_t (&v)[32], int r0,
                                             int n0, int M, int N, int lane) {
 #pragma unroll
@@ -260,34 +381,47 @@ __device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* 
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
         make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   __syncwarp();
-  if (part || e.wide) {
+  if (part) {
     const int sub = lane >> 2, c8 = (lane & 3) * 8, col = n0 + c8;
-    float bias[8];
-    if (!part) load_bias8(e, col, N, bias);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 8 * i + sub, row = r0 + r;
       if (row < M && col < N) {
-        float f[8];
+        uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * e.ldpart + col);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          Vec<float>::to_float(*reinterpret_cast<const uint4*>(stage + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4)),
-                               f + 4 * h);
-        if (part) {
-          uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * e.ldpart + col);
-          o[0] = Vec<float>::from_float(f);
-          o[1] = Vec<float>::from_float(f + 4);
-        } else {
-          finish8(e, row, col, N, f, bias);
-        }
+          o[h] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4));
       }
     }
   } else if (n0 + lane < N) {
-    const int rows = min(32, M - r0);
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r)
-      finish1(e, r0 + r, n0 + lane, N,
-              *reinterpret_cast<const float*>(stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2))));
+    const int col = n0 + lane;
+    const float bias = e.bias ? load_any(e.bias, e.bias_f32, col) : 0.f;
+#pragma unroll 1
+    for (int q = 0; q < 32 && r0 + q < M; q += 8) {
+      float f[8], res[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = q + i;
+        res[i] = e.res && r0 + r < M ? load_any(e.res, e.res_f32, (long long)(r0 + r) * e.ldres + col) : 0.f;
+        f[i] = bias +
+               *reinterpret_cast<const float*>(stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
+      }
+      const long long at = (long long)(r0 + q) * N + col;
+      if (e.z) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + q + i < M) e.z[at + (long long)i * N] = __float2bfloat16_rn(f[i]);
+      }
+      activate<8>(f, e.act);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] += res[i];
+        if (r0 + q + i < M) {
+          if (e.out_f32) static_cast<float*>(e.out)[at + (long long)i * N] = f[i];
+          else static_cast<bf16*>(e.out)[at + (long long)i * N] = __float2bfloat16_rn(f[i]);
+        }
+      }
+    }
   }
   __syncwarp();
 }
@@ -325,6 +459,7 @@ constexpr int kExactBlocks = 4;
 template <int CG, int BN, bool AT, bool BT, bool kExact>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
                 const __grid_constant__ GemmArgs p) {
   typedef Shape<CG, BN> S;
   constexpr int kStages = S::kStages;
@@ -485,6 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
+    Bulk bulk = {stage_buf, 0};
+    const bool staged = p.epi.part || !p.epi.wide;  // see store_chunk
     // this warp's reads of the accumulator are done: the next product may have it
     auto release = [&]() {
       tc_fence_before();
@@ -524,8 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+        for (int c = 0; c < kChunks; ++c) {
+          if (staged) store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+          else finish_bulk(p.epi, bulk, &tmY, &tmZ, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+        }
       } else {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
           ok = false;
@@ -538,11 +677,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
           if (c == kChunks - 1) release();
-          store_chunk(p.epi, part, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
+          if (staged) store_chunk(p.epi, part, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
+          else finish_bulk(p.epi, bulk, &tmY, &tmZ, v, r0, n0 + 32 * c, p.M, p.N, lane);
         }
         acc ^= 1;
       }
     }
+    if (lane == 0) bulk_wait_all();  // the stores have read the staging tile and are written
     if (!ok) atomicOr(&s_err, 1);
   }
 
@@ -693,48 +834,67 @@ struct SlopeArgs {
   bf16* dz;        // [s][lddz], or NULL: only the column sums
   float* part;     // [gridDim.y][N] column sums, or NULL
   long long lddy, ldz, lddz;
-  int s, N, act, dy_f32, wide;
+  int s, N;
 };
 
-// dz = dy act'(z) and its column sums: a warp walks rows of 256 columns (8 a
-// lane), a block's eight warps add up through shared memory, each block one
-// partial row.  dz is rounded to bf16 for the tensor cores; the sums are taken
-// before that.
+// dz = dy act'(z) and its column sums: a warp walks rows of 32 W columns (W a
+// lane: 16 bytes of bf16, or one element where rows are not of 16 bytes),
+// four rows' loads in flight, a block's eight warps add up through shared
+// memory, each block one partial row.  dz is rounded to bf16 for the tensor
+// cores; the sums are taken before that.
+template <int W, bool kF32, int kAct>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs p) {
-  __shared__ float acc[8][256 + 8];
+  constexpr int kRows = 4;
+  __shared__ float acc[8][32 * W + 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * 256 + lane * 8;
-  float sum[8];
+  const int col = blockIdx.x * 32 * W + lane * W;
+  float sum[W];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
-  if (col < p.N) {
-#pragma unroll 2
-    for (long long row = (long long)blockIdx.y * 8 + warp; row < p.s; row += (long long)gridDim.y * 8) {
-      float d[8], z[8];
-      if (p.wide) {
-        load8(p.dy, p.dy_f32, row * p.lddy + col, d);
-        if (p.z) load8(p.z, 0, row * p.ldz + col, z);
-      } else {
+  for (int j = 0; j < W; ++j) sum[j] = 0.f;
+  const long long step = (long long)gridDim.y * 8;
+  const int width = (int)p.lddz;  // dz's padding columns, up to 7, get zeros
+  if (col < (p.dz ? width : p.N)) {
+    const bool in = col < p.N;
+    for (long long row0 = (long long)blockIdx.y * 8 + warp; row0 < p.s; row0 += kRows * step) {
+      float d[kRows][W], z[kRows][W];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          d[j] = col + j < p.N ? load_any(p.dy, p.dy_f32, row * p.lddy + col + j) : 0.f;
-          z[j] = p.z && col + j < p.N ? load_any(p.z, 0, row * p.ldz + col + j) : 0.f;
+      for (int i = 0; i < kRows; ++i) {
+        const long long row = row0 + i * step;
+#pragma unroll
+        for (int j = 0; j < W; ++j) d[i][j] = z[i][j] = 0.f;
+        if (in && row < p.s) {
+          if (W == 8) {
+            load8(p.dy, kF32, row * p.lddy + col, d[i]);
+            if (kAct != MOE_ACT_NONE) load8(p.z, 0, row * p.ldz + col, z[i]);
+          } else {
+            d[i][0] = load_any(p.dy, kF32, row * p.lddy + col);
+            if (kAct != MOE_ACT_NONE) z[i][0] = load_any(p.z, 0, row * p.ldz + col);
+          }
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (p.z) d[j] *= slope(z[j], p.act);
-        sum[j] += d[j];
+      for (int i = 0; i < kRows; ++i) {
+        const long long row = row0 + i * step;
+        if (row >= p.s) break;
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          // rounded here, whether or not dz is stored: db has the same bits either way
+          if (kAct != MOE_ACT_NONE) d[i][j] = __fmul_rn(d[i][j], slope(z[i][j], kAct));
+          sum[j] += d[i][j];
+        }
+        if (p.dz) {
+          if (W == 8) *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = Vec<bf16>::from_float(d[i]);
+          else p.dz[row * p.lddz + col] = __float2bfloat16_rn(d[i][0]);
+        }
       }
-      if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = Vec<bf16>::from_float(d);
     }
   }
   if (!p.part) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) acc[warp][lane * 8 + j] = sum[j];
+  for (int j = 0; j < W; ++j) acc[warp][lane * W + j] = sum[j];
   __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c < p.N) {
+  const int c = blockIdx.x * 32 * W + threadIdx.x;
+  if (threadIdx.x < 32 * W && c < p.N) {
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += acc[w][threadIdx.x];
@@ -743,6 +903,20 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs p) {
 }
 
 // ---- host ------------------------------------------------------------------------
+
+// Output [outer][inner] of 4- or 2-byte elements as the epilogue stores it:
+// boxes of 32 rows x 64 bytes, 64-byte swizzle.
+bool make_out_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, bool f32) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner * (f32 ? 4 : 2)};
+  cuuint32_t box[2] = {f32 ? 16u : 32u, 32u};
+  cuuint32_t estride[2] = {1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+            strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // 2-D bf16 [outer][inner], rows ld elements apart, 128-byte swizzle.
 bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_rows) {
@@ -804,8 +978,7 @@ Plan plan_gemm(int M, int N, int K, bool exact) {
 }
 
 template <int CG, int BN, bool AT, bool BT, bool kExact>
-cudaError_t run_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs& p, const DeviceInfo& di,
-                     cudaStream_t st) {
+cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
   typedef Shape<CG, BN> S;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
@@ -827,7 +1000,7 @@ cudaError_t run_gemm(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArg
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact>, maps[0], maps[1], maps[2], maps[3], p);
 }
 
 // D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).
@@ -835,24 +1008,27 @@ template <bool AT, bool BT>
 cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
                     void* workspace, int32_t* status, const DeviceInfo& di, cudaStream_t st) {
   const Plan q = plan_gemm(M, N, K, epi.out_f32);
-  CUtensorMap ma, mb;
+  CUtensorMap maps[4] = {};
   const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
-  if (!(AT ? make_map(&ma, A, M, K, lda, 64) : make_map(&ma, A, K, M, lda, 128)) ||
-      !(BT ? make_map(&mb, B, N, K, ldb, box_b) : make_map(&mb, B, K, N, ldb, box_b)))
+  if (!(AT ? make_map(&maps[0], A, M, K, lda, 64) : make_map(&maps[0], A, K, M, lda, 128)) ||
+      !(BT ? make_map(&maps[1], B, N, K, ldb, box_b) : make_map(&maps[1], B, K, N, ldb, box_b)))
     return cudaErrorInvalidValue;
   epi.part = q.splits > 1 ? static_cast<float*>(workspace) : nullptr;
   epi.ldpart = (N + 7) / 8 * 8;
   epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
+  if (!epi.part && epi.wide &&
+      (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32) || (epi.z && !make_out_map(&maps[3], epi.z, N, M, false))))
+    return cudaErrorInvalidValue;
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
   cudaError_t err;
   if (epi.out_f32) {
-    err = q.kind == 1 ? run_gemm<2, 128, AT, BT, true>(ma, mb, p, di, st) : run_gemm<1, 64, AT, BT, true>(ma, mb, p, di, st);
+    err = q.kind == 1 ? run_gemm<2, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
   } else {
     switch (q.kind) {
-      case 0: err = run_gemm<2, 256, AT, BT, false>(ma, mb, p, di, st); break;
-      case 1: err = run_gemm<2, 128, AT, BT, false>(ma, mb, p, di, st); break;
-      case 2: err = run_gemm<1, 128, AT, BT, false>(ma, mb, p, di, st); break;
-      default: err = run_gemm<1, 64, AT, BT, false>(ma, mb, p, di, st); break;
+      case 0: err = run_gemm<2, 256, AT, BT, false>(maps, p, di, st); break;
+      case 1: err = run_gemm<2, 128, AT, BT, false>(maps, p, di, st); break;
+      case 2: err = run_gemm<1, 128, AT, BT, false>(maps, p, di, st); break;
+      default: err = run_gemm<1, 64, AT, BT, false>(maps, p, di, st); break;
     }
   }
   if (err != cudaSuccess || q.splits == 1) return err;
@@ -879,8 +1055,8 @@ cudaError_t few_rows(const LinearArgs& a, const Epi& e, cudaStream_t st) {
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 int slope_rows(int s, int N) {  // blocks along the rows: enough to fill the machine, at least 32 rows each
-  const int cols = (N + 255) / 256;
-  int rows = (4 * kPlanSms + cols - 1) / cols;
+  const int cols = (N + (N % 8 == 0 ? 255 : 31)) / (N % 8 == 0 ? 256 : 32);
+  int rows = (6 * kPlanSms + cols - 1) / cols;
   const int most = (s + 31) / 32;
   if (rows > most) rows = most;
   return rows < 1 ? 1 : rows;
@@ -904,6 +1080,23 @@ BwdPlan plan_bwd(int s, int K, int N) {
 
 size_t linear_workspace(int s, int K, int N) { return s <= kFewRows ? 0 : part_bytes(s, N, K); }
 size_t linear_bwd_workspace(int s, int K, int N) { return plan_bwd(s, K, N).total; }
+
+namespace {
+
+template <int W, bool kF32>
+cudaError_t run_slope(const SlopeArgs& p, int act, int rows, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.lddz + 32 * W - 1) / (32 * W)), (unsigned)rows);
+  switch (act) {
+    case MOE_ACT_RELU: slope_kernel<W, kF32, MOE_ACT_RELU><<<grid, 256, 0, st>>>(p); break;
+    case MOE_ACT_GELU: slope_kernel<W, kF32, MOE_ACT_GELU><<<grid, 256, 0, st>>>(p); break;
+    case MOE_ACT_GELU_TANH: slope_kernel<W, kF32, MOE_ACT_GELU_TANH><<<grid, 256, 0, st>>>(p); break;
+    case MOE_ACT_SILU: slope_kernel<W, kF32, MOE_ACT_SILU><<<grid, 256, 0, st>>>(p); break;
+    default: slope_kernel<W, kF32, MOE_ACT_NONE><<<grid, 256, 0, st>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_t st) {
   Epi e = {};
@@ -929,7 +1122,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
   if (own_dz || a.db) {
     SlopeArgs p = {};
     p.dy = a.dy;
-    p.z = a.act != MOE_ACT_NONE ? static_cast<const bf16*>(a.z) : nullptr;
+    p.z = a.act != MOE_ACT_NONE ? static_cast<const bf16*>(a.z) : nullptr;  // unused without an activation
     p.dz = own_dz ? reinterpret_cast<bf16*>(ws + q.dz) : nullptr;
     p.part = a.db ? reinterpret_cast<float*>(ws + q.part) : nullptr;
     p.lddy = a.lddy;
@@ -937,12 +1130,11 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
     p.lddz = lddz;
     p.s = a.s;
     p.N = a.N;
-    p.act = a.act;
-    p.dy_f32 = a.dy_f32;
-    p.wide = a.N % 8 == 0 && a.lddy % 8 == 0 && (!p.z || a.ldz % 8 == 0);
     const int rows = slope_rows(a.s, a.N);
-    slope_kernel<<<dim3((unsigned)((a.N + 255) / 256), (unsigned)rows), 256, 0, st>>>(p);
-    cudaError_t err = cudaGetLastError();
+    const bool wide = a.N % 8 == 0 && a.lddy % 8 == 0 && (!p.z || a.ldz % 8 == 0);
+    cudaError_t err;
+    if (wide) err = a.dy_f32 ? run_slope<8, true>(p, a.act, rows, st) : run_slope<8, false>(p, a.act, rows, st);
+    else err = a.dy_f32 ? run_slope<1, true>(p, a.act, rows, st) : run_slope<1, false>(p, a.act, rows, st);
     if (err != cudaSuccess) return err;
     if (a.db) {
       err = launch_sum_parts(p.part, rows, 0, a.N, a.db, nullptr, st);
