@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
   const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the join, later in the stream
   // tokens outside every sequence: nothing of theirs counts
   const int first = p.offsets ? __ldg(p.offsets) : 0, last = p.offsets ? __ldg(p.offsets + p.B) : p.s;
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
     }
     __syncthreads();  // the shared sums are rewritten by the next piece
   }
+  grid_dependents_launch();
   if (bad & 1) raise_status(p.status, MOE_DEV_NONFINITE);
   if (bad & 2) raise_status(p.status, MOE_DEV_BAD_ROUTE);
 }
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin 
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int b = (int)(blockIdx.x / (unsigned)p.cols), block = (int)(blockIdx.x - (unsigned)b * p.cols);
   const int col = block * 32 + tx;
+  grid_dependency_wait();
   int lo = 0, hi = p.s;
   if (p.offsets) {
     lo = max(0, __ldg(p.offsets + b));
@@ -312,6 +315,7 @@ __global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin 
       s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     }
   }
+  grid_dependents_launch();
   __syncthreads();
   if (!s_last) return;
   __threadfence();
@@ -373,6 +377,7 @@ __global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
   const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  grid_dependency_wait();
   const float wl = __ldg(p.dloss) * __ldg(p.norm), wz = 2.f * __ldg(p.dloss + 1) * __ldg(p.norm + 1);
   if (p.offsets) {
     copy_rows<V>(p, lo, min(hi, max(lo, __ldg(p.offsets))));
@@ -425,6 +430,7 @@ __global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p)
       }
     }
   }
+  grid_dependents_launch();
 }
 
 struct Shape {
@@ -494,18 +500,17 @@ cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_
   unsigned* ticket = reinterpret_cast<unsigned*>(ws + q.ticket);
   BalanceFwd p = {logits, idx, valid, offsets, s, e, k, B, chunk, lse, pc, ticket, status};
   const unsigned grid = s > 0 ? (unsigned)((s + chunk - 1) / chunk) : 1u;  // no tokens: one block clears the ticket
+  cudaError_t err = cudaErrorInvalidValue;
 #define MOE_RUN(v, l, n) \
-  if (h.V == v && h.L == l && h.NI == n) balance_kernel<v, l, n><<<grid, kBlock, 0, st>>>(p);
+  if (h.V == v && h.L == l && h.NI == n) err = launch_chained(balance_kernel<v, l, n>, dim3(grid), dim3(kBlock), 0, st, p);
   MOE_BALANCE_SHAPES(MOE_RUN)
 #undef MOE_RUN
-  cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const int cols = (e + 31) / 32;
   BalanceJoin j = {offsets, s, e, k, B, chunk, cols, pc, counts, mean_prob, coef,
                    reinterpret_cast<float*>(ws + q.part), reinterpret_cast<float*>(ws + q.zpart),
                    reinterpret_cast<int*>(ws + q.tpart), ticket, loss, norm};
-  balance_join_kernel<<<(unsigned)cols * (unsigned)B, kBlock, 0, st>>>(j);
-  return cudaGetLastError();
+  return launch_chained(balance_join_kernel, dim3((unsigned)cols * (unsigned)B), dim3(kBlock), 0, st, j);
 }
 
 cudaError_t launch_balance_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
@@ -515,11 +520,13 @@ cudaError_t launch_balance_bwd(const float* logits, const float* lse, const floa
   const int chunk = chunk_of(s, h);
   BalanceBwd p = {logits, lse, coef, norm, dloss, valid, offsets, add, dlogits, s, e, B, chunk};
   const unsigned grid = (unsigned)((s + chunk - 1) / chunk);
+  cudaError_t err = cudaErrorInvalidValue;
 #define MOE_RUN(v, l, n) \
-  if (h.V == v && h.L == l && h.NI == n) balance_bwd_kernel<v, l, n><<<grid, kBlock, 0, st>>>(p);
+  if (h.V == v && h.L == l && h.NI == n) \
+    err = launch_chained(balance_bwd_kernel<v, l, n>, dim3(grid), dim3(kBlock), 0, st, p);
   MOE_BALANCE_SHAPES(MOE_RUN)
 #undef MOE_RUN
-  return cudaGetLastError();
+  return err;
 }
 
 }  // namespace moe

@@ -344,28 +344,57 @@ __device__ __forceinline__ void put_f32(Bulk& b, const CUtensorMap* map, const f
   }
 }
 
-__device__ __forceinline__ void add32(const void* p, int is_f32, long long at, int n, float (&f)[32]) {
+// 32 consecutive values of fp32 or bf16 memory (those below n, a multiple of
+// 8), first all loads, so that they travel together, then the sum.
+struct Raw32 {
+  uint4 v[8];
+};
+
+__device__ __forceinline__ void load32(Raw32& r, const void* p, int is_f32, long long at, int n) {
+  if (is_f32) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (8 * q < n) {
-      float t[8];
-      load8(p, is_f32, at + 8 * q, t);
+    for (int i = 0; i < 8; ++i) r.v[i] = 4 * i < n ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[8 * q + j] += t[j];
-    }
+    for (int i = 0; i < 4; ++i) r.v[i] = 8 * i < n ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
   }
 }
 
+__device__ __forceinline__ void add32(const Raw32& r, int is_f32, float (&f)[32]) {
+  float t[32];
+  if (is_f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) Vec<float>::to_float(r.v[i], t + 4 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Vec<bf16>::to_float(r.v[i], t + 8 * i);
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) f[j] += t[j];
+}
+
+// The residual of this lane's row, loaded before the accumulator is waited for.
+__device__ __forceinline__ void load_residual(const Epi& e, Raw32& r, int row, int n0, int M, int N) {
+  if (e.res) load32(r, e.res, e.res_f32, (long long)row * e.ldres + n0, row < M ? N - n0 : 0);
+}
+
 __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtensorMap* tmY, const CUtensorMap* tmZ,
-                                            const uint32_t (&v)[32], int r0, int n0, int M, int N, int lane) {
+                                            const uint32_t (&v)[32], const Raw32& res, int r0, int n0, int M, int N,
+                                            int lane) {
   if (r0 >= M || n0 >= N) return;  // the whole warp
   float f[32];
 #pragma unroll
   for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-  if (e.bias) add32(e.bias, e.bias_f32, n0, N - n0, f);
+  if (e.bias) {
+    Raw32 bias;
+    load32(bias, e.bias, e.bias_f32, n0, N - n0);
+    add32(bias, e.bias_f32, f);
+  }
   if (e.z) put_bf16(b, tmZ, f, n0, r0, lane);
   if (e.act != MOE_ACT_NONE) activate<32>(f, e.act);
-  if (e.res && r0 + lane < M) add32(e.res, e.res_f32, (long long)(r0 + lane) * e.ldres + n0, N - n0, f);
+  if (e.res) add32(res, e.res_f32, f);
   if (e.out_f32) put_f32(b, tmY, f, n0, r0, N, lane);
   else put_bf16(b, tmY, f, n0, r0, lane);
 }
@@ -394,31 +423,48 @@ __device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* 
       }
     }
   } else if (n0 + lane < N) {
-    const int col = n0 + lane;
+    const int col = n0 + lane, rows = min(32, M - r0);
     const float bias = e.bias ? load_any(e.bias, e.bias_f32, col) : 0.f;
-#pragma unroll 1
-    for (int q = 0; q < 32 && r0 + q < M; q += 8) {
-      float f[8], res[8];
+    float res[32];
+    if (e.res) {  // all 32 loads in flight at once
+      const long long at = (long long)r0 * e.ldres + col;
+      if (e.res_f32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) res[i] = i < rows ? __ldg(static_cast<const float*>(e.res) + at + i * e.ldres) : 0.f;
+      } else {
+        unsigned short raw[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          raw[i] = i < rows ? __ldg(static_cast<const unsigned short*>(e.res) + at + i * e.ldres) : (unsigned short)0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) res[i] = __uint_as_float((uint32_t)raw[i] << 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) res[i] = 0.f;
+    }
+    const long long at = (long long)r0 * N + col;
+#pragma unroll
+    for (int q = 0; q < 32; q += 8) {
+      float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = q + i;
-        res[i] = e.res && r0 + r < M ? load_any(e.res, e.res_f32, (long long)(r0 + r) * e.ldres + col) : 0.f;
         f[i] = bias +
                *reinterpret_cast<const float*>(stage + r * 128 + ((((lane >> 2) ^ (r & 7)) << 4) | ((lane & 3) << 2)));
       }
-      const long long at = (long long)(r0 + q) * N + col;
       if (e.z) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (r0 + q + i < M) e.z[at + (long long)i * N] = __float2bfloat16_rn(f[i]);
+          if (q + i < rows) e.z[at + (long long)(q + i) * N] = __float2bfloat16_rn(f[i]);
       }
       activate<8>(f, e.act);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        f[i] += res[i];
-        if (r0 + q + i < M) {
-          if (e.out_f32) static_cast<float*>(e.out)[at + (long long)i * N] = f[i];
-          else static_cast<bf16*>(e.out)[at + (long long)i * N] = __float2bfloat16_rn(f[i]);
+        f[i] += res[q + i];
+        if (q + i < rows) {
+          if (e.out_f32) static_cast<float*>(e.out)[at + (long long)(q + i) * N] = f[i];
+          else static_cast<bf16*>(e.out)[at + (long long)(q + i) * N] = __float2bfloat16_rn(f[i]);
         }
       }
     }
@@ -471,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
 
   if (threadIdx.x == 0) {
     s_err = 0;
@@ -500,6 +545,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
+  grid_dependency_wait();  // all set-up is done: from here on memory of earlier kernels is read
+  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any remote signal
@@ -662,8 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (staged) store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
-          else finish_bulk(p.epi, bulk, &tmY, &tmZ, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+          if (staged) {
+            store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
+          } else {
+            Raw32 res;
+            load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
+            finish_bulk(p.epi, bulk, &tmY, &tmZ, sum[c], res, r0, n0 + 32 * c, p.M, p.N, lane);
+          }
         }
       } else {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
@@ -674,11 +726,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < kChunks; ++c) {
+          Raw32 res;
+          if (!staged) load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
           uint32_t v[32];
           tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
           if (c == kChunks - 1) release();
           if (staged) store_chunk(p.epi, part, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
-          else finish_bulk(p.epi, bulk, &tmY, &tmZ, v, r0, n0 + 32 * c, p.M, p.N, lane);
+          else finish_bulk(p.epi, bulk, &tmY, &tmZ, v, res, r0, n0 + 32 * c, p.M, p.N, lane);
         }
         acc ^= 1;
       }
@@ -687,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) atomicOr(&s_err, 1);
   }
 
+  grid_dependents_launch();
   tc_fence_before();
   __syncthreads();
   if (s_err) {  // let copies in flight land before shared memory goes
@@ -708,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Adds the partial products of a split contraction in order and finishes them.
 __global__ void __launch_bounds__(256) gemm_join_kernel(const Epi e, int M, int N, int splits) {
   const size_t step = (size_t)M * e.ldpart;
+  grid_dependency_wait();
   if (e.wide) {
     const int per_row = N / 8;
     const long long all = (long long)M * per_row;
@@ -738,6 +794,7 @@ __global__ void __launch_bounds__(256) gemm_join_kernel(const Epi e, int M, int 
       finish1(e, row, col, N, f);
     }
   }
+  grid_dependents_launch();
 }
 
 // ---- few rows -------------------------------------------------------------------
@@ -785,6 +842,7 @@ __global__ void __launch_bounds__(256) few_rows_kernel(const FewArgs p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
   const int blocks = (p.K + 31) / 32;
+  grid_dependency_wait();
   for (int kb0 = warp; kb0 < blocks; kb0 += 8 * kUnroll) {
     uint4 wv[kUnroll][NT], xa[kUnroll], xb[kUnroll];
 #pragma unroll
@@ -824,6 +882,7 @@ __global__ void __launch_bounds__(256) few_rows_kernel(const FewArgs p) {
     for (int q = 0; q < 8; ++q) f += red[q][row][j];
     finish1(p.epi, row, n0 + j, p.N, f);
   }
+  grid_dependents_launch();
 }
 
 // ---- dz and the bias' gradient --------------------------------------------------
@@ -852,6 +911,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs p) {
 #pragma unroll
   for (int j = 0; j < W; ++j) sum[j] = 0.f;
   const long long step = (long long)gridDim.y * 8;
+  grid_dependency_wait();
   const int width = (int)p.lddz;  // dz's padding columns, up to 7, get zeros
   if (col < (p.dz ? width : p.N)) {
     const bool in = col < p.N;
@@ -889,6 +949,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs p) {
       }
     }
   }
+  grid_dependents_launch();
   if (!p.part) return;
 #pragma unroll
   for (int j = 0; j < W; ++j) acc[warp][lane * W + j] = sum[j];
@@ -993,13 +1054,15 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const Devi
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = CG == 2 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact>, maps[0], maps[1], maps[2], maps[3], p);
 }
 
@@ -1034,8 +1097,7 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
   if (err != cudaSuccess || q.splits == 1) return err;
   const long long work = ((long long)M * (epi.wide ? N / 8 : N) + 255) / 256;
   const unsigned grid = (unsigned)(work < 8LL * di.sms ? work : 8LL * di.sms);
-  gemm_join_kernel<<<grid, 256, 0, st>>>(epi, M, N, q.splits);
-  return cudaGetLastError();
+  return launch_chained(gemm_join_kernel, dim3(grid), dim3(256), 0, st, epi, M, N, q.splits);
 }
 
 // Whichever output type the call will ask for.
@@ -1047,9 +1109,7 @@ size_t part_bytes(int M, int N, int K) {
 cudaError_t few_rows(const LinearArgs& a, const Epi& e, cudaStream_t st) {
   FewArgs p = {static_cast<const bf16*>(a.x), static_cast<const bf16*>(a.W), a.ldx, a.ldw, a.s, a.K, a.N, e};
   const unsigned grid = (unsigned)((a.N + 7) / 8);
-  if (a.s <= 8) few_rows_kernel<1, false><<<grid, 256, 0, st>>>(p);
-  else few_rows_kernel<1, true><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_chained(a.s <= 8 ? few_rows_kernel<1, false> : few_rows_kernel<1, true>, dim3(grid), dim3(256), 0, st, p);
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -1086,14 +1146,15 @@ namespace {
 template <int W, bool kF32>
 cudaError_t run_slope(const SlopeArgs& p, int act, int rows, cudaStream_t st) {
   const dim3 grid((unsigned)((p.lddz + 32 * W - 1) / (32 * W)), (unsigned)rows);
+  auto kern = slope_kernel<W, kF32, MOE_ACT_NONE>;
   switch (act) {
-    case MOE_ACT_RELU: slope_kernel<W, kF32, MOE_ACT_RELU><<<grid, 256, 0, st>>>(p); break;
-    case MOE_ACT_GELU: slope_kernel<W, kF32, MOE_ACT_GELU><<<grid, 256, 0, st>>>(p); break;
-    case MOE_ACT_GELU_TANH: slope_kernel<W, kF32, MOE_ACT_GELU_TANH><<<grid, 256, 0, st>>>(p); break;
-    case MOE_ACT_SILU: slope_kernel<W, kF32, MOE_ACT_SILU><<<grid, 256, 0, st>>>(p); break;
-    default: slope_kernel<W, kF32, MOE_ACT_NONE><<<grid, 256, 0, st>>>(p); break;
+    case MOE_ACT_RELU: kern = slope_kernel<W, kF32, MOE_ACT_RELU>; break;
+    case MOE_ACT_GELU: kern = slope_kernel<W, kF32, MOE_ACT_GELU>; break;
+    case MOE_ACT_GELU_TANH: kern = slope_kernel<W, kF32, MOE_ACT_GELU_TANH>; break;
+    case MOE_ACT_SILU: kern = slope_kernel<W, kF32, MOE_ACT_SILU>; break;
+    default: break;
   }
-  return cudaGetLastError();
+  return launch_chained(kern, grid, dim3(256), 0, st, p);
 }
 
 }  // namespace

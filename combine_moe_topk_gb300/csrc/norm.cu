@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) layernorm_kernel(const NormFwd
   const int groups = (blockDim.x >> 5) / G;
   const long long row = (long long)blockIdx.x * groups + group;
   if (row >= p.s) return;  // the whole group together
+  grid_dependency_wait();
   const int t = threadIdx.x - group * 32 * G, span = 32 * G;
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   Chunk<T, C> raw[E];
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) layernorm_kernel(const NormFwd
     if (p.mean) p.mean[row] = mu;
     if (p.rstd) p.rstd[row] = r;
   }
+  grid_dependents_launch();
 }
 
 // Rows too long for the registers of a block: three passes over the row,
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const NormBwd p, con
   const int groups = (blockDim.x >> 5) / G;
   const int t = threadIdx.x - group * 32 * G, span = 32 * G;
   const long long stride = (long long)gridDim.x * groups;
+  grid_dependency_wait();
   float wv[E][C], dw[E][C], db[E][C];
 #pragma unroll
   for (int i = 0; i < E; ++i) {
@@ -324,6 +327,7 @@ __global__ void __launch_bounds__(512) layernorm_bwd_kernel(const NormBwd p, con
       }
     }
   }
+  grid_dependents_launch();
   if (!p.part) return;
   for (int q = 0; q < groups; ++q) {
     const bool last = q == groups - 1;
@@ -400,17 +404,18 @@ __global__ void __launch_bounds__(512) sum_parts_kernel(const float* part, int p
                                                         float* out0, float* out1) {
   __shared__ float acc[16][33];
   float* out = blockIdx.y ? out1 : out0;
-  if (!out) return;
   const int col = blockIdx.x * 32 + threadIdx.x;
   const float* src = part + (size_t)blockIdx.y * stride_parts * m;
   float v = 0.f;
+  grid_dependency_wait();
   if (col < m) {
 #pragma unroll 4
     for (int q = threadIdx.y; q < parts; q += 16) v += src[(size_t)q * m + col];
   }
   acc[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  if (threadIdx.y == 0 && col < m) {
+  grid_dependents_launch();
+  if (threadIdx.y == 0 && col < m && out) {
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < 16; ++q) sum += acc[q][threadIdx.x];
@@ -423,8 +428,7 @@ int chunks_per_group(int chunks, int G) { return (chunks + 32 * G - 1) / (32 * G
 template <typename T, int C, int E>
 cudaError_t run_fwd(const NormFwd& p, int G, cudaStream_t st) {
   const int warps = G < 4 ? 4 : G, rows = warps / G;
-  layernorm_kernel<T, C, E><<<(unsigned)((p.s + rows - 1) / rows), 32 * warps, 0, st>>>(p, G);
-  return cudaGetLastError();
+  return launch_chained(layernorm_kernel<T, C, E>, dim3((unsigned)((p.s + rows - 1) / rows)), dim3(32 * warps), 0, st, p, G);
 }
 
 template <typename T, int C>
@@ -446,8 +450,7 @@ template <typename T, int C, int E>
 cudaError_t run_bwd(NormBwd p, int G, int grid, cudaStream_t st) {
   const int warps = G < 8 ? 8 : G, groups = warps / G;
   const size_t smem = groups > 1 && p.part ? 2 * sizeof(float) * (size_t)p.m : 0;
-  layernorm_bwd_kernel<T, C, E><<<(unsigned)grid, 32 * warps, smem, st>>>(p, G);
-  return cudaGetLastError();
+  return launch_chained(layernorm_bwd_kernel<T, C, E>, dim3((unsigned)grid), dim3(32 * warps), smem, st, p, G);
 }
 
 template <typename T, int C>
@@ -473,8 +476,8 @@ cudaError_t bwd_for(const NormBwd& p, int* grid, const DeviceInfo& di, cudaStrea
 
 cudaError_t launch_sum_parts(const float* part, int parts, int stride_parts, int m, float* out0, float* out1,
                              cudaStream_t st) {
-  sum_parts_kernel<<<dim3((unsigned)((m + 31) / 32), out1 ? 2 : 1), dim3(32, 16), 0, st>>>(part, parts, stride_parts, m, out0, out1);
-  return cudaGetLastError();
+  return launch_chained(sum_parts_kernel, dim3((unsigned)((m + 31) / 32), out1 ? 2 : 1), dim3(32, 16), 0, st, part, parts,
+                        stride_parts, m, out0, out1);
 }
 
 cudaError_t launch_layernorm(const void* x, long long ldx, int s, int m, int dtype, const void* w, int w_dtype,
