@@ -1014,9 +1014,11 @@ moe_status moe_layernorm(int s, int m, moe_dtype dtype, const void* x, int64_t l
   int dev = 0;
   MOE_TRY(check_ptrs({{x, "x", false}, {weight, "weight", true}, {bias, "bias", true}, {y, "y", false},
                       {mean, "mean", true}, {rstd, "rstd", true}}, &dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
   const int wd = weight_dtype == MOE_F32 ? 0 : 1;
   cudaError_t err = moe::launch_layernorm(x, ldx, s, m, dtype == MOE_F32 ? 0 : 1, weight, wd, bias, wd, eps, y, mean,
-                                          rstd, static_cast<cudaStream_t>(stream));
+                                          rstd, *di, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "layernorm launch");
   g_launches[MOE_KERNEL_LAYERNORM]++;
   return MOE_OK;

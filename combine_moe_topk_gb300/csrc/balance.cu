@@ -41,6 +41,9 @@ struct Pieces {
   int* tokens;    // [slots]
 };
 
+// Row groups whose loads a warp keeps in flight: 16 values a lane.
+constexpr int unroll_of(int V, int NI) { return V * NI >= 8 ? 2 : 4; }
+
 struct BalanceFwd {
   const float* logits;
   const int32_t* idx;
@@ -104,6 +107,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 template <int V, int L, int NI>
 __global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
   constexpr int kRows = 32 / L;  // rows of a warp at once
+  constexpr int U = unroll_of(V, NI);
   __shared__ int s_count[kMaxExperts];
   __shared__ float s_p[kWarps][V * L * NI];
   __shared__ float s_z[kWarps];
@@ -130,55 +134,79 @@ __global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[i][v] = 0.f;
-    for (int t0 = r.x + warp * kRows; t0 < r.y; t0 += kWarps * kRows) {
-      const int t = t0 + sub;
-      const bool in = t < r.y;
-      const bool live = in && (!p.valid || __ldg(p.valid + t) != 0);
-      float f[NI][V], top = -CUDART_INF_F;
+    for (int t0 = r.x + warp * kRows * U; t0 < r.y; t0 += kWarps * kRows * U) {
+      // the loads of U row groups and of these tokens' ids travel together
+      float f[U][NI][V];
+      bool live[U];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int c = V * (col + L * i);
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * kRows + sub;
+        live[u] = t < r.y && (!p.valid || __ldg(p.valid + t) != 0);
+      }
 #pragma unroll
-        for (int v = 0; v < V; ++v) f[i][v] = -CUDART_INF_F;
-        if (live && c < p.e) load_cols<V>(p.logits + (size_t)t * p.e + c, f[i]);
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          if (!(f[i][v] < CUDART_INF_F)) bad = 1;  // NaN or +inf
-          if (f[i][v] == -FLT_MAX) f[i][v] = -CUDART_INF_F;  // a mask of the type's lowest value
-          top = fmaxf(top, f[i][v]);
+        for (int i = 0; i < NI; ++i) {
+          const int c = V * (col + L * i);
+#pragma unroll
+          for (int v = 0; v < V; ++v) f[u][i][v] = -CUDART_INF_F;
+          if (live[u] && c < p.e) load_cols<V>(p.logits + (size_t)(t0 + u * kRows + sub) * p.e + c, f[u][i]);
         }
       }
-      top = lanes_max<L>(top);
-      const float base = top == -CUDART_INF_F ? 0.f : top;  // a row of masked experts: every exp below is 0
-      float sum = 0.f;
+      const int n_ids = min(kRows * U, r.y - t0) * p.k;
+      for (int q0 = 0; q0 < n_ids; q0 += 4 * 32) {
+        int id[4], ok[4];
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          f[i][v] = expf(f[i][v] - base);
-          sum += f[i][v];
+        for (int w = 0; w < 4; ++w) {
+          const int q = q0 + 32 * w + lane;
+          id[w] = q < n_ids ? __ldg(p.idx + (size_t)t0 * p.k + q) : -1;
+          ok[w] = !p.valid || q >= n_ids ? 1 : __ldg(p.valid + t0 + q / p.k);
         }
-      sum = lanes_sum<L>(sum);
-      const bool some = live && top != -CUDART_INF_F;
-      const float inv = some ? 1.f / sum : 0.f;
-      if (some) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          if (ok[w] == 0) continue;
+          if ((unsigned)id[w] < (unsigned)p.e) atomicAdd(&s_count[id[w]], 1);
+          else if (id[w] != -1) bad |= 2;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float top = -CUDART_INF_F;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[i][v] = fmaf(f[i][v], inv, acc[i][v]);
+          for (int v = 0; v < V; ++v) {
+            if (!(f[u][i][v] < CUDART_INF_F)) bad |= 1;  // NaN or +inf
+            if (f[u][i][v] == -FLT_MAX) f[u][i][v] = -CUDART_INF_F;  // a mask of the type's lowest value
+            top = fmaxf(top, f[u][i][v]);
+          }
+        top = lanes_max<L>(top);
+        const float base = top == -CUDART_INF_F ? 0.f : top;  // a row of masked experts: every exp below is 0
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            f[u][i][v] = expf(f[u][i][v] - base);
+            sum += f[u][i][v];
+          }
+        sum = lanes_sum<L>(sum);
+        const bool some = live[u] && top != -CUDART_INF_F;
+        if (some) {
+          const float inv = 1.f / sum;
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[i][v] = fmaf(f[u][i][v], inv, acc[i][v]);
+        }
+        const int t = t0 + u * kRows + sub;
+        if (t < r.y && col == 0) {
+          const float lse = some ? base + logf(sum) : (live[u] ? -CUDART_INF_F : 0.f);
+          p.lse[t] = lse;
+          if (some) zsum = fmaf(lse, lse, zsum);
+          tokens += live[u] ? 1 : 0;
+        }
       }
-      if (in && col == 0) {
-        const float lse = some ? base + logf(sum) : (live ? -CUDART_INF_F : 0.f);
-        p.lse[t] = lse;
-        if (some) zsum = fmaf(lse, lse, zsum);
-        tokens += live ? 1 : 0;
-      }
-    }
-    for (long long q = (long long)r.x * p.k + threadIdx.x; q < (long long)r.y * p.k; q += kBlock) {
-      if (p.valid && __ldg(p.valid + q / p.k) == 0) continue;
-      const int x = __ldg(p.idx + q);
-      if ((unsigned)x < (unsigned)p.e) atomicAdd(&s_count[x], 1);
-      else if (x != -1) bad |= 2;
     }
     // the warp's row groups, then the block's warps, in a fixed order
 #pragma unroll
@@ -237,6 +265,8 @@ struct BalanceJoin {
   float* norm;    // [2] 1 / B', 1 / T
 };
 
+constexpr int kJoin = 1024, kJoinWarps = kJoin / 32;
+
 __device__ __forceinline__ float block_sum(float v, float* scratch) {
   v = lanes_sum<32>(v);
   __syncthreads();
@@ -244,15 +274,15 @@ __device__ __forceinline__ float block_sum(float v, float* scratch) {
   __syncthreads();
   float sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += scratch[w];
+  for (int w = 0; w < kJoinWarps; ++w) sum += scratch[w];
   return sum;
 }
 
-// One block per sequence and 32 columns: the pieces, 8 threads a column; the last block to finish adds the sequences' losses in order.
-__global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin p) {
-  __shared__ float s_f[8][32];
-  __shared__ int s_c[8][32];
-  __shared__ float scratch[kWarps];
+// One block per sequence and 32 columns: the pieces, 32 threads a column; the last block to finish adds the sequences' losses in order.
+__global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p) {
+  __shared__ float s_f[kJoinWarps][32];
+  __shared__ int s_c[kJoinWarps][32];
+  __shared__ float scratch[kJoinWarps];
   __shared__ int s_last;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int b = (int)(blockIdx.x / (unsigned)p.cols), block = (int)(blockIdx.x - (unsigned)b * p.cols);
@@ -266,15 +296,16 @@ __global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin 
   const int c0 = lo / p.chunk, c1 = lo < hi ? (hi - 1) / p.chunk + 1 : c0;  // the blocks that have a piece of it
   float sum = 0.f;
   int count = 0, tokens = 0;
-  for (int c = c0 + ty; c < c1; c += 8) {
-    const size_t slot = (size_t)c + b;
-    if (col < p.e) {
-      sum += __ldg(p.pc.psum + slot * p.e + col);
-      count += __ldg(p.pc.count + slot * p.e + col);
+  if (col < p.e) {
+#pragma unroll 4
+    for (int c = c0 + ty; c < c1; c += kJoinWarps) {
+      const size_t at = ((size_t)c + b) * p.e + col;
+      sum += __ldg(p.pc.psum + at);
+      count += __ldg(p.pc.count + at);
     }
   }
   float z = 0.f;
-  for (int c = c0 + threadIdx.x; c < c1; c += kBlock) {
+  for (int c = c0 + threadIdx.x; c < c1; c += kJoin) {
     tokens += __ldg(p.pc.tokens + (size_t)c + b);
     z += __ldg(p.pc.zsum + (size_t)c + b);
   }
@@ -282,18 +313,18 @@ __global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin 
   s_c[ty][tx] = count;
   z = block_sum(z, scratch);
   // token counts as floats would stop being exact at 2^24: summed as integers
-  __shared__ int s_tok[kWarps];
+  __shared__ int s_tok[kJoinWarps];
   tokens = __reduce_add_sync(0xffffffffu, tokens);
   if (tx == 0) s_tok[ty] = tokens;
   __syncthreads();
   tokens = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) tokens += s_tok[w];
+  for (int w = 0; w < kJoinWarps; ++w) tokens += s_tok[w];
   if (ty == 0) {
     sum = 0.f;
     count = 0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kJoinWarps; ++q) {
       sum += s_f[q][tx];
       count += s_c[q][tx];
     }
@@ -320,7 +351,7 @@ __global__ void __launch_bounds__(kBlock) balance_join_kernel(const BalanceJoin 
   if (!s_last) return;
   __threadfence();
   float loss = 0.f, zall = 0.f, live = 0.f, total = 0.f;
-  for (int q = threadIdx.x; q < p.B; q += kBlock) {
+  for (int q = threadIdx.x; q < p.B; q += kJoin) {
     for (int c = 0; c < p.cols; ++c) loss += __ldcg(p.part + (size_t)q * p.cols + c);
     zall += __ldcg(p.zpart + q);
     const int n = __ldcg(p.tpart + q);
@@ -373,7 +404,7 @@ __device__ __forceinline__ void copy_rows(const BalanceBwd& p, int lo, int hi) {
 
 template <int V, int L, int NI>
 __global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p) {
-  constexpr int kRows = 32 / L;
+  constexpr int kRows = 32 / L, U = unroll_of(V, NI);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
   const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
@@ -395,38 +426,52 @@ __global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p)
         const int j = V * (col + L * i) + v;
         c[i][v] = j < p.e ? wl * __ldg(p.coef + (size_t)b * p.e + j) : 0.f;
       }
-    for (int t0 = r.x + warp * kRows; t0 < r.y; t0 += kWarps * kRows) {
-      const int t = t0 + sub;
-      const bool in = t < r.y;
-      const bool live = in && (!p.valid || __ldg(p.valid + t) != 0);
-      const float lse = live ? __ldg(p.lse + t) : 0.f;
-      const bool some = live && lse != -CUDART_INF_F;  // a row of masked experts has no probabilities
-      float f[NI][V], g[NI][V], dot = 0.f;
+    for (int t0 = r.x + warp * kRows * U; t0 < r.y; t0 += kWarps * kRows * U) {
+      float f[U][NI][V], g[U][NI][V], lse[U];
+      bool some[U];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int q = V * (col + L * i);
-#pragma unroll
-        for (int v = 0; v < V; ++v) f[i][v] = -CUDART_INF_F, g[i][v] = 0.f;
-        if (some && q < p.e) load_cols<V>(p.logits + (size_t)t * p.e + q, f[i]);
-        if (p.add && in && q < p.e) load_add<V>(p.add + (size_t)t * p.e + q, g[i]);
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * kRows + sub;
+        const bool live = t < r.y && (!p.valid || __ldg(p.valid + t) != 0);
+        lse[u] = t < r.y ? __ldg(p.lse + t) : 0.f;
+        some[u] = live && lse[u] != -CUDART_INF_F;  // a row of masked experts has no probabilities
       }
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * kRows + sub;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          f[i][v] = expf(f[i][v] - lse);
-          dot = fmaf(c[i][v], f[i][v], dot);
+        for (int i = 0; i < NI; ++i) {
+          const int q = V * (col + L * i);
+#pragma unroll
+          for (int v = 0; v < V; ++v) f[u][i][v] = -CUDART_INF_F, g[u][i][v] = 0.f;
+          if (t < r.y && q < p.e) {
+            load_cols<V>(p.logits + (size_t)t * p.e + q, f[u][i]);
+            if (p.add) load_add<V>(p.add + (size_t)t * p.e + q, g[u][i]);
+          }
         }
-      dot = lanes_sum<L>(dot);
-      const float zt = wz * lse;
+      }
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int q = V * (col + L * i);
-        if (some) {
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u * kRows + sub;
+        float dot = 0.f;
 #pragma unroll
-          for (int v = 0; v < V; ++v) g[i][v] = fmaf(f[i][v], c[i][v] - dot + zt, g[i][v]);
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            f[u][i][v] = expf(f[u][i][v] - lse[u]);
+            dot = fmaf(c[i][v], f[u][i][v], dot);
+          }
+        dot = lanes_sum<L>(dot);
+        const float zt = wz * lse[u];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int q = V * (col + L * i);
+          if (some[u]) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[u][i][v] = fmaf(f[u][i][v], c[i][v] - dot + zt, g[u][i][v]);
+          }
+          if (t < r.y && q < p.e) store_cols<V>(p.dlogits + (size_t)t * p.e + q, g[u][i]);
         }
-        if (in && q < p.e) store_cols<V>(p.dlogits + (size_t)t * p.e + q, g[i]);
       }
     }
   }
@@ -510,7 +555,7 @@ cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_
   BalanceJoin j = {offsets, s, e, k, B, chunk, cols, pc, counts, mean_prob, coef,
                    reinterpret_cast<float*>(ws + q.part), reinterpret_cast<float*>(ws + q.zpart),
                    reinterpret_cast<int*>(ws + q.tpart), ticket, loss, norm};
-  return launch_chained(balance_join_kernel, dim3((unsigned)cols * (unsigned)B), dim3(kBlock), 0, st, j);
+  return launch_chained(balance_join_kernel, dim3((unsigned)cols * (unsigned)B), dim3(kJoin), 0, st, j);
 }
 
 cudaError_t launch_balance_bwd(const float* logits, const float* lse, const float* coef, const float* norm,

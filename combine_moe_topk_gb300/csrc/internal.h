@@ -163,7 +163,7 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
 // elements between rows of the inputs (outputs are contiguous).
 cudaError_t launch_layernorm(const void* x, long long ldx, int s, int m, int dtype, const void* w, int w_dtype,
                              const void* b, int b_dtype, float eps, void* y, float* mean, float* rstd,
-                             cudaStream_t st);
+                             const DeviceInfo& di, cudaStream_t st);
 
 // Partial rows of the weight gradients: at most this many blocks write one.
 inline int layernorm_bwd_parts(int s) { return s < 640 ? s : 640; }
