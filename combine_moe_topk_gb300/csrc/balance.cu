@@ -29,7 +29,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 512;
 constexpr int kWarps = kBlock / 32;
 constexpr int kMaxExperts = 256;
 
@@ -91,6 +91,13 @@ __device__ __forceinline__ void load_add(const float* p, float* f) {
   else f[0] = *p;
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
 #pragma unroll
@@ -105,7 +112,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 template <int V, int L, int NI>
-__global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
+__global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) {
   constexpr int kRows = 32 / L;  // rows of a warp at once
   constexpr int U = unroll_of(V, NI);
   __shared__ int s_count[kMaxExperts];
@@ -154,44 +161,36 @@ __global__ void __launch_bounds__(kBlock) balance_kernel(const BalanceFwd p) {
         }
       }
       const int n_ids = min(kRows * U, r.y - t0) * p.k;
-      for (int q0 = 0; q0 < n_ids; q0 += 4 * 32) {
-        int id[4], ok[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int q = q0 + 32 * w + lane;
-          id[w] = q < n_ids ? __ldg(p.idx + (size_t)t0 * p.k + q) : -1;
-          ok[w] = !p.valid || q >= n_ids ? 1 : __ldg(p.valid + t0 + q / p.k);
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          if (ok[w] == 0) continue;
-          if ((unsigned)id[w] < (unsigned)p.e) atomicAdd(&s_count[id[w]], 1);
-          else if (id[w] != -1) bad |= 2;
-        }
+#pragma unroll 2
+      for (int q = lane; q < n_ids; q += 32) {
+        const int id = __ldg(p.idx + (size_t)t0 * p.k + q);
+        if (p.valid && __ldg(p.valid + t0 + q / p.k) == 0) continue;
+        if ((unsigned)id < (unsigned)p.e) atomicAdd(&s_count[id], 1);
+        else if (id != -1) bad |= 2;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float top = -CUDART_INF_F;
+        float top = -FLT_MAX;  // a mask of the type's lowest value counts as -inf
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (!(f[u][i][v] < CUDART_INF_F)) bad |= 1;  // NaN or +inf
-            if (f[u][i][v] == -FLT_MAX) f[u][i][v] = -CUDART_INF_F;  // a mask of the type's lowest value
-            top = fmaxf(top, f[u][i][v]);
-          }
+          for (int v = 0; v < V; ++v) top = fmaxf(top, f[u][i][v]);
         top = lanes_max<L>(top);
-        const float base = top == -CUDART_INF_F ? 0.f : top;  // a row of masked experts: every exp below is 0
+        const float base = top == -FLT_MAX ? 0.f : top;  // a row of masked experts: every exp below is 0
+        // exp(l - base) as 2^(l log2 e - base log2 e): what the second product's
+        // rounding adds is the same for the whole row and cancels in p
+        const float shift = -base * kLog2e;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            f[u][i][v] = expf(f[u][i][v] - base);
+            f[u][i][v] = exp2_approx(fmaf(f[u][i][v], kLog2e, shift));
             sum += f[u][i][v];
           }
         sum = lanes_sum<L>(sum);
-        const bool some = live[u] && top != -CUDART_INF_F;
+        if (!(sum < CUDART_INF_F)) bad |= 1;  // a NaN or +inf makes it NaN
+        const bool some = live[u] && sum != 0.f;
         if (some) {
           const float inv = 1.f / sum;
 #pragma unroll
@@ -265,28 +264,20 @@ struct BalanceJoin {
   float* norm;    // [2] 1 / B', 1 / T
 };
 
-constexpr int kJoin = 1024, kJoinWarps = kJoin / 32;
+constexpr int kJoin = 1024;
 
-__device__ __forceinline__ float block_sum(float v, float* scratch) {
-  v = lanes_sum<32>(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) sum += scratch[w];
-  return sum;
-}
-
-// One block per sequence and 32 columns: the pieces, 32 threads a column; the last block to finish adds the sequences' losses in order.
+// One block per sequence and 32 columns: the pieces, 32 threads a column, ten
+// loads of each in flight, then a warp for each column; the last block to
+// finish adds the sequences' losses in a fixed order.
 __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p) {
-  __shared__ float s_f[kJoinWarps][32];
-  __shared__ int s_c[kJoinWarps][32];
-  __shared__ float scratch[kJoinWarps];
+  __shared__ float s_f[32][33];
+  __shared__ int s_c[32][33];
+  __shared__ float s_z[32], s_share[32];
+  __shared__ int s_t[32];
+  __shared__ float4 s_last_sums[32];
   __shared__ int s_last;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int b = (int)(blockIdx.x / (unsigned)p.cols), block = (int)(blockIdx.x - (unsigned)b * p.cols);
-  const int col = block * 32 + tx;
   grid_dependency_wait();
   int lo = 0, hi = p.s;
   if (p.offsets) {
@@ -294,48 +285,60 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
     hi = min(p.s, __ldg(p.offsets + b + 1));
   }
   const int c0 = lo / p.chunk, c1 = lo < hi ? (hi - 1) / p.chunk + 1 : c0;  // the blocks that have a piece of it
-  float sum = 0.f;
-  int count = 0, tokens = 0;
-  if (col < p.e) {
-#pragma unroll 4
-    for (int c = c0 + ty; c < c1; c += kJoinWarps) {
-      const size_t at = ((size_t)c + b) * p.e + col;
-      sum += __ldg(p.pc.psum + at);
-      count += __ldg(p.pc.count + at);
+  {
+    const int col = block * 32 + tx;
+    float sum = 0.f;
+    int count = 0;
+    if (col < p.e) {
+      for (int q = c0 + ty; q < c1; q += 320) {
+        float f[10];
+        int n[10];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          const size_t at = ((size_t)min(q + 32 * i, c1 - 1) + b) * p.e + col;
+          f[i] = q + 32 * i < c1 ? __ldg(p.pc.psum + at) : 0.f;
+          n[i] = q + 32 * i < c1 ? __ldg(p.pc.count + at) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          sum += f[i];
+          count += n[i];
+        }
+      }
+    }
+    float z = 0.f;
+    int tokens = 0;
+    for (int c = c0 + threadIdx.x; c < c1; c += kJoin) {
+      tokens += __ldg(p.pc.tokens + (size_t)c + b);
+      z += __ldg(p.pc.zsum + (size_t)c + b);
+    }
+    s_f[ty][tx] = sum;
+    s_c[ty][tx] = count;
+    z = lanes_sum<32>(z);
+    tokens = __reduce_add_sync(0xffffffffu, tokens);  // as integers: floats are exact to 2^24 only
+    if (tx == 0) {
+      s_z[ty] = z;
+      s_t[ty] = tokens;
     }
   }
-  float z = 0.f;
-  for (int c = c0 + threadIdx.x; c < c1; c += kJoin) {
-    tokens += __ldg(p.pc.tokens + (size_t)c + b);
-    z += __ldg(p.pc.zsum + (size_t)c + b);
-  }
-  s_f[ty][tx] = sum;
-  s_c[ty][tx] = count;
-  z = block_sum(z, scratch);
-  // token counts as floats would stop being exact at 2^24: summed as integers
-  __shared__ int s_tok[kJoinWarps];
-  tokens = __reduce_add_sync(0xffffffffu, tokens);
-  if (tx == 0) s_tok[ty] = tokens;
   __syncthreads();
-  tokens = 0;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) tokens += s_tok[w];
-  if (ty == 0) {
-    sum = 0.f;
-    count = 0;
-#pragma unroll
-    for (int q = 0; q < kJoinWarps; ++q) {
-      sum += s_f[q][tx];
-      count += s_c[q][tx];
-    }
-    const float inv_t = tokens > 0 ? 1.f / (float)tokens : 0.f;
-    const float P = sum * inv_t, f = (float)count * inv_t / (float)p.k;
+  const int tokens = __reduce_add_sync(0xffffffffu, s_t[tx]);
+  const int col = block * 32 + ty;  // this warp's column
+  const float sum = lanes_sum<32>(s_f[tx][ty]);
+  const int count = __reduce_add_sync(0xffffffffu, s_c[tx][ty]);
+  const float inv_t = tokens > 0 ? 1.f / (float)tokens : 0.f;
+  const float P = sum * inv_t, f = (float)count * inv_t / (float)p.k;
+  if (tx == 0) {
     if (col < p.e) {
       p.counts[(size_t)b * p.e + col] = count;
       p.mean_prob[(size_t)b * p.e + col] = P;
       p.coef[(size_t)b * p.e + col] = (float)p.e * f * inv_t;
     }
-    const float share = lanes_sum<32>(col < p.e ? (float)p.e * f * P : 0.f);
+    s_share[ty] = col < p.e ? (float)p.e * f * P : 0.f;
+  }
+  __syncthreads();
+  if (ty == 0) {
+    const float share = lanes_sum<32>(s_share[tx]), z = lanes_sum<32>(s_z[tx]);
     if (tx == 0) {
       p.part[(size_t)b * p.cols + block] = share;
       if (block == 0) {
@@ -350,24 +353,29 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  float loss = 0.f, zall = 0.f, live = 0.f, total = 0.f;
+  float4 all = make_float4(0.f, 0.f, 0.f, 0.f);  // loss, z, sequences with tokens, tokens
   for (int q = threadIdx.x; q < p.B; q += kJoin) {
-    for (int c = 0; c < p.cols; ++c) loss += __ldcg(p.part + (size_t)q * p.cols + c);
-    zall += __ldcg(p.zpart + q);
+    for (int c = 0; c < p.cols; ++c) all.x += __ldcg(p.part + (size_t)q * p.cols + c);
+    all.y += __ldcg(p.zpart + q);
     const int n = __ldcg(p.tpart + q);
-    live += n > 0 ? 1.f : 0.f;
-    total += (float)n;
+    all.z += n > 0 ? 1.f : 0.f;
+    all.w += (float)n;
   }
-  loss = block_sum(loss, scratch);
-  zall = block_sum(zall, scratch);
-  live = block_sum(live, scratch);
-  total = block_sum(total, scratch);
-  if (threadIdx.x == 0) {
-    const float per_seq = 1.f / fmaxf(live, 1.f), per_token = 1.f / fmaxf(total, 1.f);
-    p.loss[0] = loss * per_seq;
-    p.loss[1] = zall * per_token;
-    p.norm[0] = per_seq;
-    p.norm[1] = per_token;
+  auto sum4 = [](float4 v) {
+    return make_float4(lanes_sum<32>(v.x), lanes_sum<32>(v.y), lanes_sum<32>(v.z), lanes_sum<32>(v.w));
+  };
+  all = sum4(all);
+  if (tx == 0) s_last_sums[ty] = all;
+  __syncthreads();
+  if (ty == 0) {
+    all = sum4(s_last_sums[tx]);
+    if (tx == 0) {
+      const float per_seq = 1.f / fmaxf(all.z, 1.f), per_token = 1.f / fmaxf(all.w, 1.f);
+      p.loss[0] = all.x * per_seq;
+      p.loss[1] = all.y * per_token;
+      p.norm[0] = per_seq;
+      p.norm[1] = per_token;
+    }
   }
 }
 
@@ -403,7 +411,7 @@ __device__ __forceinline__ void copy_rows(const BalanceBwd& p, int lo, int hi) {
 }
 
 template <int V, int L, int NI>
-__global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p) {
+__global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd p) {
   constexpr int kRows = 32 / L, U = unroll_of(V, NI);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
@@ -458,7 +466,7 @@ __global__ void __launch_bounds__(kBlock) balance_bwd_kernel(const BalanceBwd p)
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            f[u][i][v] = expf(f[u][i][v] - lse[u]);
+            f[u][i][v] = exp2_approx((f[u][i][v] - lse[u]) * kLog2e);
             dot = fmaf(c[i][v], f[u][i][v], dot);
           }
         dot = lanes_sum<L>(dot);

@@ -174,7 +174,7 @@ cudaError_t launch_layernorm_bwd(const void* dy, long long lddy, const void* x, 
                                  const DeviceInfo& di, cudaStream_t st);
 
 // --- balance loss ------------------------------------------------------------
-constexpr int kBalanceBlocks = 608;  // most blocks of its kernels (four for each of 152 SMs)
+constexpr int kBalanceBlocks = 304;  // most blocks of its kernels (two for each of 152 SMs)
 size_t balance_workspace(int e, int B);
 // offsets == NULL: one sequence of all tokens (B = 1).
 cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_t* valid, const int32_t* offsets,

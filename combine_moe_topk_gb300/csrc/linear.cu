@@ -814,75 +814,166 @@ struct FewArgs {
   long long ldx, ldw;
   int s, K, N;
   Epi epi;
+  int32_t* status;
+  long long timeout_ns;
 };
 
-// Up to 16 rows of x (decoded tokens): bound by reading W once, so W goes from
-// memory straight into the registers of warp-level MMAs, 16 bytes a lane, with
-// kUnroll loads in flight, and nothing is staged or shared before the end.  A
-// block makes 8 NT columns of y, its eight warps take every eighth 32 of the
-// contracted axis.  The order of the terms is free, so lane c of a row's four
-// feeds its 8 consecutive elements to two MMAs as their k pairs, the same for
-// x and W.  The warps' sums are added in order through shared memory.
-template <int NT, bool kHigh>
-__global__ void __launch_bounds__(256) few_rows_kernel(const FewArgs p) {
-  constexpr int kUnroll = 8 / NT;
-  __shared__ float red[8][16][8 * NT + 1];
+// Up to 16 rows of x (decoded tokens): bound by reading W once.  One block an
+// SM takes N / gridDim consecutive columns of y, so every SM reads the same
+// share of W to within a row.  W comes through a deep ring in shared memory (a
+// stage: 8 rows x 2048 of the contracted axis, a bulk copy a row), which keeps
+// up to 190 KB an SM in flight from the first microsecond on; loads into
+// registers, 128 bytes a thread, had reached 2.9 TB/s at 4096 x 4096 (11.6 us).  The rows
+// of x take the same way, a stage or two before the chunk's W.
+//   warp 8          producer: lane r copies row r of a stage
+//   warps 0..7      every eighth 32 of the contracted axis, by warp-level MMA
+//                   (16 rows of x times 8 rows of W: 8 of 16 rows idle when
+//                   s <= 8, but the tensor cores wait for memory anyway)
+// The order of the terms is free, so lane c of a row's four feeds its 8
+// consecutive elements to two MMAs as their k pairs, the same for x and W.  The
+// warps' sums are added in order through shared memory every 32 columns.
+// A wait that runs out sets the status and everyone runs on without waiting,
+// so that the barriers stay matched.
+constexpr int kFewK = 2048;                    // of the contracted axis a stage
+constexpr int kFewRow = kFewK * 2 + 64;        // row pitch: 64 bytes more, free of bank conflicts
+constexpr int kFewStage = 8 * kFewRow;
+constexpr int kFewStages = 6;
+constexpr int kFewTiles = 4;                   // 8 columns each, between two joins
+constexpr int kFewSmem = kFewStages * kFewStage;
+
+template <bool kHigh>  // rows 8..15 exist
+__global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant__ FewArgs p) {
+  constexpr int kBlocks = kFewK / 32 / 8;  // 32-wide blocks of a stage and warp
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages];
+  __shared__ float red[8][kHigh ? 16 : 8][8 * kFewTiles + 1];
+  __shared__ int s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, c = lane & 3;
-  const int n0 = blockIdx.x * 8 * NT;
-  const bf16* w[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) w[t] = p.W + (long long)min(n0 + 8 * t + g, p.N - 1) * p.ldw + c * 8;
-  const bf16* x0 = p.x + (long long)g * p.ldx + c * 8;
-  const bf16* x1 = p.x + (long long)(g + 8) * p.ldx + c * 8;
-  const bool in0 = g < p.s, in1 = kHigh && g + 8 < p.s;
-  float acc[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
-  const int blocks = (p.K + 31) / 32;
-  grid_dependency_wait();
-  for (int kb0 = warp; kb0 < blocks; kb0 += 8 * kUnroll) {
-    uint4 wv[kUnroll][NT], xa[kUnroll], xb[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int k = (kb0 + 8 * i) * 32;
-      const bool in = k + c * 8 < p.K;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) wv[i][t] = in ? ld_stream(reinterpret_cast<const uint4*>(w[t] + k)) : make_uint4(0, 0, 0, 0);
-      xa[i] = in && in0 ? __ldg(reinterpret_cast<const uint4*>(x0 + k)) : make_uint4(0, 0, 0, 0);
-      xb[i] = in && in1 ? __ldg(reinterpret_cast<const uint4*>(x1 + k)) : make_uint4(0, 0, 0, 0);
+  if (threadIdx.x == 0) {
+    s_err = 0;
+    for (int i = 0; i < kFewStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 8);
     }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const uint32_t a0[4] = {xa[i].x, xb[i].x, xa[i].y, xb[i].y}, a1[4] = {xa[i].z, xb[i].z, xa[i].w, xb[i].w};
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        mma16816(acc[t], a0, wv[i][t].x, wv[i][t].y);
-        mma16816(acc[t], a1, wv[i][t].z, wv[i][t].w);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    red[warp][g][8 * t + 2 * c] = acc[t][0];
-    red[warp][g][8 * t + 2 * c + 1] = acc[t][1];
-    if (kHigh) {
-      red[warp][g + 8][8 * t + 2 * c] = acc[t][2];
-      red[warp][g + 8][8 * t + 2 * c + 1] = acc[t][3];
-    }
+    fence_barrier_init();
   }
   __syncthreads();
-  for (int o = threadIdx.x; o < p.s * 8 * NT; o += 256) {
-    const int row = o / (8 * NT), j = o - row * 8 * NT;
-    if (n0 + j >= p.N) continue;
-    float f = 0.f;
+  grid_dependency_wait();
+  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
+  const int f0 = (int)((long long)p.N * blockIdx.x / gridDim.x), f1 = (int)((long long)p.N * (blockIdx.x + 1) / gridDim.x);
+  const int chunks = (p.K + kFewK - 1) / kFewK;
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  auto advance = [&]() {
+    if (++stage == kFewStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
+  if (warp == 8) {
+    auto put = [&](const bf16* base, long long ld, int rows, int kc) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline));
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(rows * kc * 2));
+        __syncwarp();
+        if (lane < rows) bulk_g2s(ring + stage * kFewStage + lane * kFewRow, base + lane * ld, (uint32_t)kc * 2, &full[stage]);
+      }
+      advance();
+    };
+    for (int g0 = f0; g0 < f1; g0 += 8 * kFewTiles) {
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int k0 = ch * kFewK, kc = min(kFewK, p.K - k0);
+        put(p.x + k0, p.ldx, min(8, p.s), kc);
+        if (kHigh) put(p.x + 8 * p.ldx + k0, p.ldx, p.s - 8, kc);
+        for (int t = g0; t < min(f1, g0 + 8 * kFewTiles); t += 8) put(p.W + (long long)t * p.ldw + k0, p.ldw, min(8, f1 - t), kc);
+      }
+    }
+    // the last copies are waited for by the consumers, which have read all stages
+  } else {
+    const int g = lane >> 2, c = lane & 3;
+    auto wait_full = [&]() {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, deadline));
+    };
+    auto release = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      advance();
+    };
+    // this lane's 16 bytes of block i of its warp: zeros past the row's end
+    auto frag = [&](int i, int kc) {
+      const int k = (warp + 8 * i) * 32 + c * 8;
+      return k < kc ? *reinterpret_cast<const uint4*>(ring + stage * kFewStage + g * kFewRow + k * 2) : make_uint4(0, 0, 0, 0);
+    };
+    for (int g0 = f0; g0 < f1; g0 += 8 * kFewTiles) {
+      float acc[kFewTiles][4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f += red[q][row][j];
-    finish1(p.epi, row, n0 + j, p.N, f);
+      for (int t = 0; t < kFewTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+      for (int ch = 0; ch < chunks; ++ch) {
+        const int kc = min(kFewK, p.K - ch * kFewK);
+        uint4 xa[kBlocks], xb[kBlocks];
+        wait_full();
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) xa[i] = frag(i, kc);
+        release();
+        if (kHigh) {
+          wait_full();
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i) xb[i] = frag(i, kc);
+          release();
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBlocks; ++i) xb[i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < kFewTiles; ++t) {
+          if (g0 + 8 * t < f1) {
+            wait_full();
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+              const uint4 w = frag(i, kc);
+              const uint32_t a0[4] = {xa[i].x, xb[i].x, xa[i].y, xb[i].y}, a1[4] = {xa[i].z, xb[i].z, xa[i].w, xb[i].w};
+              mma16816(acc[t], a0, w.x, w.y);
+              mma16816(acc[t], a1, w.z, w.w);
+            }
+            release();
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kFewTiles; ++t) {
+        red[warp][g][8 * t + 2 * c] = acc[t][0];
+        red[warp][g][8 * t + 2 * c + 1] = acc[t][1];
+        if constexpr (kHigh) {
+          red[warp][g + 8][8 * t + 2 * c] = acc[t][2];
+          red[warp][g + 8][8 * t + 2 * c + 1] = acc[t][3];
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const int cols = min(8 * kFewTiles, f1 - g0);
+      for (int o = threadIdx.x; o < p.s * 8 * kFewTiles; o += 256) {
+        const int row = o / (8 * kFewTiles), j = o - row * 8 * kFewTiles;
+        if (j < cols) {
+          float f = 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) f += red[q][row][j];
+          finish1(p.epi, row, g0 + j, p.N, f);
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the sums are rewritten
+    }
   }
+  if (!ok && lane == 0) atomicOr(&s_err, 1);
   grid_dependents_launch();
+  __syncthreads();
+  if (s_err) {  // let copies in flight land before shared memory goes
+    const uint64_t until = globaltimer_ns() + 200000;
+    while (globaltimer_ns() < until) {
+    }
+    if (threadIdx.x == 0) raise_status(p.status, MOE_DEV_TIMEOUT);
+  }
 }
 
 // ---- dz and the bias' gradient --------------------------------------------------
@@ -1106,10 +1197,16 @@ size_t part_bytes(int M, int N, int K) {
   return a > b ? a : b;
 }
 
-cudaError_t few_rows(const LinearArgs& a, const Epi& e, cudaStream_t st) {
-  FewArgs p = {static_cast<const bf16*>(a.x), static_cast<const bf16*>(a.W), a.ldx, a.ldw, a.s, a.K, a.N, e};
-  const unsigned grid = (unsigned)((a.N + 7) / 8);
-  return launch_chained(a.s <= 8 ? few_rows_kernel<1, false> : few_rows_kernel<1, true>, dim3(grid), dim3(256), 0, st, p);
+template <bool kHigh>
+cudaError_t few_rows(const LinearArgs& a, const Epi& e, const DeviceInfo& di, cudaStream_t st) {
+  static OncePerDevice once;
+  cudaError_t err = once.run([] {
+    return cudaFuncSetAttribute(few_rows_kernel<kHigh>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  });
+  if (err != cudaSuccess) return err;
+  FewArgs p = {static_cast<const bf16*>(a.x), static_cast<const bf16*>(a.W), a.ldx, a.ldw, a.s, a.K, a.N, e, a.status,
+               2000000000LL};
+  return launch_chained(few_rows_kernel<kHigh>, dim3((unsigned)(a.N < di.sms ? a.N : di.sms)), dim3(288), kFewSmem, st, p);
 }
 
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
@@ -1170,7 +1267,7 @@ cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_
   e.out_f32 = a.out_f32;
   e.bias_f32 = a.bias_f32;
   e.res_f32 = a.res_f32;
-  if (a.s <= kFewRows) return few_rows(a, e, st);
+  if (a.s <= kFewRows) return a.s > 8 ? few_rows<true>(a, e, di, st) : few_rows<false>(a, e, di, st);
   return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.workspace, a.status, di, st);
 }
 
