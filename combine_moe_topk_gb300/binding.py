@@ -41,7 +41,7 @@ EXPORTS = [
     "moe_dispatch_grouped_gemm", "moe_combine_gate_bwd", "moe_layout_create", "moe_layout_rebuild",
     "moe_topk_gate_layout", "moe_ep_pack", "moe_ep_dispatch", "moe_ep_combine", "moe_ep_unpack_dgate",
     "moe_layernorm", "moe_layernorm_bwd", "moe_layernorm_bwd_workspace", "moe_balance_loss", "moe_balance_loss_bwd",
-    "moe_balance_loss_workspace", "moe_linear", "moe_linear_workspace", "moe_linear_bwd", "moe_linear_bwd_workspace",
+    "moe_balance_loss_workspace", "moe_linear", "moe_linear_bwd", "moe_linear_bwd_workspace",
 ]
 
 
@@ -122,20 +122,16 @@ def lib() -> ctypes.CDLL:
             "moe_layernorm_bwd": [I, I, I, P, I64, P, I64, I, P, P, P, P, I64, P, P, P, P, Z, P],
             "moe_balance_loss": [P, P, P, P, I, I, I, I, P, P, P, P, P, P, P, Z, P, P],
             "moe_balance_loss_bwd": [P] * 8 + [I, I, I, P, P],
-            "moe_linear": [ctypes.POINTER(LinearDesc)] + [P] * 7 + [Z, P, P],
+            "moe_linear": [ctypes.POINTER(LinearDesc)] + [P] * 8,
             "moe_linear_bwd": [ctypes.POINTER(LinearBwdDesc)] + [P] * 8 + [Z, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = I
-        for name in ("moe_layernorm_bwd_workspace", "moe_balance_loss_workspace"):
+        for name in ("moe_layernorm_bwd_workspace", "moe_balance_loss_workspace", "moe_linear_bwd_workspace"):
             f = getattr(L, name)
             f.argtypes = [I, I]
-            f.restype = Z
-        for name in ("moe_linear_workspace", "moe_linear_bwd_workspace"):
-            f = getattr(L, name)
-            f.argtypes = [I, I, I]
             f.restype = Z
         L.moe_capacity.argtypes = [ctypes.c_double, I, I, I]
         L.moe_capacity.restype = I
@@ -779,16 +775,12 @@ def moe_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     elif y.shape != (s, N) or (out_dtype is not None and y.dtype != out_dtype):
         raise MoEError(1, "moe_linear", "output shape or dtype")
     z = torch.empty(s, N, dtype=torch.bfloat16, device=dev) if save_z else None
-    L = lib()
-    nbytes = L.moe_linear_workspace(s, K, N)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
     pres, ldres = _rows_ptr(residual)
     d = LinearDesc(s, K, N, ACT[act], _DTYPE.get(y.dtype, -1), 0 if bias is None else _DTYPE.get(bias.dtype, -1),
                    0 if residual is None else _DTYPE.get(residual.dtype, -1), ldx, ldw, ldres)
-    rc = L.moe_linear(d, px, pw, _addr(bias), pres, _addr(y), _addr(z), _addr(ws), nbytes, _addr(device_status),
-                      _raw_stream(x))
+    rc = lib().moe_linear(d, px, pw, _addr(bias), pres, _addr(y), _addr(z), _addr(device_status), _raw_stream(x))
     if rc:
         _check(rc, "moe_linear")
     return (y, z) if save_z else y
@@ -813,7 +805,7 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     dW = torch.empty(N, K, dtype=dw_dtype, device=dev) if need_dw else None
     db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
     L = lib()
-    nbytes = L.moe_linear_bwd_workspace(s, K, N)
+    nbytes = L.moe_linear_bwd_workspace(s, N)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)

@@ -1127,14 +1127,8 @@ moe_status check_status_ptr(const int32_t* status) {
 
 }  // namespace
 
-size_t moe_linear_workspace(int s, int K, int N) {
-  if (s < 1 || K < 1 || N < 1) return 0;
-  return moe::linear_workspace(s, K, N);
-}
-
 moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* W, const void* bias,
-                      const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
-                      int32_t* device_status, void* stream) {
+                      const void* residual, void* y, void* z, int32_t* device_status, void* stream) {
   if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
   MOE_TRY(check_linear(d->s, d->K, d->N, d->act, d->ldx, d->ldw, true, true));
   MOE_TRY(check_dtype((moe_dtype)d->out_dtype, "out_dtype"));
@@ -1145,21 +1139,20 @@ moe_status moe_linear(const moe_linear_desc* d, const void* x, const void* W, co
   }
   MOE_TRY(check_status_ptr(device_status));
   if (d->s == 0) return MOE_OK;
-  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_workspace(d->s, d->K, d->N)));
   int dev = 0;
   MOE_TRY(check_ptrs({{x, "x", false}, {W, "W", false}, {bias, "bias", true}, {residual, "residual", true},
-                      {y, "y", false}, {z, "z", true}, {workspace, "workspace", true}}, &dev));
+                      {y, "y", false}, {z, "z", true}}, &dev));
   MOE_TRY(check_device_ptr(device_status, "device_status", dev));
   const moe::DeviceInfo* di = nullptr;
   MOE_TRY(device_state(dev, &di));
-  moe::LinearArgs a = {x, W, bias, residual, y, z, workspace, device_status, d->ldx, d->ldw, d->ldres, d->s, d->K, d->N,
+  moe::LinearArgs a = {x, W, bias, residual, y, z, device_status, d->ldx, d->ldw, d->ldres, d->s, d->K, d->N,
                        d->act, d->out_dtype == MOE_F32, d->bias_dtype == MOE_F32, d->residual_dtype == MOE_F32};
   return gemm_result(moe::launch_linear(a, *di, static_cast<cudaStream_t>(stream)), "linear launch", MOE_KERNEL_LINEAR);
 }
 
-size_t moe_linear_bwd_workspace(int s, int K, int N) {
-  if (s < 1 || K < 1 || N < 1) return 0;
-  return moe::linear_bwd_workspace(s, K, N);
+size_t moe_linear_bwd_workspace(int s, int N) {
+  if (s < 1 || N < 1) return 0;
+  return moe::linear_bwd_workspace(s, N);
 }
 
 moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const void* x, const void* W,
@@ -1176,7 +1169,7 @@ moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const vo
   MOE_TRY(check_status_ptr(device_status));
   if (!dx && !dW && !db) return MOE_OK;
   if (none && !dW && !db) return MOE_OK;
-  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_bwd_workspace(d->s, d->K, d->N)));
+  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_bwd_workspace(d->s, d->N)));
   int dev = 0;
   MOE_TRY(check_ptrs({{dy, "dy", none}, {x, "x", none || !dW}, {W, "W", none || !dx}, {z, "z", none || !need_z},
                       {dx, "dx", true}, {dW, "dW", true}, {db, "db", true}, {workspace, "workspace", none}}, &dev));

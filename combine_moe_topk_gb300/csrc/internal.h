@@ -193,12 +193,10 @@ cudaError_t launch_sum_parts(const float* part, int parts, int stride_parts, int
 struct LinearArgs {
   const void *x, *W, *bias, *res;  // bf16 [s][ldx], bf16 [N][ldw], [N], [s][ldres]
   void *y, *z;                     // [s][N]; z bf16 [s][N] or NULL
-  void* workspace;
   int32_t* status;
   long long ldx, ldw, ldres;
   int s, K, N, act, out_f32, bias_f32, res_f32;
 };
-size_t linear_workspace(int s, int K, int N);
 cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 struct LinearBwdArgs {
@@ -210,7 +208,7 @@ struct LinearBwdArgs {
   long long lddy, ldx, ldw, ldz;
   int s, K, N, act, dy_f32, dx_f32, dw_f32;
 };
-size_t linear_bwd_workspace(int s, int K, int N);
+size_t linear_bwd_workspace(int s, int N);
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace moe

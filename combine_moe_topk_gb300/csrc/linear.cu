@@ -126,9 +126,7 @@ struct Epi {
   bf16* z;          // the value before the activation, or NULL
   const void* bias;
   const void* res;
-  float* part;      // split contraction: fp32 partial tiles [splits][M][ldpart], else NULL
   long long ldres;
-  int ldpart;
   int act, out_f32, bias_f32, res_f32;
   int wide;         // N and the residual's stride are multiples of 8: rows of 16-byte pieces
 };
@@ -192,7 +190,7 @@ __device__ __forceinline__ void finish1(const Epi& e, long long row, int col, in
 
 struct GemmArgs {
   int M, N, K;
-  int tiles_m, tiles_n, splits, blocks_per_split, kblocks;  // K blocks of 128
+  int tiles_m, tiles_n, splits, per_split, kblocks;  // K blocks of 128
   Epi epi;
   int32_t* status;
   long long timeout_ns;
@@ -213,6 +211,8 @@ struct Shape {
   static constexpr int kStages = (192 * 1024) / kStage;  // 3 at 64 KB a stage, 4 at 48 KB
   static constexpr int kSmem = kStages * kStage + kEpiBytes + 1024;
   static constexpr int kTmemCols = 2 * BN;
+  static constexpr int kPartRow = BN * 4 + 16;  // pitch of a split tile's fp32 rows, over the ring
+  static_assert(128 * kPartRow <= kStages * kStage, "a part fits in the ring");
 };
 
 // Matrix descriptor of a tile in shared memory, 128-byte swizzle, base on 1024
@@ -399,30 +399,17 @@ __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtenso
   else put_bf16(b, tmY, f, n0, r0, lane);
 }
 
-// The same block as fp32 through the staging tile (16-byte pieces
-// XOR-swizzled by the row), then read along rows: partial products of a split
-// contraction (four lanes a row), or, where rows are not of 16 bytes and TMA
-// cannot write them, each lane a column walking down the rows.
-__device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* stage, const uint32_t (&v)[32], int r0,
-                                            int n0, int M, int N, int lane) {
+// The same block where rows are not of 16 bytes, so that TMA cannot write
+// them: as fp32 through the staging tile (16-byte pieces XOR-swizzled by the
+// row), then each lane a column, walking down the rows.
+__device__ __forceinline__ void finish_ragged(const Epi& e, uint8_t* stage, const uint32_t (&v)[32], int r0, int n0,
+                                              int M, int N, int lane) {
 #pragma unroll
   for (int q = 0; q < 8; ++q)
     *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
         make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
   __syncwarp();
-  if (part) {
-    const int sub = lane >> 2, c8 = (lane & 3) * 8, col = n0 + c8;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 8 * i + sub, row = r0 + r;
-      if (row < M && col < N) {
-        uint4* o = reinterpret_cast<uint4*>(part + (size_t)row * e.ldpart + col);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          o[h] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((c8 / 4 + h) ^ (r & 7)) << 4));
-      }
-    }
-  } else if (n0 + lane < N) {
+  if (n0 + lane < N) {
     const int col = n0 + lane, rows = min(32, M - r0);
     const float bias = e.bias ? load_any(e.bias, e.bias_f32, col) : 0.f;
     float res[32];
@@ -473,27 +460,40 @@ __device__ __forceinline__ void store_chunk(const Epi& e, float* part, uint8_t* 
 }
 
 struct Unit {
-  int m0, n0, split, kb0, kb1;
+  int m0, n0, kb0, kb1;
 };
 
 // Units run over tiles in bands of 8 rows of tiles (the m index fastest), so
-// that the tiles in flight share operands in L2; splits outermost.
+// that the tiles in flight share operands in L2.
 template <int CG, int BN>
-__device__ __forceinline__ Unit unit_of(int u, const GemmArgs& p) {
+__device__ __forceinline__ Unit unit_of(int u, int split, const GemmArgs& p) {
   constexpr int kBand = 8;
-  const int tiles = p.tiles_m * p.tiles_n;
   Unit t;
-  t.split = u / tiles;
-  const int i = u - t.split * tiles;
-  const int band = i / (kBand * p.tiles_n);
+  const int band = u / (kBand * p.tiles_n);
   const int rows = min(kBand, p.tiles_m - band * kBand);
-  const int r = i - band * kBand * p.tiles_n;
+  const int r = u - band * kBand * p.tiles_n;
   const int n = r / rows;
   t.m0 = (band * kBand + r - n * rows) * 128 * CG;
   t.n0 = n * BN;
-  t.kb0 = t.split * p.blocks_per_split;
-  t.kb1 = min(p.kblocks, t.kb0 + p.blocks_per_split);
+  t.kb0 = split * p.per_split;
+  t.kb1 = min(p.kblocks, t.kb0 + p.per_split);
   return t;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// The cache lines of the residual that this lane's row of a tile will need.
+__device__ __forceinline__ void prefetch_residual(const Epi& e, int row, int n0, int cols, int M, int N) {
+  if (!e.res || row >= M) return;
+  const int size = e.res_f32 ? 4 : 2, n = min(cols, N - n0);
+  const char* at = static_cast<const char*>(e.res) + ((long long)row * e.ldres + n0) * size;
+  for (int b = 0; b < n * size; b += 128) prefetch_l2(at + b);
+}
+
+__device__ __forceinline__ uint4 ld_cluster(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
 }
 
 // kExact (fp32 outputs): the tensor cores' accumulator drops the bits below
@@ -502,7 +502,14 @@ __device__ __forceinline__ Unit unit_of(int u, const GemmArgs& p) {
 // every kExactBlocks K blocks, and the epilogue adds these up in registers.
 constexpr int kExactBlocks = 4;
 
-template <int CG, int BN, bool AT, bool BT, bool kExact>
+// kSplit (CG = 1): where tiles are too few to fill the machine, a cluster of
+// 2, 4 or 8 CTAs shares one, each with its part of the contracted axis.  They
+// leave their fp32 sums in their shared memory, and each finishes an equal
+// share of the tile's rows, adding the parts in order through distributed
+// shared memory.  (Partial products in global memory and a second kernel to add
+// them took the same time on the device, within 10 % either way, but another
+// launch and a workspace.)
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
@@ -516,10 +523,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  static_assert(!kSplit || CG == 1, "a split tile belongs to single CTAs");
+  const int split = kSplit ? (int)cluster_ctarank() : 0;
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
 
   if (threadIdx.x == 0) {
     s_err = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmA)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmB)) : "memory");
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -553,8 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = tmem_base;
 
-  const int units = p.tiles_m * p.tiles_n * p.splits;
-  const int worker = blockIdx.x / CG, workers = gridDim.x / CG;
+  const int units = p.tiles_m * p.tiles_n;
+  const int share = kSplit ? p.splits : CG;  // CTAs of a worker
+  const int worker = blockIdx.x / share, workers = gridDim.x / share;
 
   if (warp == 0 && lane == 0) {
     // ---- TMA producer ------------------------------------------------------
@@ -562,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, p);
+      const Unit t = unit_of<CG, BN>(u, split, p);
       const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + S::kRowsB * (int)rank;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) {
@@ -612,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, tphase[2] = {0u, 0u};
     bool ok = true;
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, p);
+      const Unit t = unit_of<CG, BN>(u, split, p);
       for (int kb0 = t.kb0; kb0 < t.kb1 && ok;) {
         const int kb1 = kExact ? min(t.kb1, kb0 + kExactBlocks) : t.kb1;
         if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
@@ -668,7 +680,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
     Bulk bulk = {stage_buf, 0};
-    const bool staged = p.epi.part || !p.epi.wide;  // see store_chunk
     // this warp's reads of the accumulator are done: the next product may have it
     auto release = [&]() {
       tc_fence_before();
@@ -679,9 +690,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, p);
+      const Unit t = unit_of<CG, BN>(u, split, p);
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew, n0 = t.n0 + half * (BN / 2);
-      float* part = p.epi.part ? p.epi.part + (size_t)t.split * p.M * p.epi.ldpart : nullptr;
+      if constexpr (kSplit) {  // for the rows that this CTA will finish
+        const int rows = 128 / p.splits, i = threadIdx.x - 128;
+        if (i < rows) prefetch_residual(p.epi, t.m0 + split * rows + i, t.n0, BN, p.M, p.N);
+      } else {
+        prefetch_residual(p.epi, r0 + lane, n0, BN / 2, p.M, p.N);
+      }
+      // a block of 32 columns on its way out, or into this CTA's part of a split tile
+      auto emit = [&](const uint32_t (&v)[32], const Raw32& res, int c) {
+        if constexpr (kSplit) {
+          uint8_t* row = smem + (32 * ew + lane) * S::kPartRow + (half * (BN / 2) + 32 * c) * 4;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            reinterpret_cast<uint4*>(row)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else if (p.epi.wide) {
+          finish_bulk(p.epi, bulk, &tmY, &tmZ, v, res, r0, n0 + 32 * c, p.M, p.N, lane);
+        } else {
+          finish_ragged(p.epi, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
+        }
+      };
+      auto residual = [&](Raw32& res, int c) {
+        if (!kSplit && p.epi.wide) load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
+      };
       auto lanes_of = [&]() { return tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2)); };
       if constexpr (kExact) {
         uint32_t sum[kChunks][32];
@@ -709,13 +741,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (staged) {
-            store_chunk(p.epi, part, stage_buf, sum[c], r0, n0 + 32 * c, p.M, p.N, lane);
-          } else {
-            Raw32 res;
-            load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
-            finish_bulk(p.epi, bulk, &tmY, &tmZ, sum[c], res, r0, n0 + 32 * c, p.M, p.N, lane);
-          }
+          Raw32 res;
+          residual(res, c);
+          emit(sum[c], res, c);
         }
       } else {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
@@ -727,12 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < kChunks; ++c) {
           Raw32 res;
-          if (!staged) load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
+          residual(res, c);
           uint32_t v[32];
           tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
           if (c == kChunks - 1) release();
-          if (staged) store_chunk(p.epi, part, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
-          else finish_bulk(p.epi, bulk, &tmY, &tmZ, v, res, r0, n0 + 32 * c, p.M, p.N, lane);
+          emit(v, res, c);
         }
         acc ^= 1;
       }
@@ -749,7 +776,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (globaltimer_ns() < until) {
     }
   }
-  if constexpr (CG == 2) cluster_sync_all();
+  if constexpr (kSplit) {
+    cluster_sync_all();  // every part is in its CTA's shared memory
+    const Unit t = unit_of<CG, BN>(worker, split, p);
+    const int rows = 128 / p.splits, groups = BN / 8;
+    const uint32_t base = smem_addr(smem);
+    for (int q = threadIdx.x; q < rows * groups; q += kThreads) {
+      const int r = split * rows + q / groups, col = t.n0 + (q % groups) * 8, row = t.m0 + r;
+      if (row >= p.M || col >= p.N) continue;
+      float f[8], bias[8];
+      if (p.epi.wide) load_bias8(p.epi, col, p.N, bias);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      const uint32_t at = base + r * S::kPartRow + (col - t.n0) * 4;
+      for (int sp = 0; sp < p.splits; sp += 2) {  // an even number; both loads in flight
+        const uint32_t from0 = mapa_shared(at, sp), from1 = mapa_shared(at, sp + 1);
+        const uint4 v[4] = {ld_cluster(from0), ld_cluster(from0 + 16), ld_cluster(from1), ld_cluster(from1 + 16)};
+        float g[16];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) Vec<float>::to_float(v[h], g + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f[j] + g[j] + g[8 + j];
+      }
+      if (p.epi.wide) {
+        finish8(p.epi, row, col, p.N, f, bias);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < p.N) finish1(p.epi, row, col + j, p.N, f[j]);
+      }
+    }
+  }
+  if constexpr (CG == 2 || kSplit) cluster_sync_all();
   tc_fence_after();
   if (warp == 2) {
     if constexpr (CG == 2)
@@ -758,43 +816,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(S::kTmemCols) : "memory");
   }
   if (threadIdx.x == 0 && s_err) raise_status(p.status, MOE_DEV_TIMEOUT);
-}
-
-// Adds the partial products of a split contraction in order and finishes them.
-__global__ void __launch_bounds__(256) gemm_join_kernel(const Epi e, int M, int N, int splits) {
-  const size_t step = (size_t)M * e.ldpart;
-  grid_dependency_wait();
-  if (e.wide) {
-    const int per_row = N / 8;
-    const long long all = (long long)M * per_row;
-    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
-      const long long row = q / per_row;
-      const int col = (int)(q - row * per_row) * 8;
-      float f[8], bias[8];
-      load_bias8(e, col, N, bias);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      const float* src = e.part + row * e.ldpart + col;
-      for (int sp = 0; sp < splits; ++sp) {
-        float g[8];
-        load8(src + sp * step, 1, 0, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += g[j];
-      }
-      finish8(e, row, col, N, f, bias);
-    }
-  } else {
-    const long long all = (long long)M * N;
-    for (long long q = (long long)blockIdx.x * 256 + threadIdx.x; q < all; q += (long long)gridDim.x * 256) {
-      const long long row = q / N;
-      const int col = (int)(q - row * N);
-      const float* src = e.part + row * e.ldpart + col;
-      float f = 0.f;
-      for (int sp = 0; sp < splits; ++sp) f += __ldg(src + sp * step);
-      finish1(e, row, col, N, f);
-    }
-  }
-  grid_dependents_launch();
 }
 
 // ---- few rows -------------------------------------------------------------------
@@ -1086,22 +1107,21 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
 // One product's plan.  kind: index into the four tile shapes.
 struct Plan {
   int kind, tiles_m, tiles_n, splits, per_split, kblocks;
-  size_t part_bytes;
 };
 constexpr int kKinds = 4;
 constexpr int kKindCG[kKinds] = {2, 2, 1, 1};
 constexpr int kKindBN[kKinds] = {256, 128, 128, 64};
-constexpr int kPlanSms = 152;  // plans (and workspaces) are made for a whole GB300
+constexpr int kPlanSms = 152;  // plans are made for a whole GB300
 
 Plan plan_gemm(int M, int N, int K, bool exact) {
   // relative time of a K block on one tile of each shape
   const double cost[kKinds] = {1.0, 0.6, 0.6, 0.42};
+  // clusters of 2, 4 and 8 CTAs that are surely resident at once
+  const int clusters[4] = {0, 72, 34, 16};
   Plan best = {};
   double best_t = 0;
   const int kblocks = (K + 127) / 128;
-  bool first = true;
-  for (int k = 0; k < kKinds; ++k) {
-    if (exact && k != 1 && k != 3) continue;  // its running sums need registers: the narrower tiles
+  for (int k = exact ? 1 : 0; k < kKinds; ++k) {  // exact: its running sums need registers, so not the widest
     Plan q;
     q.kind = k;
     q.kblocks = kblocks;
@@ -1109,39 +1129,38 @@ Plan plan_gemm(int M, int N, int K, bool exact) {
     q.tiles_n = (N + kKindBN[k] - 1) / kKindBN[k];
     const long long tiles = (long long)q.tiles_m * q.tiles_n;
     const int workers = kPlanSms / kKindCG[k];
-    // a contraction is split only where one wave does not fill the machine,
-    // and keeps at least four K blocks (512 terms) a part
-    int splits = 1;
-    if (tiles * 2 <= workers) splits = (int)(workers / tiles);
-    if (splits > kblocks / 4) splits = kblocks / 4;
-    if (splits < 1) splits = 1;
-    q.per_split = (kblocks + splits - 1) / splits;
-    q.splits = (kblocks + q.per_split - 1) / q.per_split;
-    const long long waves = (tiles * q.splits + workers - 1) / workers;
-    const double t = (double)waves * (q.per_split * cost[k] + 3.0) + (q.splits > 1 ? 12.0 : 0.0);
-    q.part_bytes = q.splits > 1 ? (size_t)q.splits * M * ((N + 7) / 8 * 8) * 4 : 0;
-    if (first || t < best_t) {
-      first = false;
-      best = q;
-      best_t = t;
+    for (int sh = 0; sh < 4; ++sh) {
+      const int S = 1 << sh;
+      // a split part keeps at least two K blocks (256 terms)
+      if (S > 1 && (kKindCG[k] == 2 || tiles > clusters[sh] || kblocks < 2 * S)) break;
+      q.per_split = (kblocks + S - 1) / S;
+      if ((S - 1) * q.per_split >= kblocks) continue;  // the last part would be empty
+      q.splits = S;
+      const long long waves = S > 1 ? 1 : (tiles + workers - 1) / workers;
+      const double t = (double)waves * (q.per_split * cost[k] + 3.0) + (S > 1 ? 2.0 : 0.0);
+      if (best.kblocks == 0 || t < best_t) {
+        best = q;
+        best_t = t;
+      }
     }
   }
   return best;
 }
 
-template <int CG, int BN, bool AT, bool BT, bool kExact>
-cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit>
+cudaError_t run_one(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
   typedef Shape<CG, BN> S;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (err != cudaSuccess) return err;
+  const long long units = (long long)p.tiles_m * p.tiles_n;
   long long workers = di.sms / CG;
-  const long long units = (long long)p.tiles_m * p.tiles_n * p.splits;
-  if (units < workers) workers = units;
+  if (kSplit || units < workers) workers = units;
+  const unsigned cluster = kSplit ? (unsigned)p.splits : CG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(workers * CG));
+  cfg.gridDim = dim3((unsigned)workers * cluster);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
@@ -1149,52 +1168,50 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const Devi
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact>, maps[0], maps[1], maps[2], maps[3], p);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact, kSplit>, maps[0], maps[1], maps[2], maps[3], p);
+}
+
+template <int CG, int BN, bool AT, bool BT, bool kExact>
+cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
+  if constexpr (CG == 1) {
+    if (p.splits > 1) return run_one<CG, BN, AT, BT, kExact, true>(maps, p, di, st);
+  }
+  return run_one<CG, BN, AT, BT, kExact, false>(maps, p, di, st);
 }
 
 // D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).
 template <bool AT, bool BT>
 cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
-                    void* workspace, int32_t* status, const DeviceInfo& di, cudaStream_t st) {
+                    int32_t* status, const DeviceInfo& di, cudaStream_t st) {
   const Plan q = plan_gemm(M, N, K, epi.out_f32);
   CUtensorMap maps[4] = {};
   const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
   if (!(AT ? make_map(&maps[0], A, M, K, lda, 64) : make_map(&maps[0], A, K, M, lda, 128)) ||
       !(BT ? make_map(&maps[1], B, N, K, ldb, box_b) : make_map(&maps[1], B, K, N, ldb, box_b)))
     return cudaErrorInvalidValue;
-  epi.part = q.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  epi.ldpart = (N + 7) / 8 * 8;
   epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
-  if (!epi.part && epi.wide &&
+  if (q.splits == 1 && epi.wide &&
       (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32) || (epi.z && !make_out_map(&maps[3], epi.z, N, M, false))))
     return cudaErrorInvalidValue;
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
-  cudaError_t err;
   if (epi.out_f32) {
-    err = q.kind == 1 ? run_gemm<2, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
-  } else {
     switch (q.kind) {
-      case 0: err = run_gemm<2, 256, AT, BT, false>(maps, p, di, st); break;
-      case 1: err = run_gemm<2, 128, AT, BT, false>(maps, p, di, st); break;
-      case 2: err = run_gemm<1, 128, AT, BT, false>(maps, p, di, st); break;
-      default: err = run_gemm<1, 64, AT, BT, false>(maps, p, di, st); break;
+      case 1: return run_gemm<2, 128, AT, BT, true>(maps, p, di, st);
+      case 2: return run_gemm<1, 128, AT, BT, true>(maps, p, di, st);
+      default: return run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
     }
   }
-  if (err != cudaSuccess || q.splits == 1) return err;
-  const long long work = ((long long)M * (epi.wide ? N / 8 : N) + 255) / 256;
-  const unsigned grid = (unsigned)(work < 8LL * di.sms ? work : 8LL * di.sms);
-  return launch_chained(gemm_join_kernel, dim3(grid), dim3(256), 0, st, epi, M, N, q.splits);
-}
-
-// Whichever output type the call will ask for.
-size_t part_bytes(int M, int N, int K) {
-  const size_t a = plan_gemm(M, N, K, false).part_bytes, b = plan_gemm(M, N, K, true).part_bytes;
-  return a > b ? a : b;
+  switch (q.kind) {
+    case 0: return run_gemm<2, 256, AT, BT, false>(maps, p, di, st);
+    case 1: return run_gemm<2, 128, AT, BT, false>(maps, p, di, st);
+    case 2: return run_gemm<1, 128, AT, BT, false>(maps, p, di, st);
+    default: return run_gemm<1, 64, AT, BT, false>(maps, p, di, st);
+  }
 }
 
 template <bool kHigh>
@@ -1220,23 +1237,20 @@ int slope_rows(int s, int N) {  // blocks along the rows: enough to fill the mac
 }
 
 struct BwdPlan {
-  size_t dz, part, gemm, total;
+  size_t dz, part, total;
 };
-BwdPlan plan_bwd(int s, int K, int N) {
+BwdPlan plan_bwd(int s, int N) {
   BwdPlan q;
   size_t at = 0;
   q.dz = at, at += up((size_t)s * ((N + 7) / 8 * 8) * 2);
   q.part = at, at += up((size_t)slope_rows(s, N) * N * 4);
-  q.gemm = at;
-  const size_t a = part_bytes(s, K, N), b = part_bytes(N, K, s);
-  q.total = at + (a > b ? a : b);
+  q.total = at;
   return q;
 }
 
 }  // namespace
 
-size_t linear_workspace(int s, int K, int N) { return s <= kFewRows ? 0 : part_bytes(s, N, K); }
-size_t linear_bwd_workspace(int s, int K, int N) { return plan_bwd(s, K, N).total; }
+size_t linear_bwd_workspace(int s, int N) { return plan_bwd(s, N).total; }
 
 namespace {
 
@@ -1268,11 +1282,11 @@ cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_
   e.bias_f32 = a.bias_f32;
   e.res_f32 = a.res_f32;
   if (a.s <= kFewRows) return a.s > 8 ? few_rows<true>(a, e, di, st) : few_rows<false>(a, e, di, st);
-  return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.workspace, a.status, di, st);
+  return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.status, di, st);
 }
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  const BwdPlan q = plan_bwd(a.s, a.K, a.N);
+  const BwdPlan q = plan_bwd(a.s, a.N);
   char* ws = static_cast<char*>(a.workspace);
   // without an activation a bf16 dy with whole 16-byte rows is dz itself
   const bool own_dz = (a.dx || a.dW) && (a.act != MOE_ACT_NONE || a.dy_f32 || a.lddy % 8 != 0);
@@ -1305,14 +1319,14 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
     Epi e = {};
     e.out = a.dx;
     e.out_f32 = a.dx_f32;
-    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, e, ws + q.gemm, a.status, di, st);
+    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   if (a.dW) {
     Epi e = {};
     e.out = a.dW;
     e.out_f32 = a.dw_f32;
-    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, e, ws + q.gemm, a.status, di, st);
+    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

@@ -536,10 +536,6 @@ typedef struct {
   int64_t ldx, ldw, ldres; /* elements between rows; ldx and ldw multiples of 8     */
 } moe_linear_desc;
 
-/* Bytes of moe_linear's workspace (partial products where the contracted axis is split over SMs);
- * 0 is common, and then the workspace may be NULL. */
-size_t moe_linear_workspace(int s, int K, int N);
-
 /* A dense product with bias, activation and residual in its epilogue:
  *   z = x W^T + bias,  y = act(z) + residual.
  * x bf16 [s,K], W bf16 [N,K] (K a multiple of 8, so that rows are whole 16
@@ -551,8 +547,7 @@ size_t moe_linear_workspace(int s, int K, int N);
  * a bounded device wait ran out.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
  * MOE_ERR_CUDA. */
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* W, const void* bias,
-                      const void* residual, void* y, void* z, void* workspace, size_t workspace_bytes,
-                      int32_t* device_status, void* stream);
+                      const void* residual, void* y, void* z, int32_t* device_status, void* stream);
 
 typedef struct {
   int32_t s, K, N;
@@ -563,7 +558,8 @@ typedef struct {
   int64_t lddy, ldx, ldw, ldz;
 } moe_linear_bwd_desc;
 
-size_t moe_linear_bwd_workspace(int s, int K, int N);
+/* Bytes of moe_linear_bwd's workspace: dz, and partial sums of db. */
+size_t moe_linear_bwd_workspace(int s, int N);
 
 /* Backward of moe_linear (the residual's gradient is dy itself):
  *   dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum_t dz.

@@ -249,14 +249,14 @@ def test_block_calls_reject_bad_arguments_without_a_gpu(lib):
     assert lib.moe_balance_loss_workspace(300, 1) == 0 and lib.moe_balance_loss_workspace(8, 4) > 0
     # products
     d = B.LinearDesc(4, 64, 8, 0, 1, 1, 1, 64, 64, 8)
-    call = lambda dd: rc_name(lib.moe_linear(ctypes.byref(dd), fake, fake, None, None, fake, None, None, 0, None, None))
+    call = lambda dd: rc_name(lib.moe_linear(ctypes.byref(dd), fake, fake, None, None, fake, None, None, None))
     for field, value in (("s", -1), ("K", 4), ("K", 12), ("N", 0), ("act", 5), ("act", -1), ("ldx", 32), ("ldx", 68), ("ldw", 60)):
         bad = B.LinearDesc(*[value if f == field else getattr(d, f) for f, _ in B.LinearDesc._fields_])
         assert call(bad) == "MOE_ERR_INVALID_ARG", field
     assert call(B.LinearDesc(4, 64, 8, 0, 2, 1, 1, 64, 64, 8)) == "MOE_ERR_DTYPE"
     assert call(B.LinearDesc(0, 64, 8, 0, 1, 1, 1, 64, 64, 8)) == "MOE_OK"
-    assert rc_name(lib.moe_linear(None, fake, fake, None, None, fake, None, None, 0, None, None)) == "MOE_ERR_INVALID_ARG"
+    assert rc_name(lib.moe_linear(None, fake, fake, None, None, fake, None, None, None)) == "MOE_ERR_INVALID_ARG"
     b = B.LinearBwdDesc(4, 64, 8, 0, 2, 1, 1, 8, 64, 64, 8)
     assert rc_name(lib.moe_linear_bwd(ctypes.byref(b), fake, fake, fake, None, fake, fake, fake, fake, 1 << 30, None,
                                       None)) == "MOE_ERR_DTYPE"
-    assert lib.moe_linear_workspace(0, 64, 8) == 0 and lib.moe_linear_bwd_workspace(16, 64, 8) > 0
+    assert lib.moe_linear_bwd_workspace(0, 8) == 0 and lib.moe_linear_bwd_workspace(16, 8) > 0
