@@ -1,5 +1,9 @@
 """Autograd wrappers and the activation-checkpoint handle recorder.
 
+Gate, dispatch and combine on a layout handle, and the operators around
+them: layer norm, dense products with their epilogue, the balance loss
+(``block.py`` strings all of them together).
+
 DeepSpeed #8213 "Add an opt-in DeepEP transport for the AutoEP expert
 all-to-all", description: the backward of a combine is a dispatch and the
 backward of a dispatch is a combine, both replayed against the handle the
@@ -89,6 +93,84 @@ def dispatch(x: torch.Tensor, handle: B.Handle) -> torch.Tensor:
 
 def combine(y: torch.Tensor, gate: torch.Tensor, handle: B.Handle) -> torch.Tensor:
     return MoECombineFn.apply(y, gate, handle)
+
+
+class LayerNormFn(torch.autograd.Function):
+    """y = layernorm(x) weight + bias; the weight gradients are summed in fp32 and rounded once to their type."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, weight, bias, eps: float):
+        y, mean, rstd = B.moe_layernorm(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        x, weight, mean, rstd = ctx.saved_tensors
+        _, need_w, need_b, _ = ctx.needs_input_grad
+        dx, dw, db = B.moe_layernorm_bwd(dy.contiguous(), x, weight, mean, rstd, need_dweight=need_w, need_dbias=need_b)
+        return dx, dw if dw is None else dw.to(weight.dtype), db if db is None else db.to(ctx.bias_dtype), None
+
+
+def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+              eps: float = 1e-5) -> torch.Tensor:
+    """Layer norm of [s, m] rows."""
+    return LayerNormFn.apply(x, weight, bias, eps)
+
+
+class LinearFn(torch.autograd.Function):
+    """y = act(x W^T + bias) + residual; z is kept (bf16) where the activation's slope needs it."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype):
+        save_z = act != "none" and any(ctx.needs_input_grad[:3])
+        out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z)
+        y, z = out if save_z else (out, None)
+        ctx.save_for_backward(x, W, z)
+        ctx.act = act
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        ctx.residual_dtype = None if residual is None else residual.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        x, W, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dW = db = None
+        if any(need[:3]):
+            dx, dW, db = B.moe_linear_bwd(dy.contiguous(), x, W, z, ctx.act, need[0], need[1], need[2])
+        return (dx, dW, db if db is None else db.to(ctx.bias_dtype),
+                dy.to(ctx.residual_dtype) if need[3] else None, None, None)
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """y [s, N] = act(x W^T + bias) + residual, bf16 (or fp32) out."""
+    return LinearFn.apply(x, W, bias, residual, act, out_dtype)
+
+
+class BalanceLossFn(torch.autograd.Function):
+    """loss [2] (balance, z) of the router's logits, with the counts held fixed in the gradient."""
+
+    @staticmethod
+    def forward(ctx, logits: torch.Tensor, topk_idx: torch.Tensor, valid, seq_offsets):
+        r = B.moe_balance_loss(logits, topk_idx, valid, seq_offsets)
+        ctx.save_for_backward(logits, r.lse, r.coef, r.norm, valid, seq_offsets)
+        ctx.mark_non_differentiable(r.counts, r.mean_prob)
+        return r.loss, r.counts, r.mean_prob
+
+    @staticmethod
+    def backward(ctx, dloss: torch.Tensor, dcounts, dmean_prob):
+        logits, lse, coef, norm, valid, seq_offsets = ctx.saved_tensors
+        d = B.moe_balance_loss_bwd(logits, lse, coef, norm, dloss.contiguous(), valid, seq_offsets)
+        return d, None, None, None
+
+
+def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Tensor | None = None,
+                 seq_offsets: torch.Tensor | None = None):
+    """(loss f32 [2]: the balance loss and the z loss, counts i32 [num_seqs, e], mean_prob f32 [num_seqs, e])."""
+    return BalanceLossFn.apply(logits, topk_idx, valid, seq_offsets)
 
 
 class HandleRecorder:
