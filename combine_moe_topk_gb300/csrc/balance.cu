@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
         if ((unsigned)id < (unsigned)p.e) atomicAdd(&s_count[id], 1);
         else if (id != -1) bad |= 2;
       }
+      float sums[U], bases[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float top = -FLT_MAX;  // a mask of the type's lowest value counts as -inf
@@ -190,20 +191,34 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
           }
         sum = lanes_sum<L>(sum);
         if (!(sum < CUDART_INF_F)) bad |= 1;  // a NaN or +inf makes it NaN
-        const bool some = live[u] && sum != 0.f;
-        if (some) {
-          const float inv = 1.f / sum;
+        // 0 for a row that takes no part; NaN stays
+        const float inv = live[u] && sum != 0.f ? __fdividef(1.f, sum) : 0.f;
+        if (live[u]) {
 #pragma unroll
           for (int i = 0; i < NI; ++i)
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[i][v] = fmaf(f[u][i][v], inv, acc[i][v]);
         }
-        const int t = t0 + u * kRows + sub;
-        if (t < r.y && col == 0) {
-          const float lse = some ? base + logf(sum) : (live[u] ? -CUDART_INF_F : 0.f);
+        sums[u] = live[u] ? sum : -1.f;
+        bases[u] = base;
+      }
+      // lse of the U row groups: lane u of a row's lanes takes group u, so that the
+      // logarithm is taken once (in rounds where a row has fewer lanes than U)
+#pragma unroll
+      for (int r0 = 0; r0 < U; r0 += L) {
+        float sum = sums[r0], base = bases[r0];
+#pragma unroll
+        for (int u = r0 + 1; u < U && u < r0 + L; ++u) {
+          sum = col == u - r0 ? sums[u] : sum;
+          base = col == u - r0 ? bases[u] : base;
+        }
+        const int t = t0 + (r0 + col) * kRows + sub;
+        if (col < U - r0 && col < L && t < r.y) {
+          const bool some = sum > 0.f || sum != sum;
+          const float lse = some ? base + logf(sum) : (sum < 0.f ? 0.f : -CUDART_INF_F);
           p.lse[t] = lse;
           if (some) zsum = fmaf(lse, lse, zsum);
-          tokens += live[u] ? 1 : 0;
+          tokens += sum < 0.f ? 0 : 1;
         }
       }
     }
