@@ -344,8 +344,10 @@ __device__ __forceinline__ void put_f32(Bulk& b, const CUtensorMap* map, const f
   }
 }
 
-// 32 consecutive values of fp32 or bf16 memory (those below n, a multiple of
-// 8), first all loads, so that they travel together, then the sum.
+// 32 consecutive values of fp32 or bf16 memory, of which the first n (a
+// multiple of 8, at least 8) exist; in the others' places the last eight come
+// again.  All loads first and none behind a condition, so that they travel
+// together, then the sum.
 struct Raw32 {
   uint4 v[8];
 };
@@ -354,11 +356,11 @@ __device__ __forceinline__ void load32(Raw32& r, const void* p, int is_f32, long
   if (is_f32) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = 4 * i < n ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) r.v[i] = __ldg(q + min(i, n / 4 - 1));
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.v[i] = 8 * i < n ? __ldg(q + i) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) r.v[i] = __ldg(q + min(i, n / 8 - 1));
   }
 }
 
@@ -377,7 +379,7 @@ __device__ __forceinline__ void add32(const Raw32& r, int is_f32, float (&f)[32]
 
 // The residual of this lane's row, loaded before the accumulator is waited for.
 __device__ __forceinline__ void load_residual(const Epi& e, Raw32& r, int row, int n0, int M, int N) {
-  if (e.res) load32(r, e.res, e.res_f32, (long long)row * e.ldres + n0, row < M ? N - n0 : 0);
+  if (e.res && n0 < N) load32(r, e.res, e.res_f32, (long long)min(row, M - 1) * e.ldres + n0, N - n0);
 }
 
 __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtensorMap* tmY, const CUtensorMap* tmZ,
@@ -421,14 +423,14 @@ __device__ __forceinline__ void finish_ragged(const Epi& e, uint8_t* stage, cons
     uint32_t cur[8], next[8];
     auto load_res = [&](uint32_t (&to)[8], int q) {
       if (!res) return;
+      // past the last row: that row again, unused, so that the loads are
+      // unconditional (behind a condition each waited for the one before it)
       if (e.res_f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          to[i] = q + i < rows ? __ldg(reinterpret_cast<const uint32_t*>(res + (q + i) * res_step)) : 0u;
+        for (int i = 0; i < 8; ++i) to[i] = __ldg(reinterpret_cast<const uint32_t*>(res + min(q + i, rows - 1) * res_step));
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          to[i] = q + i < rows ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(res + (q + i) * res_step)) << 16 : 0u;
+        for (int i = 0; i < 8; ++i) to[i] = __ldg(reinterpret_cast<const unsigned short*>(res + min(q + i, rows - 1) * res_step));
       }
     };
     load_res(cur, 0);
@@ -447,7 +449,7 @@ __device__ __forceinline__ void finish_ragged(const Epi& e, uint8_t* stage, cons
       if (e.act != MOE_ACT_NONE) activate<8>(f, e.act);
       if (res) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(cur[i]);
+        for (int i = 0; i < 8; ++i) f[i] += __uint_as_float(e.res_f32 ? cur[i] : cur[i] << 16);
       }
       if (e.out_f32) {
 #pragma unroll
