@@ -1104,18 +1104,25 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// One product's plan.  kind: index into the four tile shapes.
+// One product's plan.  kind: index into the three tile shapes.
 struct Plan {
   int kind, tiles_m, tiles_n, splits, per_split, kblocks;
 };
-constexpr int kKinds = 4;
-constexpr int kKindCG[kKinds] = {2, 2, 1, 1};
-constexpr int kKindBN[kKinds] = {256, 128, 128, 64};
+constexpr int kKinds = 3;
+constexpr int kKindCG[kKinds] = {2, 1, 1};
+constexpr int kKindBN[kKinds] = {256, 128, 64};
 constexpr int kPlanSms = 152;  // plans are made for a whole GB300
 
+// The shape and split of least estimated time, in units of a K block of the
+// widest tile (0.65 us).  Measured: a K block of a 128 x 128 tile takes 0.70 of
+// that and of 128 x 64 0.66 (both wait for shared memory, so the wide tile wins
+// wherever it fills the machine: 9728 x 4096 x 4096 172.8, 243.3, 457.1 us);
+// a launch's fixed part is 6.9, 5.9 and 4.7 us, a split's exchange 3.4 us.  So
+// 512 x 4096 x 4096 goes to 128 x 128 (20.7 us against 26.9 and 32.5), 64 rows
+// of it to four parts of 128 x 128 (14.2, unsplit wide 26.2), 1024^3 to 128 x 64
+// (7.8 against 12.8 and 9.9).
 Plan plan_gemm(int M, int N, int K, bool exact) {
-  // relative time of a K block on one tile of each shape
-  const double cost[kKinds] = {1.0, 0.6, 0.6, 0.42};
+  const double cost[kKinds] = {1.0, 0.70, 0.66}, base[kKinds] = {9.0, 8.0, 6.0};
   // clusters of 2, 4 and 8 CTAs that are surely resident at once
   const int clusters[4] = {0, 72, 34, 16};
   Plan best = {};
@@ -1137,7 +1144,7 @@ Plan plan_gemm(int M, int N, int K, bool exact) {
       if ((S - 1) * q.per_split >= kblocks) continue;  // the last part would be empty
       q.splits = S;
       const long long waves = S > 1 ? 1 : (tiles + workers - 1) / workers;
-      const double t = (double)waves * (q.per_split * cost[k] + 3.0) + (S > 1 ? 2.0 : 0.0);
+      const double t = (double)waves * (q.per_split * cost[k] + 1.0) + base[k] + (S > 1 ? 5.0 : 0.0);
       if (best.kblocks == 0 || t < best_t) {
         best = q;
         best_t = t;
@@ -1199,17 +1206,11 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
       (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32) || (epi.z && !make_out_map(&maps[3], epi.z, N, M, false))))
     return cudaErrorInvalidValue;
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
-  if (epi.out_f32) {
-    switch (q.kind) {
-      case 1: return run_gemm<2, 128, AT, BT, true>(maps, p, di, st);
-      case 2: return run_gemm<1, 128, AT, BT, true>(maps, p, di, st);
-      default: return run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
-    }
-  }
+  if (epi.out_f32)
+    return q.kind == 1 ? run_gemm<1, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
   switch (q.kind) {
     case 0: return run_gemm<2, 256, AT, BT, false>(maps, p, di, st);
-    case 1: return run_gemm<2, 128, AT, BT, false>(maps, p, di, st);
-    case 2: return run_gemm<1, 128, AT, BT, false>(maps, p, di, st);
+    case 1: return run_gemm<1, 128, AT, BT, false>(maps, p, di, st);
     default: return run_gemm<1, 64, AT, BT, false>(maps, p, di, st);
   }
 }
