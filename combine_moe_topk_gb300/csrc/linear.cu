@@ -128,6 +128,7 @@ struct Epi {
   const void* res;
   long long ldres;
   int act, out_f32, bias_f32, res_f32;
+  int narrow;       // stores of 64-byte rows
   int wide;         // N and the residual's stride are multiples of 8: rows of 16-byte pieces
 };
 
@@ -287,13 +288,18 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // 32 rows x 32 columns starting at (r0, n0), lane = row, v its columns.  The
 // usual way out (bulk): bias, activation and residual in that layout, then
 // the rounded rows into the warp's staging tile, which a TMA store writes,
-// clipped at the tensor's edge.  The tile is two pieces of 32 rows x 64 bytes,
-// used in turn, so one store drains while the next piece is filled; 64-byte
-// swizzle (the 16-byte piece's index XOR half the row), free of bank conflicts.
-// Against four lanes a row and 16-byte stores this took a quarter of the
-// instructions: dx of 16384 x 4096 from 128 columns 75.7 -> @DX@ us.
+// clipped at the tensor's edge.  The tile is one piece of 32 rows x 128 bytes
+// (64 bf16 columns, filled in two halves, or 32 fp32), or, where z is stored
+// beside y or a warp's columns are only 32, two pieces of 64 bytes a row used
+// in turn; 16-byte parts XOR-swizzled by the row (128-byte and 64-byte
+// swizzle), free of bank conflicts.  Against 16-byte stores by lanes this takes
+// a quarter of the instructions: dx of 16384 x 4096 from 128 columns, a product
+// that is little but its output, 75.7 -> 47 us (44 without the stores, 28
+// without the epilogue: what is left is the tile's hand-over between load,
+// product and epilogue).  Rows of 128 bytes instead of 64 matter to the large
+// products (8192 x 4096 x 16384: 566 -> 545 us).
 struct Bulk {
-  uint8_t* stage;  // this warp's 2 x 2 KB
+  uint8_t* stage;  // this warp's 4 KB
   int piece;
 };
 
@@ -304,8 +310,17 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-// One piece: 16 words of each lane's row to columns starting at x.
-__device__ __forceinline__ void put_piece(Bulk& b, const CUtensorMap* map, const uint32_t (&w)[16], int x, int y, int lane) {
+__device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* src, int x, int y, int lane) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, src, x, y);
+    bulk_commit();
+  }
+}
+
+// 16 words of each lane's row, 64-byte pieces, columns starting at x.
+__device__ __forceinline__ void put_narrow(Bulk& b, const CUtensorMap* map, const uint32_t* w, int x, int y, int lane) {
   uint8_t* dst = b.stage + b.piece * 2048;
   if (lane == 0) bulk_wait_read<1>();  // the store before last, from this piece
   __syncwarp();
@@ -313,34 +328,30 @@ __device__ __forceinline__ void put_piece(Bulk& b, const CUtensorMap* map, const
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(map, dst, x, y);
-    bulk_commit();
-  }
+  store_piece(map, dst, x, y, lane);
   b.piece ^= 1;
 }
 
-__device__ __forceinline__ void put_bf16(Bulk& b, const CUtensorMap* map, const float (&f)[32], int x, int y, int lane) {
-  uint32_t w[16];
+// 16 words as half `half` of a 128-byte piece whose columns start at x; the
+// piece leaves with its second half, or at once where `last`.
+__device__ __forceinline__ void put_half(Bulk& b, const CUtensorMap* map, const uint32_t* w, int half, bool last, int x,
+                                         int y, int lane) {
+  if (half == 0) {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<uint4*>(b.stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  if (half == 1 || last) store_piece(map, b.stage, x, y, lane);
+}
+
+__device__ __forceinline__ void pack_bf16(const float (&f)[32], uint32_t (&w)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
     w[j] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  put_piece(b, map, w, x, y, lane);
-}
-
-__device__ __forceinline__ void put_f32(Bulk& b, const CUtensorMap* map, const float (&f)[32], int x, int y, int N, int lane) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (x + 16 * h < N) {
-      uint32_t w[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(f[16 * h + j]);
-      put_piece(b, map, w, x + 16 * h, y, lane);
-    }
   }
 }
 
@@ -382,9 +393,11 @@ __device__ __forceinline__ void load_residual(const Epi& e, Raw32& r, int row, i
   if (e.res && n0 < N) load32(r, e.res, e.res_f32, (long long)min(row, M - 1) * e.ldres + n0, N - n0);
 }
 
+// c: which of the warp's 32-column blocks this is; kPair: they come in pairs.
+template <bool kPair>
 __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtensorMap* tmY, const CUtensorMap* tmZ,
-                                            const uint32_t (&v)[32], const Raw32& res, int r0, int n0, int M, int N,
-                                            int lane) {
+                                            const uint32_t (&v)[32], const Raw32& res, int c, int r0, int n0, int M,
+                                            int N, int lane) {
   if (r0 >= M || n0 >= N) return;  // the whole warp
   float f[32];
 #pragma unroll
@@ -394,11 +407,27 @@ __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtenso
     load32(bias, e.bias, e.bias_f32, n0, N - n0);
     add32(bias, e.bias_f32, f);
   }
-  if (e.z) put_bf16(b, tmZ, f, n0, r0, lane);
+  uint32_t w[16];
+  if (e.z) {
+    pack_bf16(f, w);
+    put_narrow(b, tmZ, w, n0, r0, lane);
+  }
   if (e.act != MOE_ACT_NONE) activate<32>(f, e.act);
   if (e.res) add32(res, e.res_f32, f);
-  if (e.out_f32) put_f32(b, tmY, f, n0, r0, N, lane);
-  else put_bf16(b, tmY, f, n0, r0, lane);
+  if (e.out_f32) {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(f);
+    if (e.narrow) {
+      put_narrow(b, tmY, u, n0, r0, lane);
+      if (n0 + 16 < N) put_narrow(b, tmY, u + 16, n0 + 16, r0, lane);
+    } else {
+      put_half(b, tmY, u, 0, false, n0, r0, lane);
+      put_half(b, tmY, u + 16, 1, true, n0, r0, lane);
+    }
+  } else {
+    pack_bf16(f, w);
+    if (!kPair || e.narrow) put_narrow(b, tmY, w, n0, r0, lane);
+    else put_half(b, tmY, w, c & 1, n0 + 32 >= N, n0 - 32 * (c & 1), r0, lane);
+  }
 }
 
 // The same block where rows are not of 16 bytes, so that TMA cannot write
@@ -714,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 8; ++q)
             reinterpret_cast<uint4*>(row)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         } else if (p.epi.wide) {
-          finish_bulk(p.epi, bulk, &tmY, &tmZ, v, res, r0, n0 + 32 * c, p.M, p.N, lane);
+          finish_bulk<BN >= 128>(p.epi, bulk, &tmY, &tmZ, v, res, c, r0, n0 + 32 * c, p.M, p.N, lane);
         } else {
           finish_ragged(p.epi, stage_buf, v, r0, n0 + 32 * c, p.M, p.N, lane);
         }
@@ -1078,16 +1107,16 @@ __global__ void __launch_bounds__(256, 6) slope_kernel(const SlopeArgs p) {
 // ---- host ------------------------------------------------------------------------
 
 // Output [outer][inner] of 4- or 2-byte elements as the epilogue stores it:
-// boxes of 32 rows x 64 bytes, 64-byte swizzle.
-bool make_out_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, bool f32) {
+// boxes of 32 rows x 64 or 128 bytes, swizzled.
+bool make_out_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, bool f32, bool narrow) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {inner * (f32 ? 4 : 2)};
-  cuuint32_t box[2] = {f32 ? 16u : 32u, 32u};
+  cuuint32_t box[2] = {(narrow ? 64u : 128u) / (f32 ? 4u : 2u), 32u};
   cuuint32_t estride[2] = {1, 1};
   return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-            strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1202,8 +1231,10 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
       !(BT ? make_map(&maps[1], B, N, K, ldb, box_b) : make_map(&maps[1], B, K, N, ldb, box_b)))
     return cudaErrorInvalidValue;
   epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
+  epi.narrow = epi.z || (!epi.out_f32 && kKindBN[q.kind] < 128);
   if (q.splits == 1 && epi.wide &&
-      (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32) || (epi.z && !make_out_map(&maps[3], epi.z, N, M, false))))
+      (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32, epi.narrow) ||
+       (epi.z && !make_out_map(&maps[3], epi.z, N, M, false, true))))
     return cudaErrorInvalidValue;
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
   if (epi.out_f32)
