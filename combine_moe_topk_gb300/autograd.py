@@ -95,11 +95,19 @@ def combine(y: torch.Tensor, gate: torch.Tensor, handle: B.Handle) -> torch.Tens
     return MoECombineFn.apply(y, gate, handle)
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor on 16 bytes, as the library wants its pointers: autograd hands out views (of a
+    concatenation's gradient, say) that may start anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class LayerNormFn(torch.autograd.Function):
     """y = layernorm(x) weight + bias; the weight gradients are summed in fp32 and rounded once to their type."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight, bias, eps: float):
+        x = x if x.dim() == 2 and x.stride(1) == 1 and x.data_ptr() % 16 == 0 else _rows(x)
         y, mean, rstd = B.moe_layernorm(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.bias_dtype = None if bias is None else bias.dtype
@@ -109,7 +117,7 @@ class LayerNormFn(torch.autograd.Function):
     def backward(ctx, dy: torch.Tensor):
         x, weight, mean, rstd = ctx.saved_tensors
         _, need_w, need_b, _ = ctx.needs_input_grad
-        dx, dw, db = B.moe_layernorm_bwd(dy.contiguous(), x, weight, mean, rstd, need_dweight=need_w, need_dbias=need_b)
+        dx, dw, db = B.moe_layernorm_bwd(_rows(dy), x, weight, mean, rstd, need_dweight=need_w, need_dbias=need_b)
         return dx, dw if dw is None else dw.to(weight.dtype), db if db is None else db.to(ctx.bias_dtype), None
 
 
@@ -124,6 +132,8 @@ class LinearFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype):
+        x = x if x.data_ptr() % 16 == 0 else _rows(x)
+        residual = residual if residual is None or residual.data_ptr() % 16 == 0 else _rows(residual)
         save_z = act != "none" and any(ctx.needs_input_grad[:3])
         out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z)
         y, z = out if save_z else (out, None)
@@ -139,7 +149,7 @@ class LinearFn(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx = dW = db = None
         if any(need[:3]):
-            dx, dW, db = B.moe_linear_bwd(dy.contiguous(), x, W, z, ctx.act, need[0], need[1], need[2])
+            dx, dW, db = B.moe_linear_bwd(_rows(dy), x, W, z, ctx.act, need[0], need[1], need[2])
         return (dx, dW, db if db is None else db.to(ctx.bias_dtype),
                 dy.to(ctx.residual_dtype) if need[3] else None, None, None)
 

@@ -61,7 +61,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int t)
   int lo = 0, hi = B;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(offsets + mid + 1) <= t) lo = mid + 1; else hi = mid;
+    if (ld_plain(offsets + mid + 1) <= t) lo = mid + 1; else hi = mid;
   }
   return lo;
 }
@@ -69,7 +69,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int t)
 // Bounds of sequence b inside [lo, hi); empty (x >= y) where they do not meet.
 __device__ __forceinline__ int2 piece_of(const int32_t* offsets, int s, int b, int lo, int hi) {
   if (!offsets) return make_int2(lo, hi);
-  const int o0 = __ldg(offsets + b), o1 = __ldg(offsets + b + 1);
+  const int o0 = ld_plain(offsets + b), o1 = ld_plain(offsets + b + 1);
   return make_int2(o0 > lo ? o0 : lo, o1 < hi ? o1 : hi);
 }
 
@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_cols(const float* p, float* f) {
     const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
     Vec<float>::to_float(v, f);
   } else {
-    f[0] = __ldg(p);
+    f[0] = ld_plain(p);
   }
 }
 
@@ -125,12 +125,12 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
   grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the join, later in the stream
   // tokens outside every sequence: nothing of theirs counts
-  const int first = p.offsets ? __ldg(p.offsets) : 0, last = p.offsets ? __ldg(p.offsets + p.B) : p.s;
+  const int first = p.offsets ? ld_plain(p.offsets) : 0, last = p.offsets ? ld_plain(p.offsets + p.B) : p.s;
   for (int t = lo + threadIdx.x; t < hi; t += kBlock)
     if (t < first || t >= last) p.lse[t] = 0.f;
   int bad = 0;
   for (int b = p.offsets ? sequence_of(p.offsets, p.B, lo) : 0; b < p.B; ++b) {
-    if (p.offsets && __ldg(p.offsets + b) >= hi) break;
+    if (p.offsets && ld_plain(p.offsets + b) >= hi) break;
     const int2 r = piece_of(p.offsets, p.s, b, lo, hi);
     if (r.x >= r.y) continue;  // the same for the whole block
     for (int j = threadIdx.x; j < p.e; j += kBlock) s_count[j] = 0;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * kRows + sub;
-        live[u] = t < r.y && (!p.valid || __ldg(p.valid + t) != 0);
+        live[u] = t < r.y && (!p.valid || ld_plain(p.valid + t) != 0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
       const int n_ids = min(kRows * U, r.y - t0) * p.k;
 #pragma unroll 2
       for (int q = lane; q < n_ids; q += 32) {
-        const int id = __ldg(p.idx + (size_t)t0 * p.k + q);
-        if (p.valid && __ldg(p.valid + t0 + q / p.k) == 0) continue;
+        const int id = ld_plain(p.idx + (size_t)t0 * p.k + q);
+        if (p.valid && ld_plain(p.valid + t0 + q / p.k) == 0) continue;
         if ((unsigned)id < (unsigned)p.e) atomicAdd(&s_count[id], 1);
         else if (id != -1) bad |= 2;
       }
@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
   grid_dependency_wait();
   int lo = 0, hi = p.s;
   if (p.offsets) {
-    lo = max(0, __ldg(p.offsets + b));
-    hi = min(p.s, __ldg(p.offsets + b + 1));
+    lo = max(0, ld_plain(p.offsets + b));
+    hi = min(p.s, ld_plain(p.offsets + b + 1));
   }
   const int c0 = lo / p.chunk, c1 = lo < hi ? (hi - 1) / p.chunk + 1 : c0;  // the blocks that have a piece of it
   {
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
           const size_t at = ((size_t)min(q + 32 * i, c1 - 1) + b) * p.e + col;
-          f[i] = q + 32 * i < c1 ? __ldg(p.pc.psum + at) : 0.f;
-          n[i] = q + 32 * i < c1 ? __ldg(p.pc.count + at) : 0;
+          f[i] = q + 32 * i < c1 ? ld_plain(p.pc.psum + at) : 0.f;
+          n[i] = q + 32 * i < c1 ? ld_plain(p.pc.count + at) : 0;
         }
 #pragma unroll
         for (int i = 0; i < 10; ++i) {
@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
     float z = 0.f;
     int tokens = 0;
     for (int c = c0 + threadIdx.x; c < c1; c += kJoin) {
-      tokens += __ldg(p.pc.tokens + (size_t)c + b);
-      z += __ldg(p.pc.zsum + (size_t)c + b);
+      tokens += ld_plain(p.pc.tokens + (size_t)c + b);
+      z += ld_plain(p.pc.zsum + (size_t)c + b);
     }
     s_f[ty][tx] = sum;
     s_c[ty][tx] = count;
@@ -432,13 +432,13 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
   const int sub = lane / L, col = lane % L;
   const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
   grid_dependency_wait();
-  const float wl = __ldg(p.dloss) * __ldg(p.norm), wz = 2.f * __ldg(p.dloss + 1) * __ldg(p.norm + 1);
+  const float wl = ld_plain(p.dloss) * ld_plain(p.norm), wz = 2.f * ld_plain(p.dloss + 1) * ld_plain(p.norm + 1);
   if (p.offsets) {
-    copy_rows<V>(p, lo, min(hi, max(lo, __ldg(p.offsets))));
-    copy_rows<V>(p, max(lo, min(hi, __ldg(p.offsets + p.B))), hi);
+    copy_rows<V>(p, lo, min(hi, max(lo, ld_plain(p.offsets))));
+    copy_rows<V>(p, max(lo, min(hi, ld_plain(p.offsets + p.B))), hi);
   }
   for (int b = p.offsets ? sequence_of(p.offsets, p.B, lo) : 0; b < p.B; ++b) {
-    if (p.offsets && __ldg(p.offsets + b) >= hi) break;
+    if (p.offsets && ld_plain(p.offsets + b) >= hi) break;
     const int2 r = piece_of(p.offsets, p.s, b, lo, hi);
     if (r.x >= r.y) continue;
     float c[NI][V];
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int j = V * (col + L * i) + v;
-        c[i][v] = j < p.e ? wl * __ldg(p.coef + (size_t)b * p.e + j) : 0.f;
+        c[i][v] = j < p.e ? wl * ld_plain(p.coef + (size_t)b * p.e + j) : 0.f;
       }
     for (int t0 = r.x + warp * kRows * U; t0 < r.y; t0 += kWarps * kRows * U) {
       float f[U][NI][V], g[U][NI][V], lse[U];
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * kRows + sub;
-        const bool live = t < r.y && (!p.valid || __ldg(p.valid + t) != 0);
-        lse[u] = t < r.y ? __ldg(p.lse + t) : 0.f;
+        const bool live = t < r.y && (!p.valid || ld_plain(p.valid + t) != 0);
+        lse[u] = t < r.y ? ld_plain(p.lse + t) : 0.f;
         some[u] = live && lse[u] != -CUDART_INF_F;  // a row of masked experts has no probabilities
       }
 #pragma unroll

@@ -34,6 +34,16 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A load that stays behind grid_dependency_wait().  __ldg says that the memory
+// is constant for the kernel's whole life, and the compiler may then move it
+// above the wait, where the kernel before may still be writing (seen in a
+// captured graph: the balance loss's backward pass read its scale before it
+// was there).
+template <typename T>
+__device__ __forceinline__ T ld_plain(const T* p) {
+  return *p;
+}
+
 // Let the next kernel in the stream begin its launch (it still waits for this
 // grid to complete before reading its results).
 __device__ __forceinline__ void grid_dependents_launch() {

@@ -133,17 +133,17 @@ struct Epi {
 };
 
 __device__ __forceinline__ float load_any(const void* p, int is_f32, long long i) {
-  return is_f32 ? __ldg(static_cast<const float*>(p) + i) : __bfloat162float(__ldg(static_cast<const bf16*>(p) + i));
+  return is_f32 ? ld_plain(static_cast<const float*>(p) + i) : __bfloat162float(ld_plain(static_cast<const bf16*>(p) + i));
 }
 
 // Eight consecutive values of fp32 or bf16 memory, 16-byte aligned.
 __device__ __forceinline__ void load8(const void* p, int is_f32, long long i, float* f) {
   if (is_f32) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-    Vec<float>::to_float(__ldg(q), f);
-    Vec<float>::to_float(__ldg(q + 1), f + 4);
+    Vec<float>::to_float(ld_plain(q), f);
+    Vec<float>::to_float(ld_plain(q + 1), f + 4);
   } else {
-    Vec<bf16>::to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + i)), f);
+    Vec<bf16>::to_float(ld_plain(reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + i)), f);
   }
 }
 
@@ -367,11 +367,11 @@ __device__ __forceinline__ void load32(Raw32& r, const void* p, int is_f32, long
   if (is_f32) {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = __ldg(q + min(i, n / 4 - 1));
+    for (int i = 0; i < 8; ++i) r.v[i] = ld_plain(q + min(i, n / 4 - 1));
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.v[i] = __ldg(q + min(i, n / 8 - 1));
+    for (int i = 0; i < 4; ++i) r.v[i] = ld_plain(q + min(i, n / 8 - 1));
   }
 }
 
@@ -456,10 +456,10 @@ __device__ __forceinline__ void finish_ragged(const Epi& e, uint8_t* stage, cons
       // unconditional (behind a condition each waited for the one before it)
       if (e.res_f32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = __ldg(reinterpret_cast<const uint32_t*>(res + min(q + i, rows - 1) * res_step));
+        for (int i = 0; i < 8; ++i) to[i] = ld_plain(reinterpret_cast<const uint32_t*>(res + min(q + i, rows - 1) * res_step));
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = __ldg(reinterpret_cast<const unsigned short*>(res + min(q + i, rows - 1) * res_step));
+        for (int i = 0; i < 8; ++i) to[i] = ld_plain(reinterpret_cast<const unsigned short*>(res + min(q + i, rows - 1) * res_step));
       }
     };
     load_res(cur, 0);

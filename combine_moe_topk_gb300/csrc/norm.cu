@@ -120,17 +120,17 @@ __device__ __forceinline__ void load_weights(const void* w, int is_f32, int c, i
     for (int j = 0; j < C; ++j) {
       f[j] = 0.f;
       if (c + j < m)
-        f[j] = is_f32 ? __ldg(static_cast<const float*>(w) + c + j)
-                      : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(w) + c + j));
+        f[j] = is_f32 ? ld_plain(static_cast<const float*>(w) + c + j)
+                      : __bfloat162float(ld_plain(static_cast<const __nv_bfloat16*>(w) + c + j));
     }
   } else if (is_f32) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(w) + c);
 #pragma unroll
-    for (int q = 0; q < C / 4; ++q) Vec<float>::to_float(__ldg(p + q), f + 4 * q);
+    for (int q = 0; q < C / 4; ++q) Vec<float>::to_float(ld_plain(p + q), f + 4 * q);
   } else if (C == 8) {
-    Vec<__nv_bfloat16>::to_float(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c)), f);
+    Vec<__nv_bfloat16>::to_float(ld_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c)), f);
   } else {  // four bf16 beside fp32 rows
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c));
+    const uint2 u = ld_plain(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + c));
     f[0] = __uint_as_float(u.x << 16);
     f[1] = __uint_as_float(u.x & 0xffff0000u);
     f[2] = __uint_as_float(u.y << 16);
@@ -347,18 +347,18 @@ __global__ void __launch_bounds__(512) layernorm_wide_kernel(const NormFwd p) {
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
   const int gw = threadIdx.x >> 5;
   float sum = 0.f;
-  for (int c = threadIdx.x; c < p.m; c += blockDim.x) sum += to_f<T>(__ldg(x + c));
+  for (int c = threadIdx.x; c < p.m; c += blockDim.x) sum += to_f<T>(ld_plain(x + c));
   const float inv_m = 1.f / (float)p.m;
   const float mu = group_sum<16>(sum, slots[0], gw, 0) * inv_m;
   float sq = 0.f;
   for (int c = threadIdx.x; c < p.m; c += blockDim.x) {
-    const float d = to_f<T>(__ldg(x + c)) - mu;
+    const float d = to_f<T>(ld_plain(x + c)) - mu;
     sq = fmaf(d, d, sq);
   }
   const float r = 1.f / sqrtf(group_sum<16>(sq, slots[1], gw, 0) * inv_m + p.eps);
   T* y = static_cast<T*>(p.y) + row * p.m;
   for (int c = threadIdx.x; c < p.m; c += blockDim.x) {
-    float o = (to_f<T>(__ldg(x + c)) - mu) * r, v[1];
+    float o = (to_f<T>(ld_plain(x + c)) - mu) * r, v[1];
     if (p.w) {
       load_weights<1>(p.w, p.w_f32, c, p.m, v);
       o *= v[0];
@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(threads_of(G), bwd_blocks(G)) layernorm_bwd_ke
     for (int u = 0; u < R; ++u) {
       const long long r = r0 + u < p.s ? r0 + u : r0;
       if (r < p.s) {
-        mu[u] = __ldg(p.mean + r);
-        rs[u] = __ldg(p.rstd + r);
+        mu[u] = ld_plain(p.mean + r);
+        rs[u] = ld_plain(p.rstd + r);
       }
     }
   };
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(threads_of(G), bwd_blocks(G)) layernorm_bwd_ke
 #pragma unroll
             for (int j = 0; j < 2 * kHalf; ++j) {
               const int c = (t + (i * kPer + j / C) * span) * C + j % C;
-              add.f[j] = c < p.m ? to_f<T>(__ldg(res_row + c)) : 0.f;
+              add.f[j] = c < p.m ? to_f<T>(ld_plain(res_row + c)) : 0.f;
             }
           }
         }
@@ -622,12 +622,12 @@ __global__ void __launch_bounds__(512) layernorm_bwd_wide_kernel(const NormBwd p
   for (long long row = blockIdx.x; row < p.s; row += gridDim.x, ++it) {
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const float mu = __ldg(p.mean + row), r = __ldg(p.rstd + row);
+    const float mu = ld_plain(p.mean + row), r = ld_plain(p.rstd + row);
     float s1 = 0.f, s2 = 0.f;
     for (int c = threadIdx.x; c < p.m; c += blockDim.x) {
       float wv[1] = {1.f};
       if (p.w) load_weights<1>(p.w, p.w_f32, c, p.m, wv);
-      const float d = to_f<T>(__ldg(dy + c)), xh = (to_f<T>(__ldg(x + c)) - mu) * r, g = d * wv[0];
+      const float d = to_f<T>(ld_plain(dy + c)), xh = (to_f<T>(ld_plain(x + c)) - mu) * r, g = d * wv[0];
       s1 += g;
       s2 = fmaf(g, xh, s2);
       if (pw) {
@@ -641,9 +641,9 @@ __global__ void __launch_bounds__(512) layernorm_bwd_wide_kernel(const NormBwd p
     for (int c = threadIdx.x; c < p.m; c += blockDim.x) {
       float wv[1] = {1.f};
       if (p.w) load_weights<1>(p.w, p.w_f32, c, p.m, wv);
-      const float g = to_f<T>(__ldg(dy + c)) * wv[0], xh = (to_f<T>(__ldg(x + c)) - mu) * r;
+      const float g = to_f<T>(ld_plain(dy + c)) * wv[0], xh = (to_f<T>(ld_plain(x + c)) - mu) * r;
       float o = r * (g - c1 - xh * c2);
-      if (p.dres) o += to_f<T>(__ldg(static_cast<const T*>(p.dres) + row * p.lddres + c));
+      if (p.dres) o += to_f<T>(ld_plain(static_cast<const T*>(p.dres) + row * p.lddres + c));
       static_cast<T*>(p.dx)[row * p.m + c] = from_f<T>(o);
     }
   }
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* part, int 
     for (int q0 = threadIdx.y; q0 < parts; q0 += 320) {
       float t[10];
 #pragma unroll
-      for (int i = 0; i < 10; ++i) t[i] = q0 + 32 * i < parts ? __ldg(src + (size_t)(q0 + 32 * i) * m + col) : 0.f;
+      for (int i = 0; i < 10; ++i) t[i] = q0 + 32 * i < parts ? ld_plain(src + (size_t)(q0 + 32 * i) * m + col) : 0.f;
 #pragma unroll
       for (int i = 0; i < 10; ++i) v += t[i];
     }

@@ -445,7 +445,8 @@ moe_status moe_dispatch_grouped_gemm(moe_handle h, int s, int rows, int K, int N
  * the path above (the norm in front of it, the router's projection and loss,
  * a shared expert).  They need no handle.  Row strides (ld*) count elements, are at least the row's length,
  * and apply to inputs; outputs are contiguous.  Any row length is taken; rows
- * and strides of whole 16 bytes are read with wide loads.  Workspaces are
+ * and strides of whole 16 bytes are read with wide loads.  Outputs must not
+ * overlap inputs, except where a call says so.  Workspaces are
  * caller-owned device memory, 16-byte aligned, of the size the _workspace
  * call names (a host computation), needed only until the call's work on
  * `stream` is done; their contents need no initialisation. */
@@ -471,8 +472,7 @@ size_t moe_layernorm_bwd_workspace(int s, int m);
  *   dx = rstd * (g - mean_m(g) - xh * mean_m(g * xh)) [+ dres],
  *   dweight = sum_t dy * xh, dbias = sum_t dy   (f32 [m], each nullable).
  * dres [s,m] (nullable): the gradient that reaches x past the norm, e.g. along
- * the residual branch, added before dx is rounded.  dx must not overlap an
- * input.  The sums over tokens are fp32 in a fixed order: the same bits on
+ * the residual branch, added before dx is rounded.  The sums over tokens are fp32 in a fixed order: the same bits on
  * every run.  With s = 0, dweight and dbias are zeroed. */
 moe_status moe_layernorm_bwd(int s, int m, moe_dtype dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,
                              moe_dtype weight_dtype, const void* weight, const float* mean, const float* rstd,

@@ -105,6 +105,13 @@ def test_autograd_wrappers_return_what_was_asked_for():
     w = torch.ones(64, device="cuda").bfloat16().requires_grad_()
     A.layernorm(x, w).sum().backward()
     assert w.grad.dtype == torch.bfloat16
+    # a concatenation's gradient: views that start off 16 bytes
+    a, c = (torch.randn(3, 7, device="cuda").bfloat16().requires_grad_() for _ in range(2))
+    torch.cat([A.layernorm(a), A.layernorm(c)]).float().square().sum().backward()
+    assert torch.isfinite(c.grad).all()
+    W3 = torch.randn(5, 64, device="cuda").bfloat16().requires_grad_()
+    torch.cat([A.linear(x[:3], W3, act="silu"), A.linear(x[3:8], W3, act="silu")]).float().sum().backward()
+    assert torch.isfinite(W3.grad).all()
     # a broadcast upstream gradient (stride 0) reaches the kernels as rows of their own
     xx = x.clone().requires_grad_()
     A.layernorm(xx, w).mean(0).sum().backward()

@@ -105,6 +105,50 @@ def test_shapes_backward(s, K, N):
     check_bwd(dy, x, W, z, "silu", B.moe_linear_bwd(dy, x, W, z, "silu"), rounded=True)
 
 
+# more tiles than workers: accumulators, ring and staging go round; both output types, N of 16-byte rows and not
+@pytest.mark.parametrize("s,K,N", [(4100, 640, 5000), (3000, 1032, 2501), (9000, 72, 1032), (300, 264, 9001)])
+def test_many_tiles(s, K, N):
+    x, W, b, r, dy, z = make(s, K, N, seed=K, res=torch.bfloat16)
+    y, zz = B.moe_linear(x, W, b, "silu", r, save_z=True)
+    check_fwd(x, W, b, r, "silu", y, zz)
+    check_fwd(x, W, b, r, "gelu", B.moe_linear(x, W, b, "gelu", r))
+    check_fwd(x, W, None, None, "none", B.moe_linear(x, W, out_dtype=torch.float32))
+    check_bwd(dy, x, W, None, "none", B.moe_linear_bwd(dy, x, W, dx_dtype=torch.float32, dw_dtype=torch.float32), rounded=False)
+    check_bwd(dy, x, W, z, "gelu_tanh", B.moe_linear_bwd(dy, x, W, z, "gelu_tanh"), rounded=True)
+
+
+def test_calls_in_a_captured_graph():
+    # one decode step and one training step, captured once and replayed on new inputs
+    x, W, b, r, dy, z = make(40, 256, 256, seed=12, res=torch.bfloat16)
+    w = torch.ones(256, device="cuda")
+
+    def step():
+        h, mean, rstd = B.moe_layernorm(x, w, w)
+        y, zz = B.moe_linear(h, W, b, "gelu", r, save_z=True)
+        few = B.moe_linear(h[:3], W, b, "silu")
+        logits = B.moe_linear(y, W[:16], out_dtype=torch.float32)
+        idx = torch.zeros(40, 2, dtype=torch.int32, device="cuda")
+        bl = B.moe_balance_loss(logits, idx)
+        dl = B.moe_balance_loss_bwd(logits, bl.lse, bl.coef, bl.norm, bl.norm)
+        dh, dW, db = B.moe_linear_bwd(dy, h, W, zz, "gelu")
+        return (h, y, few, bl.loss, dl, dW, db) + B.moe_layernorm_bwd(dh, x, w, mean, rstd)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (13, 14):
+        x.copy_(make(40, 256, 256, seed=seed)[0])
+        graph.replay()
+        got = [t.clone() for t in out]
+        for a, c in zip(got, step()):
+            assert torch.equal(a, c)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("s,K,N", [(5, 256, 40), (70, 512, 333), (700, 1024, 768)])
 def test_activations_and_types(act, s, K, N):

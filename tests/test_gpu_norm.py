@@ -92,6 +92,20 @@ def test_layernorm_and_gradient(s, m, dtype, wdtype):
     check_bwd(dy, x, w, mean, rstd, res, B.moe_layernorm_bwd(dy, x, w, mean, rstd, dres=res), dtype)
 
 
+# enough rows that every group walks over several and the ring goes round, in every width's form
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("s,m", [(30000, 40), (21000, 64), (6000, 256), (5003, 70), (5001, 515), (3001, 1000), (2600, 1537),
+                                 (1300, 4096), (1300, 4098), (700, 8192), (640, 8193), (500, 9000), (330, 16384), (321, 16400),
+                                 (310, 16385)])
+def test_many_rows(s, m, dtype):
+    x, w, b, dy, res = make(s, m, dtype, "f32", seed=s + m)
+    out = B.moe_layernorm(x, w, b)
+    check_fwd(x, w, b, out, dtype)
+    _, mean, rstd = out
+    check_bwd(dy, x, w, mean, rstd, res, B.moe_layernorm_bwd(dy, x, w, mean, rstd, dres=res), dtype)
+    check_bwd(dy, x, w, mean, rstd, None, B.moe_layernorm_bwd(dy, x, w, mean, rstd), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("m,ld", [(256, 264), (256, 259), (250, 256), (9000, 9016), (33, 50)])
 def test_strided_rows(dtype, m, ld):
