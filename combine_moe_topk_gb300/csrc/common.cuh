@@ -44,6 +44,19 @@ __device__ __forceinline__ T ld_plain(const T* p) {
   return *p;
 }
 
+// The same where the pointer is __restrict__, of which the compiler would
+// make a constant load again.
+__device__ __forceinline__ float ld_ordered(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_ordered(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+
 // Let the next kernel in the stream begin its launch (it still waits for this
 // grid to complete before reading its results).
 __device__ __forceinline__ void grid_dependents_launch() {

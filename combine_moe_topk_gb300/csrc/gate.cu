@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) topk_gate_kernel(const float* __restrict_
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int j = lane + 32 * i;
-    nxt[i] = (t < s && j < e) ? __ldg(logits + (size_t)t * e + j) : 0.0f;
+    nxt[i] = (t < s && j < e) ? ld_ordered(logits + (size_t)t * e + j) : 0.0f;
   }
   for (; t < s; t += warps) {
     float cur[EPL];
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(256) topk_gate_kernel(const float* __restrict_
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int j = lane + 32 * i;
-      nxt[i] = (tn < s && j < e) ? __ldg(logits + (size_t)tn * e + j) : 0.0f;
+      nxt[i] = (tn < s && j < e) ? ld_ordered(logits + (size_t)tn * e + j) : 0.0f;
     }
     int sel_id;
     float g;

@@ -149,7 +149,7 @@ __device__ __forceinline__ bool topk_token_thread(const float* __restrict__ row,
 #pragma unroll
     for (int q = 0; q < EM / 4; ++q)
       if (4 * q < e) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(row) + q);
+        const float4 f = ld_ordered(reinterpret_cast<const float4*>(row) + q);
         v[4 * q] = f.x;
         v[4 * q + 1] = f.y;
         v[4 * q + 2] = f.z;
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool topk_token_thread(const float* __restrict__ row,
   } else {
 #pragma unroll
     for (int j = 0; j < EM; ++j)
-      if (j < e) v[j] = __ldg(row + j);
+      if (j < e) v[j] = ld_ordered(row + j);
   }
   bool bad = false;
   uint32_t key[32];

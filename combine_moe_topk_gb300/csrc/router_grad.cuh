@@ -55,7 +55,7 @@ __device__ __forceinline__ void router_grad_token(int t, int lane, int k, int e,
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const int x = lane + 32 * i;
-      v[i] = x < e ? __ldg(l + x) : -INFINITY;
+      v[i] = x < e ? ld_ordered(l + x) : -INFINITY;
       mx = fmaxf(mx, v[i]);
     }
 #pragma unroll

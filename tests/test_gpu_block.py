@@ -116,3 +116,58 @@ def test_autograd_wrappers_return_what_was_asked_for():
     xx = x.clone().requires_grad_()
     A.layernorm(xx, w).mean(0).sum().backward()
     assert np.isfinite(xx.grad.float().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("s,e,k", [(300, 8, 2), (2048, 64, 6), (40, 128, 8)])
+def test_whole_chain_in_a_graph_equals_calls_one_by_one(s, e, k):
+    """Every call of a block's forward and backward back to back in a captured graph, replayed on new inputs,
+    against the same calls with the device idle between them: no kernel reads before its forerunner has written."""
+    m = 256
+    g = torch.Generator().manual_seed(5)
+    mk = lambda *shape: torch.randn(*shape, generator=g).bfloat16().cuda()  # noqa: E731
+    x, dy, Wr, W1, W2 = mk(s, m), mk(s, m), mk(e, m) * 0.1, mk(384, m) * 0.06, mk(m, 384) * 0.05
+    nw, nb = torch.ones(m, device="cuda"), torch.zeros(m, device="cuda")
+    dloss = torch.tensor([0.1, 0.01], device="cuda")
+    cap = B.moe_capacity(1.25, s, k, e)
+    h_graph, h_eager = (B.moe_layout_create(s, e, k, capacity=cap) for _ in range(2))
+
+    def chain(handle, wait):
+        out = []
+
+        def do(r):
+            out.extend(t for t in (r if isinstance(r, tuple) else (r,)) if torch.is_tensor(t))
+            if wait:
+                torch.cuda.synchronize()
+            return r
+
+        hn, mean, rstd = do(B.moe_layernorm(x, nw, nb))
+        logits = do(B.moe_linear(hn, Wr, out_dtype=torch.float32))
+        idx, gate = do(B.moe_topk_gate_layout(handle, logits))
+        bl = do(B.moe_balance_loss(logits, idx))
+        X = do(B.moe_dispatch(handle, hn))
+        routed = do(B.moe_combine(handle, X, gate))
+        u, z = do(B.moe_linear(hn, W1, act="silu", save_z=True))
+        do(B.moe_linear(u, W2, residual=routed))
+        dY, dgate = do(B.moe_combine_bwd(handle, dy, gate, X))
+        dl = do(B.moe_topk_gate_bwd(logits, idx, gate, dgate, e))
+        dl = do(B.moe_balance_loss_bwd(logits, bl.lse, bl.coef, bl.norm, dloss, add=dl))
+        dh0 = do(B.moe_dispatch_bwd(handle, dY))
+        du, _, _ = do(B.moe_linear_bwd(dy, u, W2))
+        do(B.moe_linear_bwd(du, hn, W1, z, "silu"))
+        do(B.moe_linear_bwd(dl, hn, Wr))
+        do(B.moe_layernorm_bwd(dh0, x, nw, mean, rstd, dres=dy))
+        return out
+
+    chain(h_graph, True)  # one-time set-up before the capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(h_graph, False)
+    for seed in range(4):
+        x.copy_(torch.randn(s, m, generator=torch.Generator().manual_seed(50 + seed)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        have = [t.clone() for t in got]
+        want = chain(h_eager, True)
+        assert len(have) == len(want)
+        for i, (a, c) in enumerate(zip(have, want)):
+            assert torch.equal(a, c), i
