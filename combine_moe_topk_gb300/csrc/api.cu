@@ -1026,7 +1026,7 @@ moe_status moe_layernorm(int s, int m, moe_dtype dtype, const void* x, int64_t l
 
 size_t moe_layernorm_bwd_workspace(int s, int m) {
   if (s < 1 || m < 1) return 0;
-  return 2 * sizeof(float) * (size_t)moe::layernorm_bwd_parts(s) * (size_t)m;
+  return 2 * sizeof(float) * (size_t)moe::layernorm_bwd_parts(s) * (size_t)((m + 7LL) / 8 * 8);
 }
 
 moe_status moe_layernorm_bwd(int s, int m, moe_dtype dtype, const void* dy, int64_t lddy, const void* x, int64_t ldx,

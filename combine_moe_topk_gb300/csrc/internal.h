@@ -167,7 +167,8 @@ cudaError_t launch_layernorm(const void* x, long long ldx, int s, int m, int dty
 
 // Partial rows of the weight gradients: at most this many blocks write one.
 inline int layernorm_bwd_parts(int s) { return s < 640 ? s : 640; }
-// part: f32 [2][layernorm_bwd_parts(s)][m] scratch, needed when dw or db is wanted.
+// part: f32 [2][layernorm_bwd_parts(s)][m up to a multiple of 8] scratch, needed
+// when dw or db is wanted.
 cudaError_t launch_layernorm_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* dres,
                                  long long lddres, int s, int m, int dtype, const void* w, int w_dtype,
                                  const float* mean, const float* rstd, void* dx, float* dw, float* db, float* part,
@@ -184,9 +185,9 @@ cudaError_t launch_balance_bwd(const float* logits, const float* lse, const floa
                                const float* dloss, const uint8_t* valid, const int32_t* offsets, const float* add,
                                int s, int e, int B, float* dlogits, cudaStream_t st);
 
-// out[c] = sum over q < parts of part[q][c] for two arrays (part, then
-// part + stride_parts * m), [m] f32 each, either may be NULL; fixed order.
-cudaError_t launch_sum_parts(const float* part, int parts, int stride_parts, int m, float* out0, float* out1,
+// out[c] = sum over q < parts of part[q][c], c < m, for two arrays of rows of mp
+// floats (part, then part + stride_parts * mp), either out may be NULL; fixed order.
+cudaError_t launch_sum_parts(const float* part, int parts, int stride_parts, int m, int mp, float* out0, float* out1,
                              cudaStream_t st);
 
 // --- dense products with an epilogue ------------------------------------------

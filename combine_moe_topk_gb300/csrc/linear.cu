@@ -1341,7 +1341,7 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
     else err = a.dy_f32 ? run_slope<1, true>(p, a.act, rows, st) : run_slope<1, false>(p, a.act, rows, st);
     if (err != cudaSuccess) return err;
     if (a.db) {
-      err = launch_sum_parts(p.part, rows, 0, a.N, a.db, nullptr, st);
+      err = launch_sum_parts(p.part, rows, 0, a.N, a.N, a.db, nullptr, st);
       if (err != cudaSuccess) return err;
     }
   }
