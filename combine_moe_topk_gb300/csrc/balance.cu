@@ -518,8 +518,8 @@ Shape shape_of(int e) {
   return h;
 }
 
-// Tokens of a block: at least one round of every warp, and not much more
-// than four blocks an SM.
+// Tokens of a block: at least one round of every warp, in at most
+// kBalanceBlocks blocks, two an SM.
 int chunk_of(int s, const Shape& h) {
   const int round = kWarps * (32 / h.L);
   long long c = ((long long)s + kBalanceBlocks - 1) / kBalanceBlocks;

@@ -12,15 +12,15 @@
 // next rows on their way while one is worked on.
 // Where all rows start on 16 bytes a thread copies and reads only its own
 // chunks, and the ring needs no barrier.  Otherwise (kShift: an odd width, a
-// strided view) it depends on the type:
-//   bf16  a stage holds the aligned 16-byte pieces that cover the row, a chunk is
-//         cut out of two of them by the row's own offset, and results go back
-//         through shared memory the same way; that takes two barriers a row more
-//         (2791 x 2815 forward 13.6 us, backward 26.6; two elements at a time,
-//         without barriers, 20.5 and 40.0).
-//   fp32  a chunk is two single elements, copied and stored 4 bytes a lane, which
-//         whole warps still coalesce (forward 15.1 us, backward 30.2; cut out of
-//         pieces 17.2 and 38.6).
+// strided view) a stage holds the aligned 16-byte pieces that cover the row, and
+// a barrier stands between their copies and the reads.  Then it depends on the type:
+//   bf16  a chunk is cut out of two pieces by the row's own offset, and results
+//         go back through shared memory the same way, another barrier
+//         (2791 x 2815 forward 13.6 us, backward 26.5; two elements at a time,
+//         copied 4 bytes a lane without barriers, 20.5 and 40.0).
+//   fp32  a chunk is two single elements, read and stored 4 bytes a lane, without
+//         bank conflicts and coalesced (forward 12.8 us, backward 25.6; copied 4
+//         bytes a lane too 15.1 and 29.8, cut out of pieces 17.2 and 38.6).
 // The variance is taken around the mean (a second reduction over the
 // registers), not as E[x^2] - mu^2, which cancels on rows with a large common
 // offset.  All statistics and sums are fp32; each output is rounded once.
@@ -46,13 +46,9 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// cp.async of 16 or 4 bytes to shared memory, of which n are read (the rest: zeros).
-template <int kBytes>
+// cp.async of 16 bytes to shared memory, of which n are read (the rest: zeros).
 __device__ __forceinline__ void async_copy(uint32_t dst, const void* src, int n) {
-  if (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // All but the newest n groups of this thread have landed.
@@ -185,30 +181,37 @@ __device__ __forceinline__ float group_sum(float a, float2* slot, int gw, int gr
 
 constexpr int threads_of(int G) { return 32 * (G < 8 ? 8 : G); }  // a block: one group, or several small ones
 
+// Copies the 16 bytes `at` bytes into the aligned pieces that cover a row (zeros
+// past its end, or all where `there` is false).
+template <typename T>
+__device__ __forceinline__ void fetch_piece(uint8_t* img, const T* row, int at, int m, bool there) {
+  const int off = skew(row), n = there ? min(16, max(0, off + m * (int)sizeof(T) - at)) : 0;
+  const uint8_t* start = reinterpret_cast<const uint8_t*>(row) - off;
+  async_copy(smem_addr(img + at), n > 0 ? start + at : start, n);
+}
+
 // How a group's threads share a row: chunks of C values, their places in
 // shared memory (kSlots pieces of 16 bytes a row and group) and in the row.
 template <typename T, int E, int G, bool kShift>
 struct Form {
   static constexpr int C = 16 / (int)sizeof(T), kChunks = E;
   static constexpr int kThreads = threads_of(G), kGroups = kThreads / (32 * G), kSpan = 32 * G;
-  static constexpr bool kCut = kShift;  // chunks cut out of two pieces: one piece more than chunks
+  static constexpr bool kCut = kShift;  // a chunk is not one piece: one piece more than chunks, read by other threads
+  static constexpr bool kPut = kShift;  // results go through shared memory
   static constexpr int kSlots = E * kSpan + (kCut ? 1 : 0);
   static constexpr int kRow = kGroups * kSlots * 16;                   // bytes of one row of each group
-  static constexpr int kOut = kCut ? kGroups * (kSlots + 1) * 16 : 0;  // and of its results
+  static constexpr int kOut = kPut ? kGroups * (kSlots + 1) * 16 : 0;  // and of its results
 
   // Column of value j of this thread's chunk i.
   __device__ __forceinline__ static int col(int t, int i, int j) { return (t + i * kSpan) * C + j; }
-  // Copies of piece i < kPieces of a row (zeros where `there` is false or the row ends).
   static constexpr int kPieces = E + (kCut ? 1 : 0);
+  // Copies of piece i < kPieces of a row (zeros where `there` is false or the row ends).
   __device__ __forceinline__ static void fetch(uint8_t* img, const T* row, int t, int i, int m, bool there) {
     if constexpr (kCut) {
-      const int off = skew(row), at = (i * kSpan + t) * 16;
-      const int n = there ? min(16, max(0, off + m * (int)sizeof(T) - at)) : 0;
-      const uint8_t* start = reinterpret_cast<const uint8_t*>(row) - off;
-      if (i < E || t == 0) async_copy<16>(smem_addr(img + at), n > 0 ? start + at : start, n);
+      if (i < E || t == 0) fetch_piece(img, row, (i * kSpan + t) * 16, m, there);
     } else {
       const bool in = there && col(t, i, 0) < m;
-      async_copy<16>(smem_addr(img + (i * kSpan + t) * 16), in ? row + col(t, i, 0) : row, in ? 16 : 0);
+      async_copy(smem_addr(img + (i * kSpan + t) * 16), in ? row + col(t, i, 0) : row, in ? 16 : 0);
     }
   }
   // Chunk i of this thread, as floats.
@@ -229,7 +232,7 @@ struct Form {
     for (int h = 0; h < C / 4; ++h)
       *reinterpret_cast<uint4*>(row + col(t, i, 4 * h)) = Vec<float>::from_float(f + 4 * h);
   }
-  // kCut: chunk i of the results into the group's output pieces (one piece of
+  // kPut: chunk i of the results into the group's output pieces (one piece of
   // room before them), and, after a barrier, those to the row.
   __device__ __forceinline__ static void put(uint8_t* img, int t, int i, const float* f) {
     reinterpret_cast<uint4*>(img)[i * kSpan + t + 1] = Vec<T>::from_float(f);
@@ -262,19 +265,17 @@ template <int E, int G>
 struct Form<float, E, G, true> {
   static constexpr int C = 2, kChunks = 2 * E;
   static constexpr int kThreads = threads_of(G), kGroups = kThreads / (32 * G), kSpan = 32 * G;
-  static constexpr bool kCut = false;
-  static constexpr int kSlots = E * kSpan, kRow = kGroups * kSlots * 16, kOut = 0;
+  static constexpr bool kCut = true, kPut = false;
+  static constexpr int kSlots = E * kSpan + 1, kRow = kGroups * kSlots * 16, kOut = 0;
 
   __device__ __forceinline__ static int col(int t, int i, int j) { return t + (2 * i + j) * kSpan; }
-  static constexpr int kPieces = 4 * E;
+  static constexpr int kPieces = E + 1;
   __device__ __forceinline__ static void fetch(uint8_t* img, const float* row, int t, int i, int m, bool there) {
-    const int c = t + i * kSpan;
-    const bool in = there && c < m;
-    async_copy<4>(smem_addr(img + c * 4), in ? row + c : row, in ? 4 : 0);
+    if (i < E || t == 0) fetch_piece(img, row, (i * kSpan + t) * 16, m, there);
   }
-  __device__ __forceinline__ static void get(const uint8_t* img, int, int t, int i, float* f) {
+  __device__ __forceinline__ static void get(const uint8_t* img, int off, int t, int i, float* f) {
 #pragma unroll
-    for (int j = 0; j < C; ++j) f[j] = reinterpret_cast<const float*>(img)[col(t, i, j)];
+    for (int j = 0; j < C; ++j) f[j] = reinterpret_cast<const float*>(img + off)[col(t, i, j)];
   }
   __device__ __forceinline__ static void store(float* row, int t, int i, int m, const float* f) {
 #pragma unroll
@@ -298,11 +299,9 @@ int ring_depth(size_t stage, size_t beside, int per_sm, int most) {
   return depth;
 }
 
-// Blocks a SM of the forward kernel, which hold its registers down: four of 256
-// threads (16384 x 4096 bf16: 57 us with three, 42 with four), three for single
-// elements, which would spill more with four (2791 x 2815 fp32: 17 against 26 us
-// at first).
-constexpr int fwd_blocks(bool singles, int G) { return G == 32 ? 1 : (singles ? 768 : 1024) / threads_of(G); }
+// Blocks a SM of the forward kernel, four of 256 threads, which hold its
+// registers down (16384 x 4096 bf16: 57 us with three, 42 with four).
+constexpr int fwd_blocks(int G) { return G == 32 ? 1 : 1024 / threads_of(G); }
 
 struct NormFwd {
   const void* x;
@@ -319,7 +318,7 @@ struct NormFwd {
 // Weights and biases stay in registers (with 32 warps a group they are read
 // again for every row, from L1).
 template <typename T, int E, int G, bool kShift>
-__global__ void __launch_bounds__(threads_of(G), fwd_blocks(kShift && sizeof(T) == 4, G)) layernorm_kernel(const NormFwd p, const int depth) {
+__global__ void __launch_bounds__(threads_of(G), fwd_blocks(G)) layernorm_kernel(const NormFwd p, const int depth) {
   typedef Form<T, E, G, kShift> F;
   constexpr int C = F::C, kChunks = F::kChunks, groups = F::kGroups, span = F::kSpan, kPairs = kChunks * C / 2;
   constexpr bool kKeepW = G < 32;
@@ -407,11 +406,11 @@ __global__ void __launch_bounds__(threads_of(G), fwd_blocks(kShift && sizeof(T) 
             for (int j = 0; j < C; ++j) v.f[i * C + j] += a[j];
           }
         }
-        if constexpr (F::kCut) F::put(out, t, i, v.f + i * C);
+        if constexpr (F::kPut) F::put(out, t, i, v.f + i * C);
         else F::store(y, t, i, p.m, v.f + i * C);
       }
     }
-    if constexpr (F::kCut) {  // the barriers of the next row come before the next put
+    if constexpr (F::kPut) {  // the barriers of the next row come before the next put
       group_sync<G>(group);
       F::write(out, y, t, p.m);
     }
@@ -635,12 +634,12 @@ __global__ void __launch_bounds__(threads_of(G), bwd_blocks(G)) layernorm_bwd_ke
           g.p2[j] = p.dres ? add2(o, add.p2[j]) : o;
         }
         if (F::col(t, i, 0) < p.m) {
-          if constexpr (F::kCut) F::put(out + u * F::kOut, t, i, g.f);
+          if constexpr (F::kPut) F::put(out + u * F::kOut, t, i, g.f);
           else F::store(dx_row, t, i, p.m, g.f);
         }
       }
     }
-    if constexpr (F::kCut) {  // the barriers of the next rows come before the next put
+    if constexpr (F::kPut) {  // the barriers of the next rows come before the next put
       group_sync<G>(group);
 #pragma unroll
       for (int u = 0; u < R; ++u)
@@ -759,7 +758,7 @@ int chunks_per_group(int chunks, int G) { return (chunks + 32 * G - 1) / (32 * G
 template <typename T, int E, int G, bool kShift>
 cudaError_t run_fwd(const NormFwd& p, const DeviceInfo& di, cudaStream_t st) {
   typedef Form<T, E, G, kShift> F;
-  constexpr int per_sm = fwd_blocks(kShift && sizeof(T) == 4, G);
+  constexpr int per_sm = fwd_blocks(G);
   static OncePerDevice once;
   cudaError_t err = once.run([] {
     return cudaFuncSetAttribute(layernorm_kernel<T, E, G, kShift>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
