@@ -147,36 +147,40 @@ __device__ __forceinline__ void load8(const void* p, int is_f32, long long i, fl
   }
 }
 
-__device__ __forceinline__ void load_bias8(const Epi& e, int col, int N, float* b) {
+// Four, aligned to their size (`whole`), or one by one, those from `n` on as n - 1.
+__device__ __forceinline__ void load4(const void* p, int is_f32, long long i, bool whole, int n, float* f) {
+  if (!whole) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = 0.f;
-  if (e.bias && col < N) load8(e.bias, e.bias_f32, col, b);
-}
-
-// Bias, activation and residual of columns col .. col+7 of row `row`, by
-// 16-byte accesses (e.wide); each output is rounded once, from fp32.
-__device__ __forceinline__ void finish8(const Epi& e, long long row, int col, int N, float* f, const float* bias) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] += bias[j];
-  const long long at = row * N + col;
-  if (e.z) *reinterpret_cast<uint4*>(e.z + at) = Vec<bf16>::from_float(f);
-  activate<8>(f, e.act);
-  if (e.res) {
-    float r[8];
-    load8(e.res, e.res_f32, row * e.ldres + col, r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] += r[j];
-  }
-  if (e.out_f32) {
-    uint4* o = reinterpret_cast<uint4*>(static_cast<float*>(e.out) + at);
-    o[0] = Vec<float>::from_float(f);
-    o[1] = Vec<float>::from_float(f + 4);
+    for (int j = 0; j < 4; ++j) f[j] = load_any(p, is_f32, i + min(j, n - 1));
+  } else if (is_f32) {
+    Vec<float>::to_float(ld_plain(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i)), f);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<bf16*>(e.out) + at) = Vec<bf16>::from_float(f);
+    const uint2 u = ld_plain(reinterpret_cast<const uint2*>(static_cast<const bf16*>(p) + i));
+    f[0] = __uint_as_float(u.x << 16);
+    f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16);
+    f[3] = __uint_as_float(u.y & 0xffff0000u);
   }
 }
 
-// The same for one value.
+__device__ __forceinline__ void store4(void* p, int is_f32, long long i, bool whole, int n, const float* f) {
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= n) continue;
+      if (is_f32) static_cast<float*>(p)[i + j] = f[j];
+      else static_cast<bf16*>(p)[i + j] = __float2bfloat16_rn(f[j]);
+    }
+  } else if (is_f32) {
+    *reinterpret_cast<uint4*>(static_cast<float*>(p) + i) = Vec<float>::from_float(f);
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2*>(static_cast<bf16*>(p) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// Bias, activation and residual of one value.
 __device__ __forceinline__ void finish1(const Epi& e, long long row, int col, int N, float f) {
   const long long at = row * N + col;
   if (e.bias) f += load_any(e.bias, e.bias_f32, col);
@@ -570,6 +574,76 @@ __device__ __forceinline__ uint4 ld_cluster(uint32_t addr) {
   return v;
 }
 
+// The rows of a split tile that each of its S CTAs finishes: an equal share of
+// those that exist.
+__device__ __forceinline__ int rows_of_share(int m0, int M, int S) { return (min(128, M - m0) + S - 1) / S; }
+
+// This CTA's share of a split tile.  A warp reads 512 consecutive bytes of one
+// part at a time; each CTA starts with its own part and goes round, so that the
+// CTAs of a cluster do not all read one SM's memory at once (a row's parts are
+// added in an order that only its place fixes).  Everything that is read
+// travels at once, bias and residual before the cluster's barrier.  64 x 4096 x
+// 4096, four parts: 14.3 -> 11.9 us (in 32-byte pieces, one part at a time, the
+// join had taken 7 of 23 thousand cycles).  Ends with this CTA's arrival at the
+// barrier after which the parts may go.
+template <int S, int BN>
+__device__ __forceinline__ void join_parts(const GemmArgs& p, const Unit& t, int split, const uint8_t* parts) {
+  constexpr int kGroups = BN / 4, kRounds = (128 / S * kGroups + kThreads - 1) / kThreads;
+  const Epi& e = p.epi;
+  const int per = rows_of_share(t.m0, p.M, S), end = min(min(128, p.M - t.m0), (split + 1) * per);
+  float bias[kRounds][4], res[kRounds][4], f[kRounds][4];
+  bool there[kRounds];
+  auto row_of = [&](int j) { return split * per + (int)(threadIdx.x + j * kThreads) / kGroups; };
+  auto col_of = [&](int j) { return (int)(threadIdx.x + j * kThreads) % kGroups * 4; };
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    const int row = row_of(j), col = t.n0 + col_of(j);
+    there[j] = row < end && col < p.N;
+    if (there[j] && e.bias) load4(e.bias, e.bias_f32, col, e.wide, p.N - col, bias[j]);
+    if (there[j] && e.res) load4(e.res, e.res_f32, (t.m0 + row) * e.ldres + col, e.wide, p.N - col, res[j]);
+  }
+  cluster_sync_all();  // every part is in its CTA's shared memory
+  uint4 v[kRounds][S];
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    const uint8_t* own = parts + min(row_of(j), 127) * Shape<1, BN>::kPartRow + col_of(j) * 4;
+    if (there[j]) {
+      v[j][0] = *reinterpret_cast<const uint4*>(own);
+#pragma unroll
+      for (int s = 1; s < S; ++s) v[j][s] = ld_cluster(mapa_shared(smem_addr(own), (split + s) & (S - 1)));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    Vec<float>::to_float(v[j][0], f[j]);
+#pragma unroll
+    for (int s = 1; s < S; ++s) {
+      float g[4];
+      Vec<float>::to_float(v[j][s], g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[j][i] += g[i];
+    }
+  }
+  cluster_arrive();
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    if (!there[j]) continue;
+    const int col = t.n0 + col_of(j), n = p.N - col;
+    const long long at = (long long)(t.m0 + row_of(j)) * p.N + col;
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[j][i] += bias[j][i];
+    }
+    if (e.z) store4(e.z, 0, at, e.wide, n, f[j]);
+    activate<4>(f[j], e.act);
+    if (e.res) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[j][i] += res[j][i];
+    }
+    store4(e.out, e.out_f32, at, e.wide, n, f[j]);
+  }
+}
+
 // kExact (fp32 outputs): the tensor cores' accumulator drops the bits below
 // its last place at every step (measured: 4.4e-6 of the result over 4096
 // terms, against 6e-7 for fp32 additions), so a product hands its sum over
@@ -767,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit t = unit_of<CG, BN>(u, split, p);
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew, n0 = t.n0 + half * (BN / 2);
       if constexpr (kSplit) {  // for the rows that this CTA will finish
-        const int rows = 128 / p.splits, i = threadIdx.x - 128;
+        const int rows = rows_of_share(t.m0, p.M, p.splits), i = threadIdx.x - 128;
         if (i < rows) prefetch_residual(p.epi, t.m0 + split * rows + i, t.n0, BN, p.M, p.N);
       } else {
         prefetch_residual(p.epi, r0 + lane, n0, BN / 2, p.M, p.N);
@@ -857,37 +931,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if constexpr (kSplit) {
-    cluster_sync_all();  // every part is in its CTA's shared memory
     const Unit t = unit_of<CG, BN>(worker, split, p);
-    const int rows = 128 / p.splits, groups = BN / 8;
-    const uint32_t base = smem_addr(smem);
-    for (int q = threadIdx.x; q < rows * groups; q += kThreads) {
-      const int r = split * rows + q / groups, col = t.n0 + (q % groups) * 8, row = t.m0 + r;
-      if (row >= p.M || col >= p.N) continue;
-      float f[8], bias[8];
-      if (p.epi.wide) load_bias8(p.epi, col, p.N, bias);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = 0.f;
-      const uint32_t at = base + r * S::kPartRow + (col - t.n0) * 4;
-      for (int sp = 0; sp < p.splits; sp += 2) {  // an even number; both loads in flight
-        const uint32_t from0 = mapa_shared(at, sp), from1 = mapa_shared(at, sp + 1);
-        const uint4 v[4] = {ld_cluster(from0), ld_cluster(from0 + 16), ld_cluster(from1), ld_cluster(from1 + 16)};
-        float g[16];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) Vec<float>::to_float(v[h], g + 4 * h);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] + g[j] + g[8 + j];
-      }
-      if (p.epi.wide) {
-        finish8(p.epi, row, col, p.N, f, bias);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (col + j < p.N) finish1(p.epi, row, col + j, p.N, f[j]);
-      }
+    switch (p.splits) {
+      case 2: join_parts<2, BN>(p, t, split, smem); break;
+      case 4: join_parts<4, BN>(p, t, split, smem); break;
+      default: join_parts<8, BN>(p, t, split, smem); break;
     }
+    cluster_wait();  // nobody reads this CTA's part any more
   }
-  if constexpr (CG == 2 || kSplit) cluster_sync_all();
+  if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   if (warp == 2) {
     if constexpr (CG == 2)
