@@ -653,10 +653,9 @@ constexpr int kExactBlocks = 4;
 // kSplit (CG = 1): where tiles are too few to fill the machine, a cluster of
 // 2, 4 or 8 CTAs shares one, each with its part of the contracted axis.  They
 // leave their fp32 sums in their shared memory, and each finishes an equal
-// share of the tile's rows, adding the parts in order through distributed
-// shared memory.  (Partial products in global memory and a second kernel to add
-// them took the same time on the device, within 10 % either way, but another
-// launch and a workspace.)
+// share of the tile's rows (join_parts).  Partial products in global memory and
+// a second kernel to add them took 13 to 16 us at 64 x 4096 x 4096 (11.9 this
+// way), another launch and a workspace.
 template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -1241,14 +1240,16 @@ constexpr int kPlanSms = 152;  // plans are made for a whole GB300
 // widest tile (0.65 us).  Measured: a K block of a 128 x 128 tile takes 0.70 of
 // that and of 128 x 64 0.66 (both wait for shared memory, so the wide tile wins
 // wherever it fills the machine: 9728 x 4096 x 4096 172.8, 243.3, 457.1 us);
-// a launch's fixed part is 6.9, 5.9 and 4.7 us, a split's exchange 3.4 us.  So
-// 512 x 4096 x 4096 goes to 128 x 128 (20.7 us against 26.9 and 32.5), 64 rows
-// of it to four parts of 128 x 128 (14.2, unsplit wide 26.2), 1024^3 to 128 x 64
-// (7.8 against 12.8 and 9.9).
+// a launch's fixed part is 6.9, 5.9 and 4.7 us, a split's join about 2 us.  So
+// 512 x 4096 x 4096 goes to 128 x 128 (22 us against 30 and 34), 64 rows of it to
+// four parts of 128 x 128 (11.8; two 14.8, unsplit 20.2, wide 26.7), 1024^3 to
+// 128 x 64 (7.8 against 12.8 and 9.9), 64 x 1024 x 1024 to four parts of that (5.8;
+// unsplit 6.9).
 Plan plan_gemm(int M, int N, int K, bool exact) {
   const double cost[kKinds] = {1.0, 0.70, 0.66}, base[kKinds] = {9.0, 8.0, 6.0};
-  // clusters of 2, 4 and 8 CTAs that are surely resident at once
-  const int clusters[4] = {0, 72, 34, 16};
+  // clusters of 2, 4 and 8 CTAs that run at once (sixteen of eight did not: 2048 x
+  // 4096 x 128 18.6 us, in four parts 10.2)
+  const int clusters[4] = {0, 72, 34, 8};
   Plan best = {};
   double best_t = 0;
   const int kblocks = (K + 127) / 128;
@@ -1268,7 +1269,7 @@ Plan plan_gemm(int M, int N, int K, bool exact) {
       if ((S - 1) * q.per_split >= kblocks) continue;  // the last part would be empty
       q.splits = S;
       const long long waves = S > 1 ? 1 : (tiles + workers - 1) / workers;
-      const double t = (double)waves * (q.per_split * cost[k] + 1.0) + base[k] + (S > 1 ? 5.0 : 0.0);
+      const double t = (double)waves * (q.per_split * cost[k] + 1.0) + base[k] + (S > 1 ? 3.0 : 0.0);
       if (best.kblocks == 0 || t < best_t) {
         best = q;
         best_t = t;
