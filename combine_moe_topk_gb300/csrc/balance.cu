@@ -352,16 +352,28 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
     s_share[ty] = col < p.e ? (float)p.e * f * P : 0.f;
   }
   __syncthreads();
+  auto write_losses = [&](float loss, float z, float sequences, float count) {
+    const float per_seq = 1.f / fmaxf(sequences, 1.f), per_token = 1.f / fmaxf(count, 1.f);
+    p.loss[0] = loss * per_seq;
+    p.loss[1] = z * per_token;
+    p.norm[0] = per_seq;
+    p.norm[1] = per_token;
+  };
   if (ty == 0) {
     const float share = lanes_sum<32>(s_share[tx]), z = lanes_sum<32>(s_z[tx]);
     if (tx == 0) {
-      p.part[(size_t)b * p.cols + block] = share;
-      if (block == 0) {
-        p.zpart[b] = z;
-        p.tpart[b] = tokens;
+      if (gridDim.x == 1) {  // there is nothing to add to it
+        write_losses(share, z, tokens > 0 ? 1.f : 0.f, (float)tokens);
+        s_last = 0;
+      } else {
+        p.part[(size_t)b * p.cols + block] = share;
+        if (block == 0) {
+          p.zpart[b] = z;
+          p.tpart[b] = tokens;
+        }
+        __threadfence();
+        s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
       }
-      __threadfence();
-      s_last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     }
   }
   grid_dependents_launch();
@@ -384,13 +396,7 @@ __global__ void __launch_bounds__(kJoin) balance_join_kernel(const BalanceJoin p
   __syncthreads();
   if (ty == 0) {
     all = sum4(s_last_sums[tx]);
-    if (tx == 0) {
-      const float per_seq = 1.f / fmaxf(all.z, 1.f), per_token = 1.f / fmaxf(all.w, 1.f);
-      p.loss[0] = all.x * per_seq;
-      p.loss[1] = all.y * per_token;
-      p.norm[0] = per_seq;
-      p.norm[1] = per_token;
-    }
+    if (tx == 0) write_losses(all.x, all.y, all.z, all.w);
   }
 }
 
