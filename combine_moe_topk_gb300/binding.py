@@ -189,6 +189,23 @@ def _raw_stream(t: torch.Tensor):
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
 
 
+# torch's own short way to an uninitialised CUDA tensor on the current device;
+# beside a launch torch.empty takes 3.9 us of host time, this 1.4.
+_strided = getattr(getattr(torch._C, "_dynamo", None) and torch._C._dynamo.guards, "_empty_strided_cuda", None)
+
+
+def _new_here(dtype: torch.dtype, n: int, m: int | None = None) -> torch.Tensor:
+    return _strided((n,), (1,), dtype) if m is None else _strided((n, m), (m, 1), dtype)
+
+
+def _new(t: torch.Tensor):
+    """How outputs beside t are allocated: new(dtype, n) or new(dtype, n, m), contiguous."""
+    if _strided is not None and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
+        return _new_here
+    dev = t.device
+    return lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _stream(device: torch.device):
     # a host tensor still goes to the library, which rejects it; use the current device's stream
     dev = device if device.type == "cuda" else None
@@ -618,19 +635,19 @@ def moe_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: tor
     """x [s,m] f32 or bf16 (rows may be strided), weight and bias [m] f32 or
     bf16 -> (y [s,m], mean f32 [s], rstd f32 [s]); stats=False returns y alone."""
     s, m = _rows2(x, "x")
-    dev, dt = x.device, x.dtype
+    new, dt = _new(x), x.dtype
     wt = weight if weight is not None else bias
     for t in (weight, bias):
         if t is not None and (t.shape != (m,) or t.dtype != wt.dtype):
             raise MoEError(1, "moe_layernorm", "weight and bias must be [m], of one dtype")
     if y is None:
-        y = torch.empty(s, m, dtype=dt, device=dev)
+        y = new(dt, s, m)
     elif y.shape != (s, m) or y.dtype != dt:
         raise MoEError(1, "moe_layernorm", "output shape")
     mean = rstd = None
     if stats:
-        mean = torch.empty(s, dtype=torch.float32, device=dev)
-        rstd = torch.empty(s, dtype=torch.float32, device=dev)
+        mean = new(torch.float32, s)
+        rstd = new(torch.float32, s)
     px, ldx = _rows_ptr(x)
     rc = lib().moe_layernorm(s, m, _DTYPE.get(dt, -1), px, ldx, 0 if wt is None else _DTYPE.get(wt.dtype, -1),
                              _addr(weight), _addr(bias), eps, _addr(y), _addr(mean), _addr(rstd), _raw_stream(x))
@@ -646,7 +663,7 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | 
     dweight f32 [m] or None, dbias f32 [m] or None).  dres [s,m]: a gradient
     that reaches x past the norm (the residual branch), added to dx."""
     s, m = _rows2(x, "x")
-    dev, dt = x.device, x.dtype
+    new, dt = _new(x), x.dtype
     for t in (dy, dres, dx):
         if t is not None and (t.shape != (s, m) or t.dtype != dt):
             raise MoEError(1, "moe_layernorm_bwd", "dy, dres and dx must have x's shape and dtype")
@@ -655,13 +672,13 @@ def moe_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | 
     if weight is not None and weight.shape != (m,):
         raise MoEError(1, "moe_layernorm_bwd", "weight must be [m]")
     if dx is None:
-        dx = torch.empty(s, m, dtype=dt, device=dev)
-    dw = torch.empty(m, dtype=torch.float32, device=dev) if need_dweight else None
-    db = torch.empty(m, dtype=torch.float32, device=dev) if need_dbias else None
+        dx = new(dt, s, m)
+    dw = new(torch.float32, m) if need_dweight else None
+    db = new(torch.float32, m) if need_dbias else None
     L, nbytes, ws = lib(), 0, None
     if need_dweight or need_dbias:
         nbytes = L.moe_layernorm_bwd_workspace(s, m)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = new(torch.uint8, nbytes)
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)
     pres, ldres = _rows_ptr(dres)
@@ -704,15 +721,15 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.
     if topk_idx.dim() != 2 or topk_idx.dtype != torch.int32 or topk_idx.shape[0] != s:
         raise MoEError(1, "moe_balance_loss", "topk_idx must be int32 [s, k]")
     n = _check_balance("moe_balance_loss", s, logits, valid, seq_offsets)
-    dev, f32, L = logits.device, torch.float32, lib()
-    loss = torch.empty(2, dtype=f32, device=dev)
-    counts = torch.empty(n, e, dtype=torch.int32, device=dev)
-    mean_prob = torch.empty(n, e, dtype=f32, device=dev)
-    lse = torch.empty(s, dtype=f32, device=dev)
-    coef = torch.empty(n, e, dtype=f32, device=dev)
-    norm = torch.empty(2, dtype=f32, device=dev)
+    new, f32, L = _new(logits), torch.float32, lib()
+    loss = new(f32, 2)
+    counts = new(torch.int32, n, e)
+    mean_prob = new(f32, n, e)
+    lse = new(f32, s)
+    coef = new(f32, n, e)
+    norm = new(f32, 2)
     nbytes = L.moe_balance_loss_workspace(e, n)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = new(torch.uint8, nbytes)
     rc = L.moe_balance_loss(_addr(logits), _addr(topk_idx), _addr(valid), _addr(seq_offsets), s, e, topk_idx.shape[1],
                             n, loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(), lse.data_ptr(),
                             coef.data_ptr(), norm.data_ptr(), ws.data_ptr(), nbytes, _addr(device_status),
@@ -736,7 +753,7 @@ def moe_balance_loss_bwd(logits: torch.Tensor, lse: torch.Tensor, coef: torch.Te
         if t is not None and (t.shape != shape or t.dtype != f32):
             raise MoEError(1, "moe_balance_loss_bwd", f"{name} must be float32 {list(shape)}")
     if dlogits is None:
-        dlogits = torch.empty(s, e, dtype=f32, device=logits.device)
+        dlogits = _new(logits)(f32, s, e)
     rc = lib().moe_balance_loss_bwd(_addr(logits), _addr(lse), _addr(coef), _addr(norm), _addr(dloss), _addr(valid),
                                     _addr(seq_offsets), _addr(add), s, e, n, _addr(dlogits), _raw_stream(logits))
     if rc:
@@ -765,16 +782,16 @@ def moe_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     gelu, gelu_tanh, silu.  save_z: return (y, z), z bf16 [s,N] the value
     before the activation, for moe_linear_bwd."""
     s, K, N = _check_linear("moe_linear", x, W, act)
-    dev = x.device
+    new = _new(x)
     if bias is not None and bias.shape != (N,):
         raise MoEError(1, "moe_linear", "bias must be [N]")
     if residual is not None and residual.shape != (s, N):
         raise MoEError(1, "moe_linear", "residual must be [s, N]")
     if y is None:
-        y = torch.empty(s, N, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+        y = new(torch.bfloat16 if out_dtype is None else out_dtype, s, N)
     elif y.shape != (s, N) or (out_dtype is not None and y.dtype != out_dtype):
         raise MoEError(1, "moe_linear", "output shape or dtype")
-    z = torch.empty(s, N, dtype=torch.bfloat16, device=dev) if save_z else None
+    z = new(torch.bfloat16, s, N) if save_z else None
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
     pres, ldres = _rows_ptr(residual)
@@ -794,19 +811,19 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     activation) -> (dx [s,K], dW [N,K], db f32 [N]), None for those not
     needed.  The residual's gradient is dy itself."""
     s, K, N = _check_linear("moe_linear_bwd", x, W, act)
-    dev = x.device
+    new = _new(x)
     if dy.shape != (s, N):
         raise MoEError(1, "moe_linear_bwd", "dy must be [s, N]")
     if act == "none":
         z = None
     elif z is None or z.shape != (s, N) or z.dtype != torch.bfloat16:
         raise MoEError(1, "moe_linear_bwd", "z must be bf16 [s, N] with an activation")
-    dx = torch.empty(s, K, dtype=dx_dtype, device=dev) if need_dx else None
-    dW = torch.empty(N, K, dtype=dw_dtype, device=dev) if need_dw else None
-    db = torch.empty(N, dtype=torch.float32, device=dev) if need_db else None
+    dx = new(dx_dtype, s, K) if need_dx else None
+    dW = new(dw_dtype, N, K) if need_dw else None
+    db = new(torch.float32, N) if need_db else None
     L = lib()
     nbytes = L.moe_linear_bwd_workspace(s, N)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    ws = new(torch.uint8, nbytes) if nbytes else None
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
