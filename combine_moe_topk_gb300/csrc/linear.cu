@@ -22,6 +22,10 @@
 //   warp 2          TMEM allocation
 //   warps 4..11     epilogue, two warps for each quarter of the TMEM lanes,
 //                   from one of two accumulators while the other fills
+// Bound by the tensor cores where both sides are long (8192 x 4096 x 16384 558 us,
+// 1.97 PFLOP/s; 8192 x 4096 x 4096 146, backward dx 146, dW 164 us), by what an SM
+// takes in where one is short (16384 x 4096 x 128 28.5 us), by the weights' bytes
+// and the launch where rows are few (64 x 4096 x 4096 11.9 us).
 // Every mbarrier wait is bounded on the global timer; a time-out records
 // MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
 #include "common.cuh"
@@ -975,7 +979,8 @@ struct FewArgs {
 // share of W to within a row.  W comes through a deep ring in shared memory (a
 // stage: 8 rows x 2048 of the contracted axis, a bulk copy a row), which keeps
 // up to 190 KB an SM in flight from the first microsecond on; loads into
-// registers, 128 bytes a thread, had reached 2.9 TB/s at 4096 x 4096 (11.6 us).  The rows
+// registers, 128 bytes a thread, had reached 2.9 TB/s at 4096 x 4096 (11.6 us; this
+// way 8.8, and 23.8 us, 5.6 TB/s, at 16384 x 4096).  The rows
 // of x take the same way, a stage or two before the chunk's W.
 //   warp 8          producer: lane r copies row r of a stage
 //   warps 0..7      every eighth 32 of the contracted axis, by warp-level MMA

@@ -21,6 +21,9 @@
 //   fp32  a chunk is two single elements, read and stored 4 bytes a lane, without
 //         bank conflicts and coalesced (forward 12.8 us, backward 25.6; copied 4
 //         bytes a lane too 15.1 and 29.8, cut out of pieces 17.2 and 38.6).
+// Measured, 16384 x 4096 bf16: forward 42.5 us (6.3 TB/s), backward with the
+// residual branch's gradient 84.2 us (6.4 TB/s), of which the weight gradients
+// are 5; one row of 4096 2.6 us.
 // The variance is taken around the mean (a second reduction over the
 // registers), not as E[x^2] - mu^2, which cancels on rows with a large common
 // offset.  All statistics and sums are fp32; each output is rounded once.
