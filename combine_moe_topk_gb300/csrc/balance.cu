@@ -10,7 +10,7 @@
 //   c_bj = e n_bj / (k T_b^2)    (the counts are not differentiable)
 // Both directions read each logit once and are bound by device memory; the
 // forward pass keeps lse (one fp32 a token), so the backward pass needs no
-// reduction for the softmax, only the row's dot product with c.
+// maximum: it takes a row's sum and its dot product with c in one reduction.
 //
 // L lanes share a row (the smallest power of two that covers it with one
 // vector a lane), so a warp works on 32/L rows at once and few experts do
@@ -20,10 +20,10 @@
 // no other piece has.  join_kernel adds each sequence's pieces in block order:
 // no floating-point atomics, so the results are the same on every run.
 //
-// Measured, 256 experts, 131072 tokens, top 8: forward 33.4 us (one sequence) and
+// Measured, 256 experts, 131072 tokens, top 8: forward 33.9 us (one sequence) and
 // 37.8 (37 of them, padding), of which the join's latency is 7 and the blocks'
-// uneven ends 4, the bytes alone 20.7; backward with a gradient added 65 us, its
-// bytes 60.  8192 x 8: 6.4 and 2.4 us.
+// uneven ends 4, the bytes alone 20.7; backward with a gradient added 66 us, its
+// bytes 60.  8192 x 8: 6.7 and 2.6 us.
 #include <float.h>
 #include <math_constants.h>
 
@@ -183,15 +183,15 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
           for (int v = 0; v < V; ++v) top = fmaxf(top, f[u][i][v]);
         top = lanes_max<L>(top);
         const float base = top == -FLT_MAX ? 0.f : top;  // a row of masked experts: every exp below is 0
-        // exp(l - base) as 2^(l log2 e - base log2 e): what the second product's
-        // rounding adds is the same for the whole row and cancels in p
-        const float shift = -base * kLog2e;
+        // subtracted before it is scaled, so that the largest term is 1 whatever the
+        // logits' size (2^(l log2 e - base log2 e) in one fma keeps the rounding of
+        // base log2 e in the exponent: at 1e10 that is hundreds)
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            f[u][i][v] = exp2_approx(fmaf(f[u][i][v], kLog2e, shift));
+            f[u][i][v] = exp2_approx((f[u][i][v] - base) * kLog2e);
             sum += f[u][i][v];
           }
         sum = lanes_sum<L>(sum);
@@ -487,22 +487,27 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * kRows + sub;
-        float dot = 0.f;
+        // lse is rounded to its own last place: past 1e8 nothing of the sum's
+        // logarithm is left in it.  Divided by the row's sum, p has that no more.
+        float dot = 0.f, sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             f[u][i][v] = exp2_approx((f[u][i][v] - lse[u]) * kLog2e);
             dot = fmaf(c[i][v], f[u][i][v], dot);
+            sum += f[u][i][v];
           }
-        dot = lanes_sum<L>(dot);
+        sum = lanes_sum<L>(sum);
+        const float inv = __fdividef(1.f, sum);  // in [1/256, 256]: lse is off by at most log e
+        dot = lanes_sum<L>(dot) * inv;
         const float zt = wz * lse[u];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int q = V * (col + L * i);
           if (some[u]) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) g[u][i][v] = fmaf(f[u][i][v], c[i][v] - dot + zt, g[u][i][v]);
+            for (int v = 0; v < V; ++v) g[u][i][v] = fmaf(f[u][i][v] * inv, c[i][v] - dot + zt, g[u][i][v]);
           }
           if (t < r.y && q < p.e) store_cols<V>(p.dlogits + (size_t)t * p.e + q, g[u][i]);
         }

@@ -496,7 +496,8 @@ size_t moe_balance_loss_workspace(int e, int num_seqs);
  * both 0 when no token is valid.  Also written: counts i32 [num_seqs,e] (n),
  * mean_prob f32 [num_seqs,e] (P), lse f32 [s] (0 for tokens that take no
  * part), and for the backward pass coef f32 [num_seqs,e] = e n_bj / (k T_b^2)
- * and norm f32 [2] = (1/B', 1/T).  Logits of -inf or of fp32's
+ * and norm f32 [2] = (1/B', 1/T).  Any finite logits are taken; past 1.8e19
+ * lse^2, and so loss[1], is an infinity.  Logits of -inf or of fp32's
  * lowest value (-FLT_MAX) are experts masked out (p = 0); a row that a mask
  * leaves nothing of has no probabilities, is left out of the z loss, and its
  * lse is -inf.  device_status (nullable): MOE_DEV_NONFINITE for a NaN or +inf logit
@@ -511,7 +512,9 @@ moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const 
  * [2] (device memory): the gradients that reach loss[0] and loss[1];
  *   dlogits_tj = add_tj + dloss[0] norm[0] p_tj (coef_bj - sum_i coef_bi p_ti)
  *                       + dloss[1] norm[1] 2 lse_t p_tj,
- * p_tj = exp(logits_tj - lse_t); tokens that take no part get add alone.  add
+ * p_tj = exp(logits_tj - lse_t) over the row's sum of these (lse is an fp32,
+ * which at 1e8 and more keeps nothing of the sum's logarithm; p still adds up
+ * to 1).  Tokens that take no part get add alone.  add
  * f32 [s,e] (nullable: 0) is typically the gradient from moe_topk_gate_bwd and
  * may be dlogits itself. */
 moe_status moe_balance_loss_bwd(const float* logits, const float* lse, const float* coef, const float* norm,
