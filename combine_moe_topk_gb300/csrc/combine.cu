@@ -75,9 +75,9 @@ template <int KMAX, bool WEIGHTED>
 __device__ __forceinline__ void token_routes(const int32_t* __restrict__ row,
                                              const float* __restrict__ gate, int t, int k, long long rows,
                                              int lane, int (&r)[KMAX], float (&g)[KMAX]) {
-  int rl = lane < k ? __ldg(row + (size_t)t * k + lane) : -1;
+  int rl = lane < k ? ld_ordered(row + (size_t)t * k + lane) : -1;
   if (rl >= rows) rl = -1;
-  const float gl = (WEIGHTED && lane < k) ? __ldg(gate + (size_t)t * k + lane) : 1.0f;
+  const float gl = (WEIGHTED && lane < k) ? ld_ordered(gate + (size_t)t * k + lane) : 1.0f;
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
     r[j] = __shfl_sync(0xffffffffu, rl, j);
@@ -165,9 +165,9 @@ __global__ void __launch_bounds__(kThreads) combine_compact_kernel(const int32_t
     const int t = (int)(u / nchunks);
     const int c0 = (int)(u - (long long)t * nchunks) * chunk;
     const int c1 = min(nvec, c0 + chunk);
-    int rl = lane < k ? __ldg(row + (size_t)t * k + lane) : -1;
+    int rl = lane < k ? ld_ordered(row + (size_t)t * k + lane) : -1;
     if (rl >= rows) rl = -1;  // past the buffer: read nothing
-    const float gl = (WEIGHTED && lane < k) ? __ldg(gate + (size_t)t * k + lane) : 1.0f;
+    const float gl = (WEIGHTED && lane < k) ? ld_ordered(gate + (size_t)t * k + lane) : 1.0f;
     unsigned kept = __ballot_sync(0xffffffffu, rl >= 0);
     const int nkept = __popc(kept);
     // lane c takes the c-th kept route
@@ -275,8 +275,8 @@ __device__ __forceinline__ void combine_bwd_body(
     int rg_id = -1;
     float rg_g = 0.f;
     if (RG && live && (G == 1 || w == 0) && lane < k) {
-      rg_id = __ldg(rg.idx + (size_t)t * k + lane);
-      rg_g = __ldg(gate + (size_t)t * k + lane);
+      rg_id = ld_ordered(rg.idx + (size_t)t * k + lane);
+      rg_g = ld_ordered(gate + (size_t)t * k + lane);
     }
     if (live) {
       token_routes<KMAX, true>(row, gate, t, k, rows, lane, r, g);
@@ -407,13 +407,13 @@ __device__ __forceinline__ void combine_bwd_compact_body(
   pdl_trigger_early();
   if (zero_fill) stage_segments_async(seg, offsets, counts, e);  // read by the zero tail
   for (int t = gw; t < s; t += warps) {
-    int rl = lane < k ? __ldg(row + (size_t)t * k + lane) : -1;
+    int rl = lane < k ? ld_ordered(row + (size_t)t * k + lane) : -1;
     if (rl >= rows) rl = -1;  // past the buffer: read nothing
-    const float gl = lane < k ? __ldg(gate + (size_t)t * k + lane) : 0.f;
+    const float gl = lane < k ? ld_ordered(gate + (size_t)t * k + lane) : 0.f;
     unsigned kept = __ballot_sync(0xffffffffu, rl >= 0);
     const int nkept = __popc(kept);
     if (lane < k && rl < 0) dgate[(size_t)t * k + lane] = 0.f;  // a dropped route
-    const int rg_id = (RG && lane < k) ? __ldg(rg.idx + (size_t)t * k + lane) : -1;
+    const int rg_id = (RG && lane < k) ? ld_ordered(rg.idx + (size_t)t * k + lane) : -1;
     float rg_dg = 0.f;  // this lane's route's gate gradient (0 when dropped)
     // lane c takes the c-th kept route, remembering its route index
     int cr = -1, cj = 0;

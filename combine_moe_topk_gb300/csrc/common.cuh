@@ -34,11 +34,11 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// A load that stays behind grid_dependency_wait().  __ldg says that the memory
-// is constant for the kernel's whole life, and the compiler may then move it
-// above the wait, where the kernel before may still be writing (seen in a
-// captured graph: the balance loss's backward pass read its scale before it
-// was there).
+// Loads that stay behind grid_dependency_wait().  __ldg and ld.global.nc say
+// that the memory is constant for the kernel's whole life, and the compiler
+// may then move them above the wait, where the kernel before may still be
+// writing (seen in a captured graph: the balance loss's backward pass read its
+// scale before it was there).  No kernel that waits there uses either.
 template <typename T>
 __device__ __forceinline__ T ld_plain(const T* p) {
   return *p;
@@ -54,6 +54,21 @@ __device__ __forceinline__ float ld_ordered(const float* p) {
 __device__ __forceinline__ float4 ld_ordered(const float4* p) {
   float4 v;
   asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_ordered(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int2 ld_ordered(const int2* p) {
+  int2 v;
+  asm volatile("ld.global.v2.s32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int4 ld_ordered(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -93,21 +108,12 @@ __device__ __forceinline__ bool row_is_owned(long long r, const P* offsets, cons
 }
 
 // The per-expert segments (e + 1 offsets, e counts; e <= 256) staged in
-// shared memory for a zero tail: one load per thread, all in flight at once,
-// so the tail's ownership tests read shared memory instead of each running a
-// chain of dependent global loads; read only after a block barrier.
+// shared memory for a zero tail, so that the tail's ownership tests read shared
+// memory instead of each running a chain of dependent global loads.
 struct SegmentStage {
   int offsets[257];
   int counts[256];
 };
-
-__device__ __forceinline__ void stage_segments(SegmentStage& st, const int32_t* offsets, const int32_t* counts,
-                                               int e) {
-  for (int x = threadIdx.x; x <= e; x += blockDim.x) {
-    st.offsets[x] = __ldg(offsets + x);
-    if (x < e) st.counts[x] = __ldg(counts + x);
-  }
-}
 
 // ------------------------------------------------------ 16-byte vectors ----
 
@@ -151,10 +157,11 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// Streaming loads / stores: payload rows are touched once per kernel.
+// Streaming loads / stores: payload rows are touched once per kernel.  Not
+// .nc: the rows may be what the kernel before has just written.
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -172,7 +179,7 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// stage_segments with asynchronous 4-byte copies: issued at a kernel's start
+// Their copies, asynchronous and of 4 bytes: issued at a kernel's start
 // (after its programmatic-launch wait), so the loads travel while the kernel
 // does its main work; segments_wait() (every thread) before reading them.
 __device__ __forceinline__ void stage_segments_async(SegmentStage& st, const int32_t* offsets,

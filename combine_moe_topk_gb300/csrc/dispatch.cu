@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) dispatch_kernel(
     const int t = (int)(u / nchunks);
     const int c0 = (int)(u - (long long)t * nchunks) * chunk;
     const int c1 = min(nvec, c0 + chunk);
-    int rl = lane < k ? __ldg(row + (size_t)t * k + lane) : -1;
+    int rl = lane < k ? ld_ordered(row + (size_t)t * k + lane) : -1;
     if (rl >= rows) {  // a row past the buffer: written nowhere, reported
       bad = true;
       rl = -1;

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kThreads) ep_pack_kernel(
     long long run = 0;
     for (int r = 0; r < R; ++r) {
       s_off[r] = run;
-      run += __ldg(rank_counts + r);
+      run += ld_ordered(rank_counts + r);
     }
   }
   __syncthreads();
@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kThreads) ep_pack_kernel(
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
     const long long t = i / R;
     const int r = (int)(i - t * R);
-    const int slot = __ldg(rank_slot + i);
+    const int slot = ld_ordered(rank_slot + i);
     long long q = slot >= 0 ? s_off[r] + slot : -1;
     if (q >= rows_sent) {  // send slots that disagree with the row count given: send nothing
       bad = true;
@@ -60,10 +60,10 @@ __global__ void __launch_bounds__(kThreads) ep_pack_kernel(
     send_row[i] = (int32_t)q;
     if (q < 0) continue;
     for (int j = 0; j < k; ++j) {
-      const int x = __ldg(idx + t * k + j);
-      const bool on = __ldg(row + t * k + j) >= 0 && x / E == r;
+      const int x = ld_ordered(idx + t * k + j);
+      const bool on = ld_ordered(row + t * k + j) >= 0 && x / E == r;
       meta_idx[q * k + j] = on ? x - r * E : -1;
-      meta_gate[q * k + j] = on ? __ldg(gate + t * k + j) : 0.f;
+      meta_gate[q * k + j] = on ? ld_ordered(gate + t * k + j) : 0.f;
     }
   }
   if (bad) raise_status(status, MOE_DEV_BAD_ROUTE);
@@ -81,10 +81,10 @@ __global__ void __launch_bounds__(kThreads) ep_unpack_dgate_kernel(
     const long long t = i / k;
     const int j = (int)(i - t * k);
     float v = 0.f;
-    if (__ldg(row + i) >= 0) {
-      const int r = __ldg(idx + i) / E;
-      const int q = __ldg(send_row + t * R + r);
-      if (q >= 0 && q < rows_sent) v = __ldg(dgate_back + (long long)q * k + j);
+    if (ld_ordered(row + i) >= 0) {
+      const int r = ld_ordered(idx + i) / E;
+      const int q = ld_ordered(send_row + t * R + r);
+      if (q >= 0 && q < rows_sent) v = ld_ordered(dgate_back + (long long)q * k + j);
     }
     dgate[i] = v;
   }

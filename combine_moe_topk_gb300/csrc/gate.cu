@@ -78,18 +78,18 @@ __global__ void __launch_bounds__(256) topk_gate_bwd_kernel(
   int n_ij = -1;
   float n_gj = 0.f, n_dgj = 0.f;
   if (t < s && lane < k) {
-    n_ij = __ldg(idx + (size_t)t * k + lane);
-    n_gj = __ldg(gate + (size_t)t * k + lane);
-    n_dgj = __ldg(dgate + (size_t)t * k + lane);
+    n_ij = ld_ordered(idx + (size_t)t * k + lane);
+    n_gj = ld_ordered(gate + (size_t)t * k + lane);
+    n_dgj = ld_ordered(dgate + (size_t)t * k + lane);
   }
   for (; t < s; t += warps) {
     const int ij = n_ij;
     const float gj = n_gj, dgj = n_dgj;
     const int tn = t + warps;
     if (tn < s && lane < k) {
-      n_ij = __ldg(idx + (size_t)tn * k + lane);
-      n_gj = __ldg(gate + (size_t)tn * k + lane);
-      n_dgj = __ldg(dgate + (size_t)tn * k + lane);
+      n_ij = ld_ordered(idx + (size_t)tn * k + lane);
+      n_gj = ld_ordered(gate + (size_t)tn * k + lane);
+      n_dgj = ld_ordered(dgate + (size_t)tn * k + lane);
     }
     router_grad_token<EPL>(t, lane, k, e, renorm, ij, gj, dgj, logits, dlogits);
   }

@@ -158,7 +158,7 @@ __device__ __forceinline__ unsigned load_routes(const Params& p, int t, int* xs,
 #pragma unroll
     for (int j4 = 0; j4 < (KM / 4); ++j4)
       if (4 * j4 < p.k) {
-        const int4 v = __ldg(reinterpret_cast<const int4*>(src) + j4);
+        const int4 v = ld_ordered(reinterpret_cast<const int4*>(src) + j4);
         xs[4 * j4] = v.x;
         xs[4 * j4 + 1] = v.y;
         xs[4 * j4 + 2] = v.z;
@@ -168,14 +168,14 @@ __device__ __forceinline__ unsigned load_routes(const Params& p, int t, int* xs,
 #pragma unroll
     for (int j2 = 0; j2 < (KM / 2); ++j2)
       if (2 * j2 < p.k) {
-        const int2 v = __ldg(reinterpret_cast<const int2*>(src) + j2);
+        const int2 v = ld_ordered(reinterpret_cast<const int2*>(src) + j2);
         xs[2 * j2] = v.x;
         xs[2 * j2 + 1] = v.y;
       }
   } else {
 #pragma unroll
     for (int j = 0; j < KM; ++j)
-      if (j < p.k) xs[j] = __ldg(src + j);
+      if (j < p.k) xs[j] = ld_ordered(src + j);
   }
   unsigned valid = 0, none = 0;
 #pragma unroll
@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(kThreads) token_ranks_kernel(const Params p) {
 #pragma unroll
       for (int j = 0; j < kMaxK; ++j)
         if (j < p.k_tok) {
-          xs[j] = __ldg(p.topk_idx + (size_t)t * p.k_tok + j);
-          if (__ldg(p.out.row + (size_t)t * p.k_tok + j) >= 0) ranks |= 1ull << (xs[j] / per_rank);
+          xs[j] = ld_ordered(p.topk_idx + (size_t)t * p.k_tok + j);
+          if (ld_ordered(p.out.row + (size_t)t * p.k_tok + j) >= 0) ranks |= 1ull << (xs[j] / per_rank);
 #pragma unroll
           for (int jj = 0; jj < j; ++jj)
             if (xs[jj] == xs[j] && !(p.absent_ok && xs[j] == -1)) bad = true;
