@@ -126,13 +126,13 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
   __shared__ int s_t[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
-  const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  const int lo = blockIdx.x * p.chunk, hi = lo + min(p.chunk, p.s - lo);
   grid_dependency_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;  // for the join, later in the stream
   // tokens outside every sequence: nothing of theirs counts
   const int first = p.offsets ? ld_plain(p.offsets) : 0, last = p.offsets ? ld_plain(p.offsets + p.B) : p.s;
-  for (int t = lo + threadIdx.x; t < hi; t += kBlock)
-    if (t < first || t >= last) p.lse[t] = 0.f;
+  for (int i = threadIdx.x; i < hi - lo; i += kBlock)
+    if (lo + i < first || lo + i >= last) p.lse[lo + i] = 0.f;
   int bad = 0;
   for (int b = p.offsets ? sequence_of(p.offsets, p.B, lo) : 0; b < p.B; ++b) {
     if (p.offsets && ld_plain(p.offsets + b) >= hi) break;
@@ -146,14 +146,17 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[i][v] = 0.f;
-    for (int t0 = r.x + warp * kRows * U; t0 < r.y; t0 += kWarps * kRows * U) {
+    // i0, then a row's place o behind it: a token's number near 2^31 plus a step would not fit an int
+    for (int i0 = warp * kRows * U; i0 < r.y - r.x; i0 += kWarps * kRows * U) {
+      const int t0 = r.x + i0, left = r.y - t0;
+      const float* x = p.logits + ((size_t)t0 + sub) * p.e;  // this lane's row of the first group
       // the loads of U row groups and of these tokens' ids travel together
       float f[U][NI][V];
       bool live[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * kRows + sub;
-        live[u] = t < r.y && (!p.valid || ld_plain(p.valid + t) != 0);
+        const int o = u * kRows + sub;
+        live[u] = o < left && (!p.valid || ld_plain(p.valid + t0 + o) != 0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -162,10 +165,10 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
           const int c = V * (col + L * i);
 #pragma unroll
           for (int v = 0; v < V; ++v) f[u][i][v] = -CUDART_INF_F;
-          if (live[u] && c < p.e) load_cols<V>(p.logits + (size_t)(t0 + u * kRows + sub) * p.e + c, f[u][i]);
+          if (live[u] && c < p.e) load_cols<V>(x + u * kRows * p.e + c, f[u][i]);
         }
       }
-      const int n_ids = min(kRows * U, r.y - t0) * p.k;
+      const int n_ids = min(kRows * U, left) * p.k;
 #pragma unroll 2
       for (int q = lane; q < n_ids; q += 32) {
         const int id = ld_plain(p.idx + (size_t)t0 * p.k + q);
@@ -217,11 +220,11 @@ __global__ void __launch_bounds__(kBlock, 2) balance_kernel(const BalanceFwd p) 
           sum = col == u - r0 ? sums[u] : sum;
           base = col == u - r0 ? bases[u] : base;
         }
-        const int t = t0 + (r0 + col) * kRows + sub;
-        if (col < U - r0 && col < L && t < r.y) {
+        const int o = (r0 + col) * kRows + sub;
+        if (col < U - r0 && col < L && o < left) {
           const bool some = sum > 0.f || sum != sum;
           const float lse = some ? base + logf(sum) : (sum < 0.f ? 0.f : -CUDART_INF_F);
-          p.lse[t] = lse;
+          p.lse[t0 + o] = lse;
           if (some) zsum = fmaf(lse, lse, zsum);
           tokens += sum < 0.f ? 0 : 1;
         }
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
   constexpr int kRows = 32 / L, U = unroll_of(V, NI);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / L, col = lane % L;
-  const int lo = blockIdx.x * p.chunk, hi = min(p.s, lo + p.chunk);
+  const int lo = blockIdx.x * p.chunk, hi = lo + min(p.chunk, p.s - lo);
   grid_dependency_wait();
   const float wl = ld_plain(p.dloss) * ld_plain(p.norm), wz = 2.f * ld_plain(p.dloss + 1) * ld_plain(p.norm + 1);
   if (p.offsets) {
@@ -460,33 +463,34 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
         const int j = V * (col + L * i) + v;
         c[i][v] = j < p.e ? wl * ld_plain(p.coef + (size_t)b * p.e + j) : 0.f;
       }
-    for (int t0 = r.x + warp * kRows * U; t0 < r.y; t0 += kWarps * kRows * U) {
+    for (int i0 = warp * kRows * U; i0 < r.y - r.x; i0 += kWarps * kRows * U) {
+      const int t0 = r.x + i0, left = r.y - t0;
       float f[U][NI][V], g[U][NI][V], lse[U];
       bool some[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * kRows + sub;
-        const bool live = t < r.y && (!p.valid || ld_plain(p.valid + t) != 0);
-        lse[u] = t < r.y ? ld_plain(p.lse + t) : 0.f;
+        const int o = u * kRows + sub;
+        const bool live = o < left && (!p.valid || ld_plain(p.valid + t0 + o) != 0);
+        lse[u] = o < left ? ld_plain(p.lse + t0 + o) : 0.f;
         some[u] = live && lse[u] != -CUDART_INF_F;  // a row of masked experts has no probabilities
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * kRows + sub;
+        const int o = u * kRows + sub;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           const int q = V * (col + L * i);
 #pragma unroll
           for (int v = 0; v < V; ++v) f[u][i][v] = -CUDART_INF_F, g[u][i][v] = 0.f;
-          if (t < r.y && q < p.e) {
-            load_cols<V>(p.logits + (size_t)t * p.e + q, f[u][i]);
-            if (p.add) load_add<V>(p.add + (size_t)t * p.e + q, g[u][i]);
+          if (o < left && q < p.e) {
+            load_cols<V>(p.logits + (size_t)((unsigned)t0 + o) * p.e + q, f[u][i]);
+            if (p.add) load_add<V>(p.add + (size_t)((unsigned)t0 + o) * p.e + q, g[u][i]);
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int t = t0 + u * kRows + sub;
+        const int o = u * kRows + sub;
         // lse is rounded to its own last place: past 1e8 nothing of the sum's
         // logarithm is left in it.  Divided by the row's sum, p has that no more.
         float dot = 0.f, sum = 0.f;
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(kBlock, 2) balance_bwd_kernel(const BalanceBwd
 #pragma unroll
             for (int v = 0; v < V; ++v) g[u][i][v] = fmaf(f[u][i][v] * inv, c[i][v] - dot + zt, g[u][i][v]);
           }
-          if (t < r.y && q < p.e) store_cols<V>(p.dlogits + (size_t)t * p.e + q, g[u][i]);
+          if (o < left && q < p.e) store_cols<V>(p.dlogits + (size_t)((unsigned)t0 + o) * p.e + q, g[u][i]);
         }
       }
     }
@@ -583,7 +587,7 @@ cudaError_t launch_balance(const float* logits, const int32_t* idx, const uint8_
                reinterpret_cast<float*>(ws + q.zsum), reinterpret_cast<int*>(ws + q.tokens)};
   unsigned* ticket = reinterpret_cast<unsigned*>(ws + q.ticket);
   BalanceFwd p = {logits, idx, valid, offsets, s, e, k, B, chunk, lse, pc, ticket, status};
-  const unsigned grid = s > 0 ? (unsigned)((s + chunk - 1) / chunk) : 1u;  // no tokens: one block clears the ticket
+  const unsigned grid = s > 0 ? (unsigned)((s - 1) / chunk + 1) : 1u;  // no tokens: one block clears the ticket
   cudaError_t err = cudaErrorInvalidValue;
 #define MOE_RUN(v, l, n) \
   if (h.V == v && h.L == l && h.NI == n) err = launch_chained(balance_kernel<v, l, n>, dim3(grid), dim3(kBlock), 0, st, p);
@@ -603,7 +607,7 @@ cudaError_t launch_balance_bwd(const float* logits, const float* lse, const floa
   const Shape h = shape_of(e);
   const int chunk = chunk_of(s, h);
   BalanceBwd p = {logits, lse, coef, norm, dloss, valid, offsets, add, dlogits, s, e, B, chunk};
-  const unsigned grid = (unsigned)((s + chunk - 1) / chunk);
+  const unsigned grid = (unsigned)((s - 1) / chunk + 1);
   cudaError_t err = cudaErrorInvalidValue;
 #define MOE_RUN(v, l, n) \
   if (h.V == v && h.L == l && h.NI == n) \

@@ -80,3 +80,25 @@ def test_random_rows_of_every_size():
     r = np.random.default_rng(2)
     logits = (r.normal(size=(300, 32)) * 10.0 ** r.uniform(-3, 37, size=(300, 1))).astype(np.float32)
     check(logits, np.argsort(-logits, axis=1)[:, :2].astype(np.int32))
+
+
+@pytest.mark.parametrize("s", [2 ** 31 - 1, 2 ** 31 - 4097])
+def test_as_many_tokens_as_are_accepted(s):
+    # one expert, so that s * e may come to 2^31 - 1: token numbers and the ends of blocks at the edge of an int.
+    # p = 1, lse = the logit: everything can be said without a reference of this size (four arrays of 8.6 GB)
+    logits = torch.full((s, 1), 0.5, device="cuda")
+    logits[-3000:] = torch.arange(3000, device="cuda").float()[:, None] / 1024
+    idx = torch.zeros(s, 1, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, s - 2000, s - 5], dtype=torch.int32).cuda()  # the last five tokens belong to nobody
+    for offsets, live in ((None, s), (off, s - 5)):
+        r = B.moe_balance_loss(logits, idx, None, offsets)
+        assert torch.equal(r.lse[:live], logits[:live, 0]) and not r.lse[live:].any()
+        assert r.counts[:, 0].tolist() == ([s] if offsets is None else [s - 2000, 1995])
+        assert abs(r.loss[0].item() - 1) <= 512 * U and ((r.mean_prob - 1).abs() <= 320 * U).all()
+        z = 0.25 * (s - 3000) + float(np.square(np.arange(3000 - (s - live)) / 1024).sum())
+        assert abs(r.loss[1].item() - z / live) <= 320 * U * z / live
+        d = B.moe_balance_loss_bwd(logits, r.lse, r.coef, r.norm, torch.tensor([0.7, 0.3 * live]).cuda(), None, offsets)
+        # dz = 0.3 * 2 lse; c - dot is 0 but for the roundings of p = 1 (2 u) times coef (about 1/T)
+        want = 0.6 * logits[:, 0]
+        assert ((d[:live, 0] - want[:live]).abs() <= 16 * U * (1 + want[:live])).all() and not d[live:].any()
+        del d, want, r
