@@ -20,15 +20,50 @@ routing is pinned across recompute; the recorder checks the expert ids it is
 given against the logged ones (on the device) when asked to.
 
 All arithmetic runs in the CUDA library (``binding``); this module only
-wires tensors and handles together.
+wires tensors and handles together.  The library's gradients carry no graph:
+a second derivative is refused (``first_order``), not taken as zero.
 """
 from __future__ import annotations
 
+import functools
 from collections import deque
 
 import torch
 
 from . import binding as B
+
+
+class _NoSecondDerivative(torch.autograd.Function):
+    """The first argument, tied to the tensors that it depends on by a node that raises."""
+
+    @staticmethod
+    def forward(ctx, value: torch.Tensor, *sources):
+        return value.view_as(value)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("the MoE library's gradients cannot be differentiated again")
+
+
+def first_order(backward):
+    """For a ``backward`` whose results carry no graph.  Under ``create_graph=True`` they are tied to the incoming
+    gradients and the saved inputs, so that a derivative that would go through them raises.  (torch's
+    ``once_differentiable`` ties them to nothing: ``torch.autograd.grad`` then never reaches its error.)"""
+
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        sources = [t for t in (*grads, *ctx.saved_tensors) if t is not None and t.requires_grad]
+        if not sources:
+            return out
+        tied = tuple(t if t is None else _NoSecondDerivative.apply(t, *sources)
+                     for t in (out if isinstance(out, tuple) else (out,)))
+        return tied if isinstance(out, tuple) else tied[0]
+
+    return call
 
 
 class MoETopkGateFn(torch.autograd.Function):
@@ -46,6 +81,7 @@ class MoETopkGateFn(torch.autograd.Function):
         return idx, gate
 
     @staticmethod
+    @first_order
     def backward(ctx, didx, dgate: torch.Tensor):
         logits, idx, gate = ctx.saved_tensors
         dl = B.moe_topk_gate_bwd(logits, idx, gate, dgate.contiguous(), ctx.e, ctx.renorm)
@@ -53,7 +89,7 @@ class MoETopkGateFn(torch.autograd.Function):
 
 
 def topk_gate(logits: torch.Tensor, k: int, renorm: int = 1):
-    return MoETopkGateFn.apply(logits, k, renorm)
+    return MoETopkGateFn.apply(logits.contiguous(), k, renorm)
 
 
 class MoEDispatchFn(torch.autograd.Function):
@@ -65,6 +101,7 @@ class MoEDispatchFn(torch.autograd.Function):
         return B.moe_dispatch(handle, x.contiguous())
 
     @staticmethod
+    @first_order
     def backward(ctx, dX: torch.Tensor):
         return B.moe_dispatch_bwd(ctx.handle, dX.contiguous()), None
 
@@ -81,6 +118,7 @@ class MoECombineFn(torch.autograd.Function):
         return B.moe_combine(handle, y, gate)
 
     @staticmethod
+    @first_order
     def backward(ctx, dout: torch.Tensor):
         y, gate = ctx.saved_tensors
         dY, dgate = B.moe_combine_bwd(ctx.handle, dout.contiguous(), gate, y)
@@ -88,11 +126,11 @@ class MoECombineFn(torch.autograd.Function):
 
 
 def dispatch(x: torch.Tensor, handle: B.Handle) -> torch.Tensor:
-    return MoEDispatchFn.apply(x, handle)
+    return MoEDispatchFn.apply(x.contiguous(), handle)
 
 
 def combine(y: torch.Tensor, gate: torch.Tensor, handle: B.Handle) -> torch.Tensor:
-    return MoECombineFn.apply(y, gate, handle)
+    return MoECombineFn.apply(y.contiguous(), gate.contiguous(), handle)
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -107,13 +145,13 @@ class LayerNormFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight, bias, eps: float):
-        x = x if x.dim() == 2 and x.stride(1) == 1 and x.data_ptr() % 16 == 0 else _rows(x)
         y, mean, rstd = B.moe_layernorm(x, weight, bias, eps)
         ctx.save_for_backward(x, weight, mean, rstd)
         ctx.bias_dtype = None if bias is None else bias.dtype
         return y
 
     @staticmethod
+    @first_order
     def backward(ctx, dy: torch.Tensor):
         x, weight, mean, rstd = ctx.saved_tensors
         _, need_w, need_b, _ = ctx.needs_input_grad
@@ -124,6 +162,8 @@ class LayerNormFn(torch.autograd.Function):
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
               eps: float = 1e-5) -> torch.Tensor:
     """Layer norm of [s, m] rows."""
+    # copies are made before the node, so that what it saves is its own input
+    x = x if x.dim() == 2 and x.stride(1) == 1 and x.data_ptr() % 16 == 0 else _rows(x)
     return LayerNormFn.apply(x, weight, bias, eps)
 
 
@@ -132,8 +172,6 @@ class LinearFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype):
-        x = x if x.data_ptr() % 16 == 0 else _rows(x)
-        residual = residual if residual is None or residual.data_ptr() % 16 == 0 else _rows(residual)
         save_z = act != "none" and any(ctx.needs_input_grad[:3])
         out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z)
         y, z = out if save_z else (out, None)
@@ -144,19 +182,27 @@ class LinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
-    def backward(ctx, dy: torch.Tensor):
+    @first_order
+    def products(ctx, dy: torch.Tensor):
         x, W, z = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx = dW = db = None
-        if any(need[:3]):
-            dx, dW, db = B.moe_linear_bwd(_rows(dy), x, W, z, ctx.act, need[0], need[1], need[2])
-        return (dx, dW, db if db is None else db.to(ctx.bias_dtype),
-                dy.to(ctx.residual_dtype) if need[3] else None, None, None)
+        if not any(need[:3]):
+            return None, None, None
+        dx, dW, db = B.moe_linear_bwd(_rows(dy), x, W, z, ctx.act, need[0], need[1], need[2])
+        return dx, dW, db if db is None else db.to(ctx.bias_dtype)
+
+    @staticmethod
+    def backward(ctx, dy: torch.Tensor):
+        # the residual's gradient is dy itself, which may be differentiated
+        dres = dy.to(ctx.residual_dtype) if ctx.needs_input_grad[3] else None
+        return (*LinearFn.products(ctx, dy), dres, None, None)
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
            residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """y [s, N] = act(x W^T + bias) + residual, bf16 (or fp32) out."""
+    x = x if x.data_ptr() % 16 == 0 else _rows(x)
+    residual = residual if residual is None or residual.data_ptr() % 16 == 0 else _rows(residual)
     return LinearFn.apply(x, W, bias, residual, act, out_dtype)
 
 
@@ -171,6 +217,7 @@ class BalanceLossFn(torch.autograd.Function):
         return r.loss, r.counts, r.mean_prob
 
     @staticmethod
+    @first_order
     def backward(ctx, dloss: torch.Tensor, dcounts, dmean_prob):
         logits, lse, coef, norm, valid, seq_offsets = ctx.saved_tensors
         d = B.moe_balance_loss_bwd(logits, lse, coef, norm, dloss.contiguous(), valid, seq_offsets)
