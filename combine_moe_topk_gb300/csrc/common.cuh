@@ -242,6 +242,21 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// The same with the limit counted from this wait's own start (the timer is
+// read only where a wait lasts).
+__device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t deadline = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63) == 63) {
+      const uint64_t now = globaltimer_ns();
+      if (deadline == 0) deadline = now + (uint64_t)limit_ns;
+      else if (now > deadline) return false;
+    }
+  }
+}
+
 // 1-D bulk copy global -> shared, completion counted on `bar` (bytes).
 // Non-multicast; the destination is this CTA's own shared memory.
 __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, uint32_t bytes,

@@ -26,7 +26,8 @@
 // 1.97 PFLOP/s; 8192 x 4096 x 4096 146, backward dx 146, dW 164 us), by what an SM
 // takes in where one is short (16384 x 4096 x 128 28.5 us), by the weights' bytes
 // and the launch where rows are few (64 x 4096 x 4096 11.9 us).
-// Every mbarrier wait is bounded on the global timer; a time-out records
+// Every mbarrier wait is bounded on the global timer, each from its own start, so
+// that a long product does not run into the limit; a time-out records
 // MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
 #include "common.cuh"
 #include "internal.h"
@@ -202,7 +203,7 @@ struct GemmArgs {
   int tiles_m, tiles_n, splits, per_split, kblocks;  // K blocks of 128
   Epi epi;
   int32_t* status;
-  long long timeout_ns;
+  long long timeout_ns;  // of a single wait
 };
 
 constexpr int kThreads = 384;
@@ -708,7 +709,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   grid_dependency_wait();  // all set-up is done: from here on memory of earlier kernels is read
-  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any remote signal
@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit t = unit_of<CG, BN>(u, split, p);
       const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + S::kRowsB * (int)rank;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) {
+        if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every stage's last fill consumed: nothing still arrives at this CTA's
     // barriers or shared memory when it leaves
     for (int i = 0; i < kStages && ok; ++i) {
-      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) ok = false;
+      if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) ok = false;
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit t = unit_of<CG, BN>(u, split, p);
       for (int kb0 = t.kb0; kb0 < t.kb1 && ok;) {
         const int kb1 = kExact ? min(t.kb1, kb0 + kExactBlocks) : t.kb1;
-        if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
+        if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t dt = tbase + (uint32_t)(acc * BN);
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait_cluster(&full[stage], phase, deadline)) {
+          if (!mbar_wait_cluster_limited(&full[stage], phase, p.timeout_ns)) {
             ok = false;
             break;
           }
@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // memory before the CTAs leave (one more commit, to this CTA only)
       if constexpr (CG == 2) mma_commit_pair(&drain, 0x1);
       else commit<CG>(&drain);
-      mbar_wait_bounded(&drain, 0, globaltimer_ns() + (uint64_t)p.timeout_ns);
+      mbar_wait_limited(&drain, 0, p.timeout_ns);
       atomicOr(&s_err, 1);
     }
   } else if (warp >= 4) {
@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[c][j] = 0u;
         for (int kb = t.kb0; kb < t.kb1; kb += kExactBlocks) {
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+          if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
             ok = false;
             break;
           }
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         start();
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+        if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
           ok = false;
           break;
         }
@@ -1016,7 +1016,6 @@ __global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant_
   }
   __syncthreads();
   grid_dependency_wait();
-  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
   const int f0 = (int)((long long)p.N * blockIdx.x / gridDim.x), f1 = (int)((long long)p.N * (blockIdx.x + 1) / gridDim.x);
   const int chunks = (p.K + kFewK - 1) / kFewK;
   int stage = 0;
@@ -1030,7 +1029,7 @@ __global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant_
   };
   if (warp == 8) {
     auto put = [&](const bf16* base, long long ld, int rows, int kc) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns));
       if (ok) {
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], (uint32_t)(rows * kc * 2));
         __syncwarp();
@@ -1050,7 +1049,7 @@ __global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant_
   } else {
     const int g = lane >> 2, c = lane & 3;
     auto wait_full = [&]() {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, deadline));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait_limited(&full[stage], phase, p.timeout_ns));
     };
     auto release = [&]() {
       __syncwarp();
@@ -1240,6 +1239,7 @@ constexpr int kKinds = 3;
 constexpr int kKindCG[kKinds] = {2, 1, 1};
 constexpr int kKindBN[kKinds] = {256, 128, 64};
 constexpr int kPlanSms = 152;  // plans are made for a whole GB300
+constexpr long long kWaitNs = 2000000000LL;  // the limit of a device wait
 
 // The shape and split of least estimated time, in units of a K block of the
 // widest tile (0.65 us).  Measured: a K block of a 128 x 128 tile takes 0.70 of
@@ -1337,7 +1337,9 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
       (!make_out_map(&maps[2], epi.out, N, M, epi.out_f32, epi.narrow) ||
        (epi.z && !make_out_map(&maps[3], epi.z, N, M, false, true))))
     return cudaErrorInvalidValue;
-  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, 2000000000LL};
+  // the longest wait is the epilogue's, for a tile's whole contraction: 0.65 us a K block when all is well
+  const long long limit = kWaitNs + 20000LL * q.per_split;
+  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, limit};
   if (epi.out_f32)
     return q.kind == 1 ? run_gemm<1, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
   switch (q.kind) {
@@ -1355,7 +1357,7 @@ cudaError_t few_rows(const LinearArgs& a, const Epi& e, const DeviceInfo& di, cu
   });
   if (err != cudaSuccess) return err;
   FewArgs p = {static_cast<const bf16*>(a.x), static_cast<const bf16*>(a.W), a.ldx, a.ldw, a.s, a.K, a.N, e, a.status,
-               2000000000LL};
+               kWaitNs};
   return launch_chained(few_rows_kernel<kHigh>, dim3((unsigned)(a.N < di.sms ? a.N : di.sms)), dim3(288), kFewSmem, st, p);
 }
 

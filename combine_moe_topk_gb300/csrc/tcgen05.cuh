@@ -87,20 +87,36 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask = 0
       : "memory");
 }
 
-// Bounded wait with cluster-scope acquire, for barriers that receive
-// arrivals from the other CTA of the pair.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Bounded waits with cluster-scope acquire, for barriers that receive
+// arrivals from the other CTA of the pair: until a point in time, or for
+// limit_ns from the wait's own start.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
   for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 63) == 63 && globaltimer_ns() > deadline_ns) return false;
+  }
+}
+__device__ __forceinline__ bool mbar_wait_cluster_limited(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  uint64_t deadline = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if ((it & 63) == 63) {
+      const uint64_t now = globaltimer_ns();
+      if (deadline == 0) deadline = now + (uint64_t)limit_ns;
+      else if (now > deadline) return false;
+    }
   }
 }
 

@@ -1,0 +1,36 @@
+"""The dense products at the far ends of their range."""
+import numpy as np
+import pytest
+import torch
+
+from combine_moe_topk_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def test_a_product_longer_than_the_limit_of_a_wait():
+    """2 * 122880^3 operations take more than two seconds, the limit of one device wait.  Rows repeat every 256, so
+    256 x 256 values of the definition tell all of them."""
+    n, r = 122880, 256
+    g = torch.Generator(device="cuda").manual_seed(0)
+    few = [(torch.randn(r, n, generator=g, device="cuda") / n ** 0.25).bfloat16() for _ in range(2)]
+    x, W = (t.repeat(n // r, 1) for t in few)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = B.moe_linear(x, W, device_status=st)
+    assert st.item() == 0
+    want = few[0].double() @ few[1].double().t()
+    mags = few[0].double().abs() @ few[1].double().abs().t()
+    got = y[:r, :r].double()
+    # the chain of the tensor cores' additions, 16 terms each, and the rounding to bf16
+    tol = (n / 16 + 48) * 2.0 ** -23 * mags + want.abs() * 2.0 ** -8 + 1e-38
+    assert ((got - want).abs() <= tol).all()
+    first = y[:r]
+    assert (first.view(r, n // r, r) == first[:, None, :r]).all()
+    for at in range(0, n, 16 * r):
+        block = y[at:at + 16 * r].view(-1, r, n)
+        assert (block == first).all(), at
