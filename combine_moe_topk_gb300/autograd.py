@@ -33,6 +33,40 @@ import torch
 from . import binding as B
 
 
+_words: dict[int, torch.Tensor] = {}  # a device's status word, the same for its whole life
+
+
+def _status(t: torch.Tensor) -> torch.Tensor | None:
+    """The status word of t's device (a host tensor goes to the library, which rejects it)."""
+    if not t.is_cuda:
+        return None
+    word = _words.get(t.get_device())
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None  # it would belong to the graph; a run before the capture makes it
+        word = torch.zeros(1, dtype=torch.int32, device=t.device)
+        torch.cuda.current_stream(t.device).synchronize()  # it is written from any stream
+        _words[t.get_device()] = word
+    return word
+
+
+def status(device: torch.device | int | None = None) -> int:
+    """Synchronise, read and clear what the kernels behind these wrappers reported on a device since the last call:
+    MOE_DEV_* bits, 0 when all went well.  A set MOE_DEV_TIMEOUT means that a product's outputs are not all there.
+    (A layout handle has a status of its own, ``Handle.status``.)"""
+    index = torch.device("cuda", device).index if isinstance(device, int) else \
+        torch.device(device).index if device is not None else None
+    word = _words.get(torch.cuda.current_device() if index is None else index)
+    if word is None:
+        return 0
+    torch.cuda.synchronize(word.device)
+    bits = int(word.item())
+    if bits:
+        word.zero_()
+        torch.cuda.synchronize(word.device)
+    return bits
+
+
 class _NoSecondDerivative(torch.autograd.Function):
     """The first argument, tied to the tensors that it depends on by a node that raises."""
 
@@ -73,7 +107,7 @@ class MoETopkGateFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits: torch.Tensor, k: int, renorm: int):
         logits = logits.contiguous()
-        idx, gate = B.moe_topk_gate(logits, k, renorm)
+        idx, gate = B.moe_topk_gate(logits, k, renorm, device_status=_status(logits))
         ctx.renorm = int(renorm)
         ctx.e = logits.shape[1]
         ctx.save_for_backward(None if renorm else logits, idx, gate)
@@ -173,7 +207,7 @@ class LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype):
         save_z = act != "none" and any(ctx.needs_input_grad[:3])
-        out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z)
+        out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z, device_status=_status(x))
         y, z = out if save_z else (out, None)
         ctx.save_for_backward(x, W, z)
         ctx.act = act
@@ -188,7 +222,7 @@ class LinearFn(torch.autograd.Function):
         need = ctx.needs_input_grad
         if not any(need[:3]):
             return None, None, None
-        dx, dW, db = B.moe_linear_bwd(_rows(dy), x, W, z, ctx.act, need[0], need[1], need[2])
+        dx, dW, db = B.moe_linear_bwd(_rows(dy), x, W, z, ctx.act, need[0], need[1], need[2], device_status=_status(x))
         return dx, dW, db if db is None else db.to(ctx.bias_dtype)
 
     @staticmethod
@@ -211,7 +245,7 @@ class BalanceLossFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, logits: torch.Tensor, topk_idx: torch.Tensor, valid, seq_offsets):
-        r = B.moe_balance_loss(logits, topk_idx, valid, seq_offsets)
+        r = B.moe_balance_loss(logits, topk_idx, valid, seq_offsets, device_status=_status(logits))
         ctx.save_for_backward(logits, r.lse, r.coef, r.norm, valid, seq_offsets)
         ctx.mark_non_differentiable(r.counts, r.mean_prob)
         return r.loss, r.counts, r.mean_prob

@@ -84,6 +84,8 @@ def main(steps: int = 20):
         opt.zero_grad()
         loss.backward()
         opt.step()
+        if A.status():
+            raise RuntimeError("a kernel of this step reported a time-out, a NaN or a bad route")
         print(f"step {step}: loss {loss.item():.4f} (auxiliary {aux.item():.4f}), routes per expert {counts[0].tolist()}")
 
 

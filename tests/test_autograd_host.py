@@ -60,7 +60,7 @@ def calls(monkeypatch):
     for name, fn in (("moe_layernorm", layernorm), ("moe_layernorm_bwd", layernorm_bwd), ("moe_linear", linear),
                      ("moe_linear_bwd", linear_bwd), ("moe_balance_loss", balance_loss),
                      ("moe_balance_loss_bwd", balance_loss_bwd),
-                     ("moe_topk_gate", lambda l, k, renorm=1: (l.topk(k, 1).indices.int(), torch.softmax(l.topk(k, 1).values, 1))),
+                     ("moe_topk_gate", lambda l, k, renorm=1, **kw: (l.topk(k, 1).indices.int(), torch.softmax(l.topk(k, 1).values, 1))),
                      ("moe_topk_gate_bwd", lambda l, idx, gate, dgate, e, renorm=1: torch.zeros(len(idx), e)),
                      ("moe_dispatch", lambda h, x: x * 1.0), ("moe_dispatch_bwd", lambda h, dX: dX * 1.0),
                      ("moe_combine", lambda h, y, gate: y * gate[:, :1]),
@@ -126,3 +126,15 @@ def test_the_residual_of_a_product_can_be_differentiated_twice(calls):
     g, = torch.autograd.grad(y.pow(3).sum(), r, create_graph=True)
     h, = torch.autograd.grad(g.sum(), r)
     assert torch.allclose(h, 6 * y.detach(), rtol=1e-6)
+
+
+def test_every_call_that_can_report_gets_a_status_word(calls, monkeypatch):
+    monkeypatch.setattr(A, "_status", lambda t: "the word")
+    x, W = leaf(4, 8, dtype=torch.bfloat16), leaf(6, 8, dtype=torch.bfloat16, seed=1)
+    A.linear(x, W, act="relu").float().sum().backward()
+    logits = leaf(4, 6)
+    A.balance_loss(logits, idx_of(logits))[0].sum().backward()
+    A.topk_gate(logits, 2)[1].sum().backward()
+    for name, _, kw in calls:
+        if name in ("moe_linear", "moe_linear_bwd", "moe_balance_loss", "moe_topk_gate"):
+            assert kw.get("device_status") == "the word", name
