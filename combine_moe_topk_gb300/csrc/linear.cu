@@ -988,6 +988,8 @@ struct FewArgs {
 //                   s <= 8, but the tensor cores wait for memory anyway)
 // The order of the terms is free, so lane c of a row's four feeds its 8
 // consecutive elements to two MMAs as their k pairs, the same for x and W.  The
+// accumulator, which drops the bits below its last place as that of the tiles
+// does, is emptied into an fp32 sum after every chunk: 256 terms of a warp.  The
 // warps' sums are added in order through shared memory every 32 columns.
 // A wait that runs out sets the status and everyone runs on without waiting,
 // so that the barriers stay matched.
@@ -1062,11 +1064,11 @@ __global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant_
       return k < kc ? *reinterpret_cast<const uint4*>(ring + stage * kFewStage + g * kFewRow + k * 2) : make_uint4(0, 0, 0, 0);
     };
     for (int g0 = f0; g0 < f1; g0 += 8 * kFewTiles) {
-      float acc[kFewTiles][4];
+      float sum[kFewTiles][4];
 #pragma unroll
       for (int t = 0; t < kFewTiles; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sum[t][j] = 0.f;
       for (int ch = 0; ch < chunks; ++ch) {
         const int kc = min(kFewK, p.K - ch * kFewK);
         uint4 xa[kBlocks], xb[kBlocks];
@@ -1086,25 +1088,28 @@ __global__ void __launch_bounds__(288, 1) few_rows_kernel(const __grid_constant_
 #pragma unroll
         for (int t = 0; t < kFewTiles; ++t) {
           if (g0 + 8 * t < f1) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
             wait_full();
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i) {
               const uint4 w = frag(i, kc);
               const uint32_t a0[4] = {xa[i].x, xb[i].x, xa[i].y, xb[i].y}, a1[4] = {xa[i].z, xb[i].z, xa[i].w, xb[i].w};
-              mma16816(acc[t], a0, w.x, w.y);
-              mma16816(acc[t], a1, w.z, w.w);
+              mma16816(acc, a0, w.x, w.y);
+              mma16816(acc, a1, w.z, w.w);
             }
             release();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[t][j] += acc[j];
           }
         }
       }
 #pragma unroll
       for (int t = 0; t < kFewTiles; ++t) {
-        red[warp][g][8 * t + 2 * c] = acc[t][0];
-        red[warp][g][8 * t + 2 * c + 1] = acc[t][1];
+        red[warp][g][8 * t + 2 * c] = sum[t][0];
+        red[warp][g][8 * t + 2 * c + 1] = sum[t][1];
         if constexpr (kHigh) {
-          red[warp][g + 8][8 * t + 2 * c] = acc[t][2];
-          red[warp][g + 8][8 * t + 2 * c + 1] = acc[t][3];
+          red[warp][g + 8][8 * t + 2 * c] = sum[t][2];
+          red[warp][g + 8][8 * t + 2 * c + 1] = sum[t][3];
         }
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");

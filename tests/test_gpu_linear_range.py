@@ -34,3 +34,18 @@ def test_a_product_longer_than_the_limit_of_a_wait():
     for at in range(0, n, 16 * r):
         block = y[at:at + 16 * r].view(-1, r, n)
         assert (block == first).all(), at
+
+
+@pytest.mark.parametrize("s,K,N", [(1, 16384, 24), (1, 65536, 24), (8, 65536, 130), (16, 16384, 24), (16, 65536, 24),
+                                   (17, 65536, 24), (200, 65536, 24)])
+def test_long_fp32_sums(s, K, N):
+    """All terms positive, so that what an accumulator drops adds up instead of cancelling.  Up to 16 rows, 256 terms
+    go through the tensor cores' accumulator (16 steps, each off by at most 2 u of the sum), K / 2048 such sums and
+    those of 8 warps are added in fp32: 32 + K/2048 + 10 u.  From 17 rows on, 512 terms, and K/512 sums."""
+    g = torch.Generator().manual_seed(K + s)
+    x, W = (torch.rand(n, K, generator=g).bfloat16().cuda() for n in (s, N))
+    y = B.moe_linear(x, W, out_dtype=torch.float32)
+    want = x.double() @ W.double().t()
+    tol = (32 + K / 2048 + 10 if s <= 16 else 64 + K / 512 + 10) * U
+    err = ((y.double() - want) / want).abs().max().item()
+    assert err <= tol, (err / U, tol / U)
