@@ -97,11 +97,6 @@ __device__ __forceinline__ void load_add(const float* p, float* f) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float exp2_approx(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
-}
 
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {

@@ -109,25 +109,6 @@ __device__ __forceinline__ void load_weights(const void* w, int is_f32, int c, i
   }
 }
 
-// Two fp32 operations an instruction.
-__device__ __forceinline__ uint64_t bits(float2 v) { return *reinterpret_cast<uint64_t*>(&v); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // ---- sums over a group of G warps --------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -49,3 +49,34 @@ def test_long_fp32_sums(s, K, N):
     tol = (32 + K / 2048 + 10 if s <= 16 else 64 + K / 512 + 10) * U
     err = ((y.double() - want) / want).abs().max().item()
     assert err <= tol, (err / U, tol / U)
+
+
+def normal(z):
+    """(Phi(z), phi(z)) in 64 bits, the tail by the complementary error function."""
+    from scipy.special import erfc
+
+    return 0.5 * erfc(-z / np.sqrt(2.0)), np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+
+
+@pytest.mark.parametrize("s", [1, 40])
+def test_gelu_keeps_its_relative_precision_in_the_tail(s):
+    """z comes in through the bias, exactly.  Phi's polynomial is good to 8 u, the exponential's argument and itself
+    to (4 + 2 z^2) u, three products and a division to 8 u more: (20 + 2 z^2) u of the result, near 0 of which the
+    values stay far from fp32's smallest."""
+    pytest.importorskip("scipy")
+    z = torch.linspace(-12, 8, 8000)
+    x, W = torch.zeros(s, 8, device="cuda").bfloat16(), torch.zeros(8000, 8, device="cuda").bfloat16()
+    y = f64(B.moe_linear(x, W, z.cuda(), "gelu", out_dtype=torch.float32))
+    zz = f64(z)
+    cdf, _ = normal(zz)
+    want = zz * cdf
+    bad = np.abs(y - want) > (20 + 2 * zz * zz) * U * np.abs(want) + 1e-44
+    assert not bad.any(), (np.abs(y / want - 1) / U).max()
+    # the slope, by the bias' gradient of one row: Phi + z phi, each to the same precision
+    zb = z.bfloat16()
+    _, _, db = B.moe_linear_bwd(torch.ones(1, 8000, device="cuda"), x[:1], W, zb.cuda()[None], "gelu", need_dx=False,
+                                need_dw=False)
+    zz = f64(zb)
+    cdf, pdf = normal(zz)
+    tol = (24 + 2 * zz * zz) * U * (cdf + np.abs(zz) * pdf)
+    assert (np.abs(f64(db) - (cdf + zz * pdf)) <= tol + 1e-44).all()
