@@ -202,11 +202,12 @@ def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.T
 
 
 class LinearFn(torch.autograd.Function):
-    """y = act(x W^T + bias) + residual; z is kept (bf16) where the activation's slope needs it."""
+    """y = act(x W^T + bias) + residual; z is kept (bf16) where the activation's slope needs it.  grad: whether a
+    gradient can be asked for at all (needs_input_grad stays true for parameters under no_grad)."""
 
     @staticmethod
-    def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype):
-        save_z = act != "none" and any(ctx.needs_input_grad[:3])
+    def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, residual, act: str, out_dtype, grad: bool):
+        save_z = grad and act != "none" and any(ctx.needs_input_grad[:3])
         out = B.moe_linear(x, W, bias, act, residual, out_dtype=out_dtype, save_z=save_z, device_status=_status(x))
         y, z = out if save_z else (out, None)
         ctx.save_for_backward(x, W, z)
@@ -229,7 +230,7 @@ class LinearFn(torch.autograd.Function):
     def backward(ctx, dy: torch.Tensor):
         # the residual's gradient is dy itself, which may be differentiated
         dres = dy.to(ctx.residual_dtype) if ctx.needs_input_grad[3] else None
-        return (*LinearFn.products(ctx, dy), dres, None, None)
+        return (*LinearFn.products(ctx, dy), dres, None, None, None)
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -237,7 +238,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, a
     """y [s, N] = act(x W^T + bias) + residual, bf16 (or fp32) out."""
     x = x if x.data_ptr() % 16 == 0 else _rows(x)
     residual = residual if residual is None or residual.data_ptr() % 16 == 0 else _rows(residual)
-    return LinearFn.apply(x, W, bias, residual, act, out_dtype)
+    return LinearFn.apply(x, W, bias, residual, act, out_dtype, torch.is_grad_enabled())
 
 
 class BalanceLossFn(torch.autograd.Function):

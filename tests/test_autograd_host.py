@@ -138,3 +138,19 @@ def test_every_call_that_can_report_gets_a_status_word(calls, monkeypatch):
     for name, _, kw in calls:
         if name in ("moe_linear", "moe_linear_bwd", "moe_balance_loss", "moe_topk_gate"):
             assert kw.get("device_status") == "the word", name
+
+
+def test_inference_keeps_nothing_for_a_backward_pass(calls):
+    x, W = leaf(4, 8, dtype=torch.bfloat16).detach(), leaf(6, 8, dtype=torch.bfloat16, seed=1)
+
+    def saved():
+        calls.clear()
+        A.linear(x, W, act="relu")
+        return [kw["save_z"] for name, _, kw in calls if name == "moe_linear"]
+
+    assert saved() == [True]
+    for off in (torch.no_grad(), torch.inference_mode()):
+        with off:
+            assert saved() == [False]
+    W.requires_grad_(False)
+    assert saved() == [False]
