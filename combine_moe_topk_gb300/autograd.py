@@ -100,13 +100,31 @@ def first_order(backward):
     return call
 
 
+def _rows(t: torch.Tensor | None) -> torch.Tensor | None:
+    """A contiguous tensor on 16 bytes, as the library wants its pointers: autograd hands out views (of a
+    concatenation's gradient, say), and so do users (one expert's bias out of a packed one), that may start anywhere."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _strided(t: torch.Tensor | None, multiple: int = 1) -> torch.Tensor | None:
+    """The same for calls that take rows apart from one another: a copy only where the rows are not contiguous, overlap
+    (a broadcast), or start off the boundary (the first on 16 bytes, the others `multiple` elements apart)."""
+    if t is None or (t.dim() == 2 and t.data_ptr() % 16 == 0 and (t.stride(1) == 1 or t.shape[1] == 1) and
+                     (t.shape[0] == 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % multiple == 0))):
+        return t
+    return _rows(t)
+
+
 class MoETopkGateFn(torch.autograd.Function):
     """(idx, gate) = topk_gate(logits); dlogits = topk_gate_bwd(dgate).  The
     expert ids are not differentiable; the gates' gradient reaches the router."""
 
     @staticmethod
     def forward(ctx, logits: torch.Tensor, k: int, renorm: int):
-        logits = logits.contiguous()
+        logits = _rows(logits)
         idx, gate = B.moe_topk_gate(logits, k, renorm, device_status=_status(logits))
         ctx.renorm = int(renorm)
         ctx.e = logits.shape[1]
@@ -118,12 +136,13 @@ class MoETopkGateFn(torch.autograd.Function):
     @first_order
     def backward(ctx, didx, dgate: torch.Tensor):
         logits, idx, gate = ctx.saved_tensors
-        dl = B.moe_topk_gate_bwd(logits, idx, gate, dgate.contiguous(), ctx.e, ctx.renorm)
+        dl = B.moe_topk_gate_bwd(logits, idx, gate, _rows(dgate), ctx.e, ctx.renorm)
         return dl, None, None
 
 
 def topk_gate(logits: torch.Tensor, k: int, renorm: int = 1):
-    return MoETopkGateFn.apply(logits.contiguous(), k, renorm)
+    # copies are made before the node, so that what it saves is its own input
+    return MoETopkGateFn.apply(_rows(logits), k, renorm)
 
 
 class MoEDispatchFn(torch.autograd.Function):
@@ -132,12 +151,12 @@ class MoEDispatchFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x: torch.Tensor, handle: B.Handle):
         ctx.handle = handle
-        return B.moe_dispatch(handle, x.contiguous())
+        return B.moe_dispatch(handle, _rows(x))
 
     @staticmethod
     @first_order
     def backward(ctx, dX: torch.Tensor):
-        return B.moe_dispatch_bwd(ctx.handle, dX.contiguous()), None
+        return B.moe_dispatch_bwd(ctx.handle, _rows(dX)), None
 
 
 class MoECombineFn(torch.autograd.Function):
@@ -145,8 +164,7 @@ class MoECombineFn(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, y: torch.Tensor, gate: torch.Tensor, handle: B.Handle):
-        y = y.contiguous()
-        gate = gate.contiguous()
+        y, gate = _rows(y), _rows(gate)
         ctx.handle = handle
         ctx.save_for_backward(y, gate)
         return B.moe_combine(handle, y, gate)
@@ -155,23 +173,16 @@ class MoECombineFn(torch.autograd.Function):
     @first_order
     def backward(ctx, dout: torch.Tensor):
         y, gate = ctx.saved_tensors
-        dY, dgate = B.moe_combine_bwd(ctx.handle, dout.contiguous(), gate, y)
+        dY, dgate = B.moe_combine_bwd(ctx.handle, _rows(dout), gate, y)
         return dY, dgate, None
 
 
 def dispatch(x: torch.Tensor, handle: B.Handle) -> torch.Tensor:
-    return MoEDispatchFn.apply(x.contiguous(), handle)
+    return MoEDispatchFn.apply(_rows(x), handle)
 
 
 def combine(y: torch.Tensor, gate: torch.Tensor, handle: B.Handle) -> torch.Tensor:
-    return MoECombineFn.apply(y.contiguous(), gate.contiguous(), handle)
-
-
-def _rows(t: torch.Tensor) -> torch.Tensor:
-    """A contiguous tensor on 16 bytes, as the library wants its pointers: autograd hands out views (of a
-    concatenation's gradient, say) that may start anywhere."""
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return MoECombineFn.apply(_rows(y), _rows(gate), handle)
 
 
 class LayerNormFn(torch.autograd.Function):
@@ -196,9 +207,7 @@ class LayerNormFn(torch.autograd.Function):
 def layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
               eps: float = 1e-5) -> torch.Tensor:
     """Layer norm of [s, m] rows."""
-    # copies are made before the node, so that what it saves is its own input
-    x = x if x.dim() == 2 and x.stride(1) == 1 and x.data_ptr() % 16 == 0 else _rows(x)
-    return LayerNormFn.apply(x, weight, bias, eps)
+    return LayerNormFn.apply(_strided(x), _rows(weight), _rows(bias), eps)
 
 
 class LinearFn(torch.autograd.Function):
@@ -236,9 +245,8 @@ class LinearFn(torch.autograd.Function):
 def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
            residual: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """y [s, N] = act(x W^T + bias) + residual, bf16 (or fp32) out."""
-    x = x if x.data_ptr() % 16 == 0 else _rows(x)
-    residual = residual if residual is None or residual.data_ptr() % 16 == 0 else _rows(residual)
-    return LinearFn.apply(x, W, bias, residual, act, out_dtype, torch.is_grad_enabled())
+    return LinearFn.apply(_strided(x, 8), _strided(W, 8), _rows(bias), _strided(residual), act, out_dtype,
+                          torch.is_grad_enabled())
 
 
 class BalanceLossFn(torch.autograd.Function):
@@ -262,7 +270,7 @@ class BalanceLossFn(torch.autograd.Function):
 def balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.Tensor | None = None,
                  seq_offsets: torch.Tensor | None = None):
     """(loss f32 [2]: the balance loss and the z loss, counts i32 [num_seqs, e], mean_prob f32 [num_seqs, e])."""
-    return BalanceLossFn.apply(logits, topk_idx, valid, seq_offsets)
+    return BalanceLossFn.apply(_rows(logits), _rows(topk_idx), _rows(valid), _rows(seq_offsets))
 
 
 class HandleRecorder:
