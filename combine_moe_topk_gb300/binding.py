@@ -184,6 +184,13 @@ def _addr(t: torch.Tensor | None):
     return t.data_ptr()
 
 
+def _status_addr(t: torch.Tensor | None, where: str):
+    """Address of a status word: the kernels set bits of an int32."""
+    if t is not None and 0 < t.numel() * t.element_size() < 4:
+        raise MoEError(1, where, "device_status must hold an int32")
+    return _addr(t)
+
+
 def _raw_stream(t: torch.Tensor):
     """The current stream of a CUDA tensor's device; a host tensor goes to the library, which rejects it."""
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
@@ -328,7 +335,7 @@ def moe_topk_gate(logits: torch.Tensor, k: int, renorm: int = 1, topk_idx: torch
     if topk_gate is None:
         topk_gate = torch.empty(s, k, dtype=torch.float32, device=dev)
     rc = lib().moe_topk_gate(_ptr(logits), s, e, int(k), int(renorm), _ptr(topk_idx), _ptr(topk_gate),
-                             _ptr(device_status), _stream(dev))
+                             _status_addr(device_status, "moe_topk_gate"), _stream(dev))
     _check(rc, "moe_topk_gate")
     return topk_idx, topk_gate
 
@@ -732,8 +739,8 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, valid: torch.
     ws = new(torch.uint8, nbytes)
     rc = L.moe_balance_loss(_addr(logits), _addr(topk_idx), _addr(valid), _addr(seq_offsets), s, e, topk_idx.shape[1],
                             n, loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(), lse.data_ptr(),
-                            coef.data_ptr(), norm.data_ptr(), ws.data_ptr(), nbytes, _addr(device_status),
-                            _raw_stream(logits))
+                            coef.data_ptr(), norm.data_ptr(), ws.data_ptr(), nbytes,
+                            _status_addr(device_status, "moe_balance_loss"), _raw_stream(logits))
     if rc:
         _check(rc, "moe_balance_loss")
     return BalanceLoss(loss, counts, mean_prob, lse, coef, norm)
@@ -797,7 +804,8 @@ def moe_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     pres, ldres = _rows_ptr(residual)
     d = LinearDesc(s, K, N, ACT[act], _DTYPE.get(y.dtype, -1), 0 if bias is None else _DTYPE.get(bias.dtype, -1),
                    0 if residual is None else _DTYPE.get(residual.dtype, -1), ldx, ldw, ldres)
-    rc = lib().moe_linear(d, px, pw, _addr(bias), pres, _addr(y), _addr(z), _addr(device_status), _raw_stream(x))
+    rc = lib().moe_linear(d, px, pw, _addr(bias), pres, _addr(y), _addr(z),
+                          _status_addr(device_status, "moe_linear"), _raw_stream(x))
     if rc:
         _check(rc, "moe_linear")
     return (y, z) if save_z else y
@@ -830,8 +838,8 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     pz, ldz = _rows_ptr(z)
     d = LinearBwdDesc(s, K, N, ACT[act], _DTYPE.get(dy.dtype, -1), _DTYPE.get(dx_dtype, -1), _DTYPE.get(dw_dtype, -1),
                       lddy, ldx, ldw, ldz)
-    rc = L.moe_linear_bwd(d, pdy, px, pw, pz, _addr(dx), _addr(dW), _addr(db), _addr(ws), nbytes, _addr(device_status),
-                          _raw_stream(x))
+    rc = L.moe_linear_bwd(d, pdy, px, pw, pz, _addr(dx), _addr(dW), _addr(db), _addr(ws), nbytes,
+                          _status_addr(device_status, "moe_linear_bwd"), _raw_stream(x))
     if rc:
         _check(rc, "moe_linear_bwd")
     return dx, dW, db

@@ -260,3 +260,19 @@ def test_block_calls_reject_bad_arguments_without_a_gpu(lib):
     assert rc_name(lib.moe_linear_bwd(ctypes.byref(b), fake, fake, fake, None, fake, fake, fake, fake, 1 << 30, None,
                                       None)) == "MOE_ERR_DTYPE"
     assert lib.moe_linear_bwd_workspace(0, 8) == 0 and lib.moe_linear_bwd_workspace(16, 8) > 0
+
+
+@pytest.mark.parametrize("dtype", ["uint8", "bool", "int16"])
+def test_a_status_word_that_is_too_small_is_refused(lib, dtype):
+    # the kernels set bits of four bytes
+    import torch
+
+    st = torch.zeros(1, dtype=getattr(torch, dtype))
+    x, W = torch.zeros(4, 8).bfloat16(), torch.zeros(3, 8).bfloat16()
+    logits, idx = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: B.moe_linear(x, W, device_status=st),
+                 lambda: B.moe_linear_bwd(torch.zeros(4, 3).bfloat16(), x, W, device_status=st),
+                 lambda: B.moe_balance_loss(logits, idx, device_status=st),
+                 lambda: B.moe_topk_gate(logits, 2, device_status=st)):
+        with pytest.raises(B.MoEError, match="device_status"):
+            call()
