@@ -677,11 +677,16 @@ __device__ __forceinline__ void join_parts(const GemmArgs& p, const Unit& t, int
   }
 }
 
-// kExact (fp32 outputs): the tensor cores' accumulator drops the bits below
-// its last place at every step (measured: 4.4e-6 of the result over 4096
-// terms, against 6e-7 for fp32 additions), so a product hands its sum over
-// every kExactBlocks K blocks, and the epilogue adds these up in registers.
+// kExact (fp32 outputs, and sums of more than kLongSum terms): the tensor cores'
+// accumulator drops the bits below its last place at every step (measured:
+// 4.4e-6 of the result over 4096 terms, against 6e-7 for fp32 additions), so a
+// product hands its sum over every kExactBlocks K blocks, and the epilogue adds
+// these up in registers.  Where all terms have one sign, n of them come out up to
+// n / 16 units of 2^-24 short: at kLongSum 2^-10, a quarter of what rounding to bf16
+// may take, so a bf16 output keeps the one accumulator up to there (4096 x 4096 from
+// 2^19 terms takes 20.3 ms this way; that way 13.1, and up to 2e-3 short).
 constexpr int kExactBlocks = 4;
+constexpr int kLongSum = 1 << 18;
 
 // kSplit (CG = 1): where tiles are too few to fill the machine, a cluster of
 // 2, 4 or 8 CTAs shares one, each with its part of the contracted axis.  They
@@ -1359,7 +1364,8 @@ cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const Devi
 template <bool AT, bool BT>
 cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
                     int32_t* status, const DeviceInfo& di, cudaStream_t st) {
-  const Plan q = plan_gemm(M, N, K, epi.out_f32);
+  const bool exact = epi.out_f32 || K > kLongSum;
+  const Plan q = plan_gemm(M, N, K, exact);
   CUtensorMap maps[4] = {};
   const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
   if (!(AT ? make_map(&maps[0], A, M, K, lda, 64) : make_map(&maps[0], A, K, M, lda, 128)) ||
@@ -1374,7 +1380,7 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
   // the longest wait is the epilogue's, for a tile's whole contraction: 0.65 us a K block when all is well
   const long long limit = kWaitNs + 20000LL * q.per_split;
   GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, limit};
-  if (epi.out_f32)
+  if (exact)
     return q.kind == 1 ? run_gemm<1, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
   switch (q.kind) {
     case 0: return run_gemm<2, 256, AT, BT, false>(maps, p, di, st);

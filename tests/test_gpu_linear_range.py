@@ -80,3 +80,21 @@ def test_gelu_keeps_its_relative_precision_in_the_tail(s):
     cdf, pdf = normal(zz)
     tol = (24 + 2 * zz * zz) * U * (cdf + np.abs(zz) * pdf)
     assert (np.abs(f64(db) - (cdf + zz * pdf)) <= tol + 1e-44).all()
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_long_sums_into_bf16(back):
+    """Half a million terms, all positive: the sum may be off by (64 + K/512 + 10) u before it is rounded to bf16, at
+    most half a unit in its last place (2^-8 of the power of two below it)."""
+    n, K = 2304, 2 ** 19
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a, c = (torch.rand(*((K, n) if back else (n, K)), generator=g, device="cuda").bfloat16() for _ in range(2))
+    if back:
+        W = torch.zeros(n, n, device="cuda").bfloat16()
+        _, got, _ = B.moe_linear_bwd(a, c, W, need_dx=False, need_db=False)
+        a, c = a[:, :64].t(), c[:, :64].t()
+    else:
+        got = B.moe_linear(a, c)
+    want = a[:64].double() @ c[:64].double().t()
+    tol = 2.0 ** (want.log2().floor() - 8) + (64 + K / 512 + 10) * U * want
+    assert ((got[:64, :64].double() - want).abs() <= tol).all()
