@@ -42,6 +42,7 @@ EXPORTS = [
     "moe_topk_gate_layout", "moe_ep_pack", "moe_ep_dispatch", "moe_ep_combine", "moe_ep_unpack_dgate",
     "moe_layernorm", "moe_layernorm_bwd", "moe_layernorm_bwd_workspace", "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_balance_loss_workspace", "moe_linear", "moe_linear_bwd", "moe_linear_bwd_workspace",
+    "moe_linear_bwd_workspace_for",
 ]
 
 
@@ -133,6 +134,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.argtypes = [I, I]
             f.restype = Z
+        L.moe_linear_bwd_workspace_for.argtypes = [ctypes.POINTER(LinearBwdDesc), I, I, I]
+        L.moe_linear_bwd_workspace_for.restype = Z
         L.moe_capacity.argtypes = [ctypes.c_double, I, I, I]
         L.moe_capacity.restype = I
         L.moe_status_string.argtypes = [I]
@@ -830,14 +833,14 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     dW = new(dw_dtype, N, K) if need_dw else None
     db = new(torch.float32, N) if need_db else None
     L = lib()
-    nbytes = L.moe_linear_bwd_workspace(s, N)
-    ws = new(torch.uint8, nbytes) if nbytes else None
     pdy, lddy = _rows_ptr(dy)
     px, ldx = _rows_ptr(x)
     pw, ldw = _rows_ptr(W)
     pz, ldz = _rows_ptr(z)
     d = LinearBwdDesc(s, K, N, ACT[act], _DTYPE.get(dy.dtype, -1), _DTYPE.get(dx_dtype, -1), _DTYPE.get(dw_dtype, -1),
                       lddy, ldx, ldw, ldz)
+    nbytes = L.moe_linear_bwd_workspace_for(d, need_dx, need_dw, need_db)
+    ws = new(torch.uint8, nbytes) if nbytes else None
     rc = L.moe_linear_bwd(d, pdy, px, pw, pz, _addr(dx), _addr(dW), _addr(db), _addr(ws), nbytes,
                           _status_addr(device_status, "moe_linear_bwd"), _raw_stream(x))
     if rc:

@@ -1155,6 +1155,11 @@ size_t moe_linear_bwd_workspace(int s, int N) {
   return moe::linear_bwd_workspace(s, N);
 }
 
+size_t moe_linear_bwd_workspace_for(const moe_linear_bwd_desc* d, int dx, int dW, int db) {
+  if (!d || d->s < 1 || d->N < 1) return 0;
+  return moe::linear_bwd_workspace(d->s, d->N, d->act, d->dy_dtype == MOE_F32, d->lddy, dx || dW, db != 0);
+}
+
 moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const void* x, const void* W,
                           const void* z, void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
                           int32_t* device_status, void* stream) {
@@ -1169,10 +1174,11 @@ moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const vo
   MOE_TRY(check_status_ptr(device_status));
   if (!dx && !dW && !db) return MOE_OK;
   if (none && !dW && !db) return MOE_OK;
-  MOE_TRY(check_workspace(workspace, workspace_bytes, moe_linear_bwd_workspace(d->s, d->N)));
+  const size_t need = moe_linear_bwd_workspace_for(d, dx != nullptr, dW != nullptr, db != nullptr);
+  MOE_TRY(check_workspace(workspace, workspace_bytes, need));
   int dev = 0;
   MOE_TRY(check_ptrs({{dy, "dy", none}, {x, "x", none || !dW}, {W, "W", none || !dx}, {z, "z", none || !need_z},
-                      {dx, "dx", true}, {dW, "dW", true}, {db, "db", true}, {workspace, "workspace", none}}, &dev));
+                      {dx, "dx", true}, {dW, "dW", true}, {db, "db", true}, {workspace, "workspace", need == 0}}, &dev));
   MOE_TRY(check_device_ptr(device_status, "device_status", dev));
   const moe::DeviceInfo* di = nullptr;
   MOE_TRY(device_state(dev, &di));

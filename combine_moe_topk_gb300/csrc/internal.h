@@ -209,7 +209,8 @@ struct LinearBwdArgs {
   long long lddy, ldx, ldw, ldz;
   int s, K, N, act, dy_f32, dx_f32, dw_f32;
 };
-size_t linear_bwd_workspace(int s, int N);
+size_t linear_bwd_workspace(int s, int N);  // enough for every call
+size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool db);
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace moe

@@ -1411,21 +1411,31 @@ int slope_rows(int s, int N) {  // blocks along the rows: enough to fill the mac
   return rows < 1 ? 1 : rows;
 }
 
+// dz, where it is not dy itself, and the partial sums of db.
 struct BwdPlan {
   size_t dz, part, total;
 };
-BwdPlan plan_bwd(int s, int N) {
+BwdPlan plan_bwd(int s, int N, bool own_dz, bool db) {
   BwdPlan q;
   size_t at = 0;
-  q.dz = at, at += up((size_t)s * ((N + 7) / 8 * 8) * 2);
-  q.part = at, at += up((size_t)slope_rows(s, N) * N * 4);
+  q.dz = at, at += own_dz ? up((size_t)s * ((N + 7) / 8 * 8) * 2) : 0;
+  q.part = at, at += db ? up((size_t)slope_rows(s, N) * N * 4) : 0;
   q.total = at;
   return q;
 }
 
+// Without an activation a bf16 dy with whole 16-byte rows is dz itself.
+bool own_dz(bool products, int act, bool dy_f32, long long lddy) {
+  return products && (act != MOE_ACT_NONE || dy_f32 || lddy % 8 != 0);
+}
+
 }  // namespace
 
-size_t linear_bwd_workspace(int s, int N) { return plan_bwd(s, N).total; }
+size_t linear_bwd_workspace(int s, int N) { return plan_bwd(s, N, true, true).total; }
+
+size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool db) {
+  return plan_bwd(s, N, own_dz(products, act, dy_f32, lddy), db).total;
+}
 
 namespace {
 
@@ -1461,16 +1471,15 @@ cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_
 }
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  const BwdPlan q = plan_bwd(a.s, a.N);
+  const bool own = own_dz(a.dx || a.dW, a.act, a.dy_f32, a.lddy);
+  const BwdPlan q = plan_bwd(a.s, a.N, own, a.db != nullptr);
   char* ws = static_cast<char*>(a.workspace);
-  // without an activation a bf16 dy with whole 16-byte rows is dz itself
-  const bool own_dz = (a.dx || a.dW) && (a.act != MOE_ACT_NONE || a.dy_f32 || a.lddy % 8 != 0);
   const int lddz = (a.N + 7) / 8 * 8;
-  if (own_dz || a.db) {
+  if (own || a.db) {
     SlopeArgs p = {};
     p.dy = a.dy;
     p.z = a.act != MOE_ACT_NONE ? static_cast<const bf16*>(a.z) : nullptr;  // unused without an activation
-    p.dz = own_dz ? reinterpret_cast<bf16*>(ws + q.dz) : nullptr;
+    p.dz = own ? reinterpret_cast<bf16*>(ws + q.dz) : nullptr;
     p.part = a.db ? reinterpret_cast<float*>(ws + q.part) : nullptr;
     p.lddy = a.lddy;
     p.ldz = a.ldz;
@@ -1488,8 +1497,8 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
       if (err != cudaSuccess) return err;
     }
   }
-  const void* dz = own_dz ? ws + q.dz : a.dy;
-  const long long ld = own_dz ? lddz : a.lddy;
+  const void* dz = own ? ws + q.dz : a.dy;
+  const long long ld = own ? lddz : a.lddy;
   if (a.dx) {
     Epi e = {};
     e.out = a.dx;

@@ -561,8 +561,12 @@ typedef struct {
   int64_t lddy, ldx, ldw, ldz;
 } moe_linear_bwd_desc;
 
-/* Bytes of moe_linear_bwd's workspace: dz, and partial sums of db. */
+/* Bytes of moe_linear_bwd's workspace, dz and partial sums of db: enough for
+ * every call of these sizes, and what a call with this description needs that
+ * asks for dx, dW and db (0 or not) -- no dz where a bf16 dy without an
+ * activation is dz itself, or for db alone; 0: the workspace may be NULL. */
 size_t moe_linear_bwd_workspace(int s, int N);
+size_t moe_linear_bwd_workspace_for(const moe_linear_bwd_desc* desc, int dx, int dW, int db);
 
 /* Backward of moe_linear (the residual's gradient is dy itself):
  *   dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum_t dz.

@@ -276,3 +276,22 @@ def test_a_status_word_that_is_too_small_is_refused(lib, dtype):
                  lambda: B.moe_topk_gate(logits, 2, device_status=st)):
         with pytest.raises(B.MoEError, match="device_status"):
             call()
+
+
+def test_a_product_backward_asks_for_the_workspace_it_uses(lib):
+    s, N = 512, 264
+    need = lambda act=0, dy=1, lddy=N, dx=1, dW=1, db=1: lib.moe_linear_bwd_workspace_for(  # noqa: E731
+        ctypes.byref(B.LinearBwdDesc(s, 64, N, act, dy, 1, 1, lddy, 64, 64, N)), dx, dW, db)
+    most = lib.moe_linear_bwd_workspace(s, N)
+    dz = s * N * 2
+    assert need(db=0) == 0 and need(act=4, dx=0, dW=0, db=0) == 0
+    assert 0 < need() < dz, "a bf16 dy without an activation is dz itself"
+    assert need(act=4, dx=0, dW=0) == need()
+    assert need(act=4, db=0) >= dz and need(dy=0, db=0) >= dz and need(lddy=N + 3, db=0) >= dz
+    assert need(act=4) == need(act=4, db=0) + need() <= most
+    assert lib.moe_linear_bwd_workspace_for(None, 1, 1, 1) == 0
+    fake = P(0x10000)
+    d = B.LinearBwdDesc(s, 64, N, 4, 1, 1, 1, N, 64, 64, N)
+    assert rc_name(lib.moe_linear_bwd(ctypes.byref(d), fake, fake, fake, fake, fake, fake, fake, fake, need(act=4) - 1, None,
+                                      None)) == "MOE_ERR_INVALID_ARG"
+    assert "workspace" in lib.moe_last_error().decode()

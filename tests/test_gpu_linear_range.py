@@ -98,3 +98,16 @@ def test_long_sums_into_bf16(back):
     want = a[:64].double() @ c[:64].double().t()
     tol = 2.0 ** (want.log2().floor() - 8) + (64 + K / 512 + 10) * U * want
     assert ((got[:64, :64].double() - want).abs() <= tol).all()
+
+
+def test_a_backward_without_an_activation_takes_no_room_for_dz():
+    s, N, K = 4096, 2048, 64
+    dy, x, W = torch.randn(s, N, device="cuda").bfloat16(), torch.randn(s, K, device="cuda").bfloat16(), \
+        torch.randn(N, K, device="cuda").bfloat16()
+    B.moe_linear_bwd(dy, x, W)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    out = B.moe_linear_bwd(dy, x, W)
+    outputs = sum((t.numel() * t.element_size() + 511) // 512 * 512 for t in out)
+    assert torch.cuda.max_memory_allocated() - before < outputs + s * N * 2
