@@ -1157,7 +1157,8 @@ size_t moe_linear_bwd_workspace(int s, int N) {
 
 size_t moe_linear_bwd_workspace_for(const moe_linear_bwd_desc* d, int dx, int dW, int db) {
   if (!d || d->s < 1 || d->N < 1) return 0;
-  return moe::linear_bwd_workspace(d->s, d->N, d->act, d->dy_dtype == MOE_F32, d->lddy, dx || dW, db != 0);
+  return moe::linear_bwd_workspace(d->s, d->N, d->act, d->dy_dtype == MOE_F32, d->lddy, dx || dW,
+                                   (dx && d->dx_dtype == MOE_F32) || (dW && d->dw_dtype == MOE_F32), db != 0);
 }
 
 moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const void* x, const void* W,

@@ -210,7 +210,7 @@ struct LinearBwdArgs {
   int s, K, N, act, dy_f32, dx_f32, dw_f32;
 };
 size_t linear_bwd_workspace(int s, int N);  // enough for every call
-size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool db);
+size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool f32_results, bool db);
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace moe

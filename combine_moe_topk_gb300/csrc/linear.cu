@@ -29,6 +29,8 @@
 // Every mbarrier wait is bounded on the global timer, each from its own start, so
 // that a long product does not run into the limit; a time-out records
 // MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
+#include <math_constants.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -229,6 +231,7 @@ __device__ __forceinline__ void finish1(const Epi& e, long long row, int col, in
 struct GemmArgs {
   int M, N, K;
   int tiles_m, tiles_n, splits, per_split, kblocks;  // K blocks of 128
+  int pass, lower;  // kTwice: K blocks of one pass over B, rows from A's first terms to its second
   Epi epi;
   int32_t* status;
   long long timeout_ns;  // of a single wait
@@ -694,7 +697,13 @@ constexpr int kLongSum = 1 << 18;
 // share of the tile's rows (join_parts).  Partial products in global memory and
 // a second kernel to add them took 13 to 16 us at 64 x 4096 x 4096 (11.9 this
 // way), another launch and a workspace.
-template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit>
+//
+// kTwice (gradients in fp32): A is a sum of two bf16 terms, the second `lower` rows
+// below the first, so the contracted axis is gone through twice.  Tiles that
+// reach past the first term's end read into the second: rows of D that are not
+// stored, or terms that meet B's zeros.  (As a second product with the first
+// one's result for its residual: 16384 x 4096 x 128, dx and dW, 309 us; this way 125.)
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
@@ -766,16 +775,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         uint8_t* sa = smem + stage * S::kStage;
+        const bool second = kTwice && kb >= p.pass;
+        const int lower = second ? p.lower : 0, kb_in = second ? kb - p.pass : kb;
         const uint32_t fb = CG == 2 ? mapa_shared(smem_addr(&full[stage]), 0) : smem_addr(&full[stage]);
         if (rank == 0) mbar_arrive_expect_tx(&full[stage], CG * S::kStage);
 #pragma unroll
         for (int q = 0; q < kKB; ++q) {
-          const int k = (kb * kKB + q) * 64;
+          const int k = (kb_in * kKB + q) * 64;
           if constexpr (AT) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) load_tile<CG>(sa + q * kSubA + g * 8192, &tmA, m0 + 64 * g, k, fb);
+            for (int g = 0; g < 2; ++g) load_tile<CG>(sa + q * kSubA + g * 8192, &tmA, m0 + 64 * g, k + lower, fb);
           } else {
-            load_tile<CG>(sa + q * kSubA, &tmA, k, m0, fb);
+            load_tile<CG>(sa + q * kSubA, &tmA, k, m0 + lower, fb);
           }
           uint8_t* sb = sa + kKB * kSubA + q * S::kSubB;
           if constexpr (BT) {
@@ -1188,8 +1199,11 @@ struct SlopeArgs {
 // unrolled in fewer (8192 x 4096 silu, sums alone: four rows in two blocks 46.6 us,
 // two in four 35.6, one in six 27.4; gelu at 8192 x 8192 81.6, with its slope two
 // values an instruction 95.7, though 70 against 75 where L2 holds the data).  dz is
-// rounded to bf16 for the tensor cores; the sums are taken before that.
-template <int W, bool kF32, int kAct>
+// rounded to bf16 for the tensor cores; the sums are taken before that.  For an
+// fp32 result what the rounding left is stored too (kTwo), and the product
+// goes over both: dz to 2^-16.  A bf16 result is rounded as coarsely as dz.  (kTwo as an
+// argument of the kernel instead: gelu at 8192 x 8192 94 us.)
+template <int W, bool kF32, int kAct, bool kTwo>
 __global__ void __launch_bounds__(256, 6) slope_kernel(const SlopeArgs p) {
   __shared__ float acc[8][32 * W + 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1222,8 +1236,19 @@ __global__ void __launch_bounds__(256, 6) slope_kernel(const SlopeArgs p) {
         sum[j] += d[j];
       }
       if (p.dz) {
-        if (W == 8) *reinterpret_cast<uint4*>(p.dz + row * p.lddz + col) = Vec<bf16>::from_float(d);
-        else p.dz[row * p.lddz + col] = __float2bfloat16_rn(d[0]);
+        bf16* at = p.dz + row * p.lddz + col;
+        if (W == 8) *reinterpret_cast<uint4*>(at) = Vec<bf16>::from_float(d);
+        else *at = __float2bfloat16_rn(d[0]);
+        if (kTwo) {  // and what the rounding left, [s][lddz] further on
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            d[j] -= __bfloat162float(__float2bfloat16_rn(d[j]));
+            if (!(fabsf(d[j]) < CUDART_INF_F)) d[j] = 0.f;  // of an infinity or a NaN
+          }
+          at += (long long)p.s * p.lddz;
+          if (W == 8) *reinterpret_cast<uint4*>(at) = Vec<bf16>::from_float(d);
+          else *at = __float2bfloat16_rn(d[0]);
+        }
       }
     }
   }
@@ -1289,14 +1314,14 @@ constexpr long long kWaitNs = 2000000000LL;  // the limit of a device wait
 // four parts of 128 x 128 (11.8; two 14.8, unsplit 20.2, wide 26.7), 1024^3 to
 // 128 x 64 (7.8 against 12.8 and 9.9), 64 x 1024 x 1024 to four parts of that (5.8;
 // unsplit 6.9).
-Plan plan_gemm(int M, int N, int K, bool exact) {
+Plan plan_gemm(int M, int N, int K, int passes, bool exact) {
   const double cost[kKinds] = {1.0, 0.70, 0.66}, base[kKinds] = {9.0, 8.0, 6.0};
   // clusters of 2, 4 and 8 CTAs that run at once (sixteen of eight did not: 2048 x
   // 4096 x 128 18.6 us, in four parts 10.2)
   const int clusters[4] = {0, 72, 34, 8};
   Plan best = {};
   double best_t = 0;
-  const int kblocks = (K + 127) / 128;
+  const int kblocks = (K + 127) / 128 * passes;
   for (int k = exact ? 1 : 0; k < kKinds; ++k) {  // exact: its running sums need registers, so not the widest
     Plan q;
     q.kind = k;
@@ -1323,12 +1348,12 @@ Plan plan_gemm(int M, int N, int K, bool exact) {
   return best;
 }
 
-template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit>
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice>
 cudaError_t run_one(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
   typedef Shape<CG, BN> S;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (err != cudaSuccess) return err;
   const long long units = (long long)p.tiles_m * p.tiles_n;
@@ -1349,26 +1374,28 @@ cudaError_t run_one(const CUtensorMap (&maps)[4], const GemmArgs& p, const Devic
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact, kSplit>, maps[0], maps[1], maps[2], maps[3], p);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice>, maps[0], maps[1], maps[2], maps[3], p);
 }
 
-template <int CG, int BN, bool AT, bool BT, bool kExact>
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kTwice = false>
 cudaError_t run_gemm(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
   if constexpr (CG == 1) {
-    if (p.splits > 1) return run_one<CG, BN, AT, BT, kExact, true>(maps, p, di, st);
+    if (p.splits > 1) return run_one<CG, BN, AT, BT, kExact, true, kTwice>(maps, p, di, st);
   }
-  return run_one<CG, BN, AT, BT, kExact, false>(maps, p, di, st);
+  return run_one<CG, BN, AT, BT, kExact, false, kTwice>(maps, p, di, st);
 }
 
-// D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).
+// D [M,N] = A B^T with A [M][K] (AT: [K][M]) and B [N][K] (BT: [K][N]).  twice: A is
+// the sum of two such matrices, one behind the other (BT and fp32 results only).
 template <bool AT, bool BT>
-cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
+cudaError_t product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, bool twice, Epi epi,
                     int32_t* status, const DeviceInfo& di, cudaStream_t st) {
   const bool exact = epi.out_f32 || K > kLongSum;
-  const Plan q = plan_gemm(M, N, K, exact);
+  const int passes = twice ? 2 : 1, rows = AT ? K : M;
+  const Plan q = plan_gemm(M, N, K, passes, exact);
   CUtensorMap maps[4] = {};
   const int box_b = BT ? 64 : kKindBN[q.kind] / kKindCG[q.kind];
-  if (!(AT ? make_map(&maps[0], A, M, K, lda, 64) : make_map(&maps[0], A, K, M, lda, 128)) ||
+  if (!make_map(&maps[0], A, AT ? M : K, (uint64_t)rows * passes, lda, AT ? 64 : 128) ||
       !(BT ? make_map(&maps[1], B, N, K, ldb, box_b) : make_map(&maps[1], B, K, N, ldb, box_b)))
     return cudaErrorInvalidValue;
   epi.wide = N % 8 == 0 && (!epi.res || epi.ldres % 8 == 0);
@@ -1379,7 +1406,12 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
     return cudaErrorInvalidValue;
   // the longest wait is the epilogue's, for a tile's whole contraction: 0.65 us a K block when all is well
   const long long limit = kWaitNs + 20000LL * q.per_split;
-  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, epi, status, limit};
+  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks,
+                q.kblocks / passes, rows, epi, status, limit};
+  if constexpr (BT) {
+    if (twice)
+      return q.kind == 1 ? run_gemm<1, 128, AT, BT, true, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true, true>(maps, p, di, st);
+  }
   if (exact)
     return q.kind == 1 ? run_gemm<1, 128, AT, BT, true>(maps, p, di, st) : run_gemm<1, 64, AT, BT, true>(maps, p, di, st);
   switch (q.kind) {
@@ -1411,46 +1443,55 @@ int slope_rows(int s, int N) {  // blocks along the rows: enough to fill the mac
   return rows < 1 ? 1 : rows;
 }
 
-// dz, where it is not dy itself, and the partial sums of db.
+// dz, where it is not dy itself (once, or with what its rounding left), and the
+// partial sums of db.
 struct BwdPlan {
   size_t dz, part, total;
 };
-BwdPlan plan_bwd(int s, int N, bool own_dz, bool db) {
+BwdPlan plan_bwd(int s, int N, int dz, bool db) {
   BwdPlan q;
   size_t at = 0;
-  q.dz = at, at += own_dz ? up((size_t)s * ((N + 7) / 8 * 8) * 2) : 0;
+  q.dz = at, at += up((size_t)s * ((N + 7) / 8 * 8) * 2 * dz);
   q.part = at, at += db ? up((size_t)slope_rows(s, N) * N * 4) : 0;
   q.total = at;
   return q;
 }
 
-// Without an activation a bf16 dy with whole 16-byte rows is dz itself.
-bool own_dz(bool products, int act, bool dy_f32, long long lddy) {
-  return products && (act != MOE_ACT_NONE || dy_f32 || lddy % 8 != 0);
+// Copies of dz: none where a bf16 dy with whole 16-byte rows, without an
+// activation, is dz itself; two where dz is rounded and a result is fp32.
+int copies_of_dz(bool products, bool f32_results, int act, bool dy_f32, long long lddy) {
+  const bool rounded = act != MOE_ACT_NONE || dy_f32;
+  if (!products || (!rounded && lddy % 8 == 0)) return 0;
+  return rounded && f32_results ? 2 : 1;
 }
 
 }  // namespace
 
-size_t linear_bwd_workspace(int s, int N) { return plan_bwd(s, N, true, true).total; }
+size_t linear_bwd_workspace(int s, int N) { return plan_bwd(s, N, 2, true).total; }
 
-size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool db) {
-  return plan_bwd(s, N, own_dz(products, act, dy_f32, lddy), db).total;
+size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool f32_results, bool db) {
+  return plan_bwd(s, N, copies_of_dz(products, f32_results, act, dy_f32, lddy), db).total;
 }
 
 namespace {
 
-template <int W, bool kF32>
+template <int W, bool kF32, bool kTwo>
 cudaError_t run_slope(const SlopeArgs& p, int act, int rows, cudaStream_t st) {
   const dim3 grid((unsigned)((p.lddz + 32 * W - 1) / (32 * W)), (unsigned)rows);
-  auto kern = slope_kernel<W, kF32, MOE_ACT_NONE>;
+  auto kern = slope_kernel<W, kF32, MOE_ACT_NONE, kTwo>;
   switch (act) {
-    case MOE_ACT_RELU: kern = slope_kernel<W, kF32, MOE_ACT_RELU>; break;
-    case MOE_ACT_GELU: kern = slope_kernel<W, kF32, MOE_ACT_GELU>; break;
-    case MOE_ACT_GELU_TANH: kern = slope_kernel<W, kF32, MOE_ACT_GELU_TANH>; break;
-    case MOE_ACT_SILU: kern = slope_kernel<W, kF32, MOE_ACT_SILU>; break;
+    case MOE_ACT_RELU: kern = slope_kernel<W, kF32, MOE_ACT_RELU, kTwo>; break;
+    case MOE_ACT_GELU: kern = slope_kernel<W, kF32, MOE_ACT_GELU, kTwo>; break;
+    case MOE_ACT_GELU_TANH: kern = slope_kernel<W, kF32, MOE_ACT_GELU_TANH, kTwo>; break;
+    case MOE_ACT_SILU: kern = slope_kernel<W, kF32, MOE_ACT_SILU, kTwo>; break;
     default: break;
   }
   return launch_chained(kern, grid, dim3(256), 0, st, p);
+}
+
+template <int W, bool kF32>
+cudaError_t run_slope(const SlopeArgs& p, int act, int rows, bool two, cudaStream_t st) {
+  return two ? run_slope<W, kF32, true>(p, act, rows, st) : run_slope<W, kF32, false>(p, act, rows, st);
 }
 
 }  // namespace
@@ -1467,11 +1508,12 @@ cudaError_t launch_linear(const LinearArgs& a, const DeviceInfo& di, cudaStream_
   e.bias_f32 = a.bias_f32;
   e.res_f32 = a.res_f32;
   if (a.s <= kFewRows) return a.s > 8 ? few_rows<true>(a, e, di, st) : few_rows<false>(a, e, di, st);
-  return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.status, di, st);
+  return product<false, false>(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, false, e, a.status, di, st);
 }
 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  const bool own = own_dz(a.dx || a.dW, a.act, a.dy_f32, a.lddy);
+  const bool f32_dx = a.dx && a.dx_f32, f32_dw = a.dW && a.dw_f32;
+  const int own = copies_of_dz(a.dx || a.dW, f32_dx || f32_dw, a.act, a.dy_f32, a.lddy);
   const BwdPlan q = plan_bwd(a.s, a.N, own, a.db != nullptr);
   char* ws = static_cast<char*>(a.workspace);
   const int lddz = (a.N + 7) / 8 * 8;
@@ -1489,8 +1531,8 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
     const int rows = slope_rows(a.s, a.N);
     const bool wide = a.N % 8 == 0 && a.lddy % 8 == 0 && (!p.z || a.ldz % 8 == 0);
     cudaError_t err;
-    if (wide) err = a.dy_f32 ? run_slope<8, true>(p, a.act, rows, st) : run_slope<8, false>(p, a.act, rows, st);
-    else err = a.dy_f32 ? run_slope<1, true>(p, a.act, rows, st) : run_slope<1, false>(p, a.act, rows, st);
+    if (wide) err = a.dy_f32 ? run_slope<8, true>(p, a.act, rows, own == 2, st) : run_slope<8, false>(p, a.act, rows, own == 2, st);
+    else err = a.dy_f32 ? run_slope<1, true>(p, a.act, rows, own == 2, st) : run_slope<1, false>(p, a.act, rows, own == 2, st);
     if (err != cudaSuccess) return err;
     if (a.db) {
       err = launch_sum_parts(p.part, rows, 0, a.N, a.N, a.db, nullptr, st);
@@ -1503,14 +1545,14 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
     Epi e = {};
     e.out = a.dx;
     e.out_f32 = a.dx_f32;
-    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, e, a.status, di, st);
+    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, own == 2 && f32_dx, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   if (a.dW) {
     Epi e = {};
     e.out = a.dW;
     e.out_f32 = a.dw_f32;
-    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, e, a.status, di, st);
+    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, own == 2 && f32_dw, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

@@ -571,10 +571,11 @@ size_t moe_linear_bwd_workspace_for(const moe_linear_bwd_desc* desc, int dx, int
 /* Backward of moe_linear (the residual's gradient is dy itself):
  *   dz = dy act'(z);  dx = dz W;  dW = dz^T x;  db = sum_t dz.
  * dy [s,N] fp32 or bf16, z bf16 [s,N] (may be NULL without an activation);
- * dx [s,K] and dW [N,K] fp32 or bf16, db f32 [N], each nullable.  dz is
- * rounded to bf16 for the two products (2^-9 of each term, averaged over the
- * sums) unless it is a bf16 dy itself; db sums it in fp32 before that.  All sums run in a
- * fixed order: the same bits on every run.  With s = 0, dW and db are zeroed. */
+ * dx [s,K] and dW [N,K] fp32 or bf16, db f32 [N], each nullable.  For a bf16
+ * result dz is rounded to bf16 too (at most 2^-8 of each term, averaged over
+ * the sum) unless it is a bf16 dy itself; for an fp32 result it is taken in two
+ * bf16 terms (to 2^-16), which doubles that product's time.  db sums it in fp32
+ * before that.  All sums run in a fixed order: the same bits on every run.  With s = 0, dW and db are zeroed. */
 moe_status moe_linear_bwd(const moe_linear_bwd_desc* desc, const void* dy, const void* x, const void* W,
                           const void* z, void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
                           int32_t* device_status, void* stream);

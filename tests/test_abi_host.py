@@ -289,6 +289,8 @@ def test_a_product_backward_asks_for_the_workspace_it_uses(lib):
     assert need(act=4, dx=0, dW=0) == need()
     assert need(act=4, db=0) >= dz and need(dy=0, db=0) >= dz and need(lddy=N + 3, db=0) >= dz
     assert need(act=4) == need(act=4, db=0) + need() <= most
+    two = lib.moe_linear_bwd_workspace_for(ctypes.byref(B.LinearBwdDesc(s, 64, N, 4, 1, 0, 1, N, 64, 64, N)), 1, 1, 1)
+    assert two == need(act=4) + dz == most, "an fp32 result takes dz in two terms"
     assert lib.moe_linear_bwd_workspace_for(None, 1, 1, 1) == 0
     fake = P(0x10000)
     d = B.LinearBwdDesc(s, 64, N, 4, 1, 1, 1, N, 64, 64, N)

@@ -111,3 +111,44 @@ def test_a_backward_without_an_activation_takes_no_room_for_dz():
     out = B.moe_linear_bwd(dy, x, W)
     outputs = sum((t.numel() * t.element_size() + 511) // 512 * 512 for t in out)
     assert torch.cuda.max_memory_allocated() - before < outputs + s * N * 2
+
+
+@pytest.mark.parametrize("s,K,N", [(1, 64, 8), (7, 136, 33), (130, 264, 129), (300, 1032, 70), (700, 256, 2051), (4100, 72, 130)])
+@pytest.mark.parametrize("act,dy_dtype", [("none", torch.float32), ("silu", torch.bfloat16), ("gelu", torch.float32)])
+def test_fp32_gradients_take_dz_to_more_than_bf16(s, K, N, act, dy_dtype):
+    """An fp32 result takes dz in two bf16 terms: off by 2^-16 of each term at most, the activation's slope by 24 u of
+    |dy| times the slope's terms (below 1.2 each), and the sums' own chain."""
+    from oracle import block as O
+
+    g = torch.Generator().manual_seed(s + N)
+    x, W = torch.randn(s, K, generator=g).bfloat16().cuda(), (torch.randn(N, K, generator=g) / K ** 0.5).bfloat16().cuda()
+    dy, z = torch.randn(s, N, generator=g).to(dy_dtype).cuda(), torch.randn(s, N, generator=g).bfloat16().cuda()
+    z = z if act != "none" else None
+    dx, dW, db = B.moe_linear_bwd(dy, x, W, z, act, dx_dtype=torch.float32, dw_dtype=torch.float32)
+    ox, ow, _, dz = O.linear_bwd(f64(dy), f64(x), f64(W), None if z is None else f64(z), act)
+    slip = 0 if act == "none" else np.abs(f64(dy)) * 32 * U
+    for got, want, k, by, order in ((dx, ox, N, np.abs(f64(W)), lambda m: m), (dW, ow, s, np.abs(f64(x)), lambda m: m.T)):
+        tol = ((k / 16 + 48) * 2.0 ** -23 + 2.0 ** -16) * (order(np.abs(dz)) @ by)
+        tol = tol + (0 if act == "none" else order(slip) @ by) + U * np.abs(want) + 1e-38
+        assert (np.abs(f64(got) - want) <= tol).all()
+        if want.size > 1000:
+            assert np.linalg.norm(f64(got) - want) <= 2.0 ** -15 * np.linalg.norm(want)
+    # one fp32 result beside a bf16 one, and the bf16 one as without it
+    a = B.moe_linear_bwd(dy, x, W, z, act, dx_dtype=torch.float32)
+    c = B.moe_linear_bwd(dy, x, W, z, act, dw_dtype=torch.float32)
+    e = B.moe_linear_bwd(dy, x, W, z, act)
+    assert torch.equal(a[0], dx) and torch.equal(c[1], dW) and torch.equal(a[1], e[1]) and torch.equal(c[0], e[0])
+    assert torch.equal(db, e[2])
+
+
+def test_fp32_gradients_of_infinite_rows():
+    # an infinity stays what it is in the first term, and the second holds nothing for it
+    x, W, dy = torch.randn(200, 64).bfloat16().cuda(), torch.randn(40, 64).bfloat16().cuda(), torch.randn(200, 40).cuda()
+    dy[150, 3] = float("inf")
+    dy[20, 5] = float("nan")
+    W[3], x[150] = 1.0, 1.0
+    dx, dW, _ = B.moe_linear_bwd(dy, x, W, dx_dtype=torch.float32, dw_dtype=torch.float32)
+    assert (dx[150] == float("inf")).all() and dx[20].isnan().all() and (dW[3] == float("inf")).all() and dW[5].isnan().all()
+    rows = [i for i in range(200) if i not in (20, 150)]
+    cols = [i for i in range(40) if i not in (3, 5)]
+    assert torch.isfinite(dx[rows]).all() and torch.isfinite(dW[cols]).all()
