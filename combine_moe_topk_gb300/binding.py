@@ -200,8 +200,13 @@ def _raw_stream(t: torch.Tensor):
 
 
 # torch's own short way to an uninitialised CUDA tensor on the current device;
-# beside a launch torch.empty takes 3.9 us of host time, this 1.4.
+# beside a launch torch.empty takes 3.9 us of host time, this 1.4.  It goes past
+# the dispatcher, so while a dispatch mode (a memory tracker, say) is active,
+# or where either name is missing, torch.empty it is.
 _strided = getattr(getattr(torch._C, "_dynamo", None) and torch._C._dynamo.guards, "_empty_strided_cuda", None)
+_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+if _modes is None:
+    _strided = None
 
 
 def _new_here(dtype: torch.dtype, n: int, m: int | None = None) -> torch.Tensor:
@@ -210,7 +215,7 @@ def _new_here(dtype: torch.dtype, n: int, m: int | None = None) -> torch.Tensor:
 
 def _new(t: torch.Tensor):
     """How outputs beside t are allocated: new(dtype, n) or new(dtype, n, m), contiguous."""
-    if _strided is not None and t.is_cuda and t.get_device() == torch._C._cuda_getDevice():
+    if _strided is not None and t.is_cuda and not _modes() and t.get_device() == torch._C._cuda_getDevice():
         return _new_here
     dev = t.device
     return lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
