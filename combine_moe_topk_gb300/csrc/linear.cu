@@ -623,9 +623,8 @@ __device__ __forceinline__ int rows_of_share(int m0, int M, int S) { return (min
 // join had taken 7 of 23 thousand cycles).  Ends with this CTA's arrival at the
 // barrier after which the parts may go.
 template <int S, int BN>
-__device__ __forceinline__ void join_parts(const GemmArgs& p, const Unit& t, int split, const uint8_t* parts) {
+__device__ __forceinline__ void join_parts(const GemmArgs& p, const Epi& e, const Unit& t, int split, const uint8_t* parts) {
   constexpr int kGroups = BN / 4, kRounds = (128 / S * kGroups + kThreads - 1) / kThreads;
-  const Epi& e = p.epi;
   const int per = rows_of_share(t.m0, p.M, S), end = min(min(128, p.M - t.m0), (split + 1) * per);
   float bias[kRounds][4], res[kRounds][4], f[kRounds][4];
   bool there[kRounds];
@@ -756,6 +755,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (CG == 2) cluster_sync_all();  // both CTAs' barriers exist before any remote signal
   tc_fence_after();
   const uint32_t tbase = tmem_base;
+
+  // a gradient's product (BT) has nothing in its epilogue but the store
+  Epi plain = {};
+  if constexpr (BT) {
+    plain.out = p.epi.out;
+    plain.act = MOE_ACT_NONE;
+    plain.out_f32 = p.epi.out_f32;
+    plain.narrow = p.epi.narrow;
+    plain.wide = p.epi.wide;
+  }
+  const Epi& epi = BT ? plain : p.epi;
 
   const int units = p.tiles_m * p.tiles_n;
   const int share = kSplit ? p.splits : CG;  // CTAs of a worker
@@ -889,13 +899,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew, n0 = t.n0 + half * (BN / 2);
       if constexpr (kSplit) {  // for the rows that this CTA will finish
         const int rows = rows_of_share(t.m0, p.M, p.splits), i = threadIdx.x - 128;
-        if (i < rows) prefetch_residual(p.epi, t.m0 + split * rows + i, t.n0, BN, p.M, p.N);
+        if (i < rows) prefetch_residual(epi, t.m0 + split * rows + i, t.n0, BN, p.M, p.N);
       } else {
-        prefetch_residual(p.epi, r0 + lane, n0, BN / 2, p.M, p.N);
+        prefetch_residual(epi, r0 + lane, n0, BN / 2, p.M, p.N);
       }
       Ahead ahead;
       auto start = [&]() {
-        if (!kSplit && !p.epi.wide) start_ragged(p.epi, ahead, r0, n0, p.M, p.N, lane);
+        if (!kSplit && !epi.wide) start_ragged(epi, ahead, r0, n0, p.M, p.N, lane);
       };
       // a block of 32 columns on its way out, or into this CTA's part of a split tile
       auto emit = [&](const uint32_t (&v)[32], const Raw32& res, int c) {
@@ -904,14 +914,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             reinterpret_cast<uint4*>(row)[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else if (p.epi.wide) {
-          finish_bulk<BN >= 128>(p.epi, bulk, &tmY, &tmZ, v, res, c, r0, n0 + 32 * c, p.M, p.N, lane);
+        } else if (epi.wide) {
+          finish_bulk<BN >= 128>(epi, bulk, &tmY, &tmZ, v, res, c, r0, n0 + 32 * c, p.M, p.N, lane);
         } else {
-          finish_ragged(p.epi, stage_buf, v, ahead, c, kChunks, r0, n0, p.M, p.N, lane);
+          finish_ragged(epi, stage_buf, v, ahead, c, kChunks, r0, n0, p.M, p.N, lane);
         }
       };
       auto residual = [&](Raw32& res, int c) {
-        if (!kSplit && p.epi.wide) load_residual(p.epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
+        if (!kSplit && epi.wide) load_residual(epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
       };
       auto lanes_of = [&]() { return tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2)); };
       if constexpr (kExact) {
@@ -980,9 +990,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (kSplit) {
     const Unit t = unit_of<CG, BN>(worker, split, p);
     switch (p.splits) {
-      case 2: join_parts<2, BN>(p, t, split, smem); break;
-      case 4: join_parts<4, BN>(p, t, split, smem); break;
-      default: join_parts<8, BN>(p, t, split, smem); break;
+      case 2: join_parts<2, BN>(p, epi, t, split, smem); break;
+      case 4: join_parts<4, BN>(p, epi, t, split, smem); break;
+      default: join_parts<8, BN>(p, epi, t, split, smem); break;
     }
     cluster_wait();  // nobody reads this CTA's part any more
   }
