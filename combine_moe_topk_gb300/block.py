@@ -48,7 +48,8 @@ class MoEBlock(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, valid: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
                 topk_idx: torch.Tensor | None = None):
-        """valid, seq_offsets: see ``balance_loss``; topk_idx: routes to take instead of the gate's own choice
+        """valid, seq_offsets: see ``balance_loss`` (padding is left out of the losses; it is routed, and takes up
+        capacity, like any other token); topk_idx: routes to take instead of the gate's own choice
         (replay), their gates still the softmax over the chosen logits."""
         h = A.layernorm(x, self.norm_w, self.norm_b)
         logits = A.linear(h, self.router, out_dtype=torch.float32)

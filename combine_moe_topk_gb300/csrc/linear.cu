@@ -23,7 +23,7 @@
 //   warps 4..11     epilogue, two warps for each quarter of the TMEM lanes,
 //                   from one of two accumulators while the other fills
 // Bound by the tensor cores where both sides are long (8192 x 4096 x 16384 558 us,
-// 1.97 PFLOP/s; 8192 x 4096 x 4096 146, backward dx 146, dW 164 us), by what an SM
+// 1.97 PFLOP/s; 8192 x 4096 x 4096 147, backward dx 148, dW 165 us), by what an SM
 // takes in where one is short (16384 x 4096 x 128 28.5 us), by the weights' bytes
 // and the launch where rows are few (64 x 4096 x 4096 11.9 us).
 // Every mbarrier wait is bounded on the global timer, each from its own start, so
@@ -336,7 +336,8 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // a quarter of the instructions: dx of 16384 x 4096 from 128 columns, a product
 // that is little but its output, 75.7 -> 47 us (44 without the stores, 28
 // without the epilogue: what is left is the tile's hand-over between load,
-// product and epilogue).  Rows of 128 bytes instead of 64 matter to the large
+// product and epilogue; 38.9 since a gradient's product is compiled without the
+// rest of the epilogue).  Rows of 128 bytes instead of 64 matter to the large
 // products (8192 x 4096 x 16384: 566 -> 545 us).
 struct Bulk {
   uint8_t* stage;  // this warp's 4 KB

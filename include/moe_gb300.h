@@ -463,8 +463,8 @@ moe_status moe_layernorm(int s, int m, moe_dtype dtype, const void* x, int64_t l
                          const void* weight, const void* bias, float eps, void* y, float* mean, float* rstd,
                          void* stream);
 
-/* Bytes of moe_layernorm_bwd's workspace (0 when neither dweight nor dbias is
- * wanted, or s = 0). */
+/* Bytes of moe_layernorm_bwd's workspace, needed when dweight or dbias is
+ * wanted (0 for s = 0); a call that wants neither takes NULL and 0 bytes. */
 size_t moe_layernorm_bwd_workspace(int s, int m);
 
 /* Layer norm backward, from the forward pass's mean and rstd.  With
@@ -545,9 +545,11 @@ typedef struct {
  * bytes; any s >= 0 and N >= 1); bias [N] and residual [s,N] nullable, fp32 or
  * bf16; y [s,N] fp32 or bf16.  z bf16 [s,N] (nullable): what the backward pass
  * of an activation needs, rounded to bf16 to halve what is kept.  Products of
- * bf16 are exact, sums fp32 on the tensor cores (tcgen05), the epilogue fp32;
- * y and z are each rounded once.  device_status (nullable): MOE_DEV_TIMEOUT if
- * a bounded device wait ran out.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
+ * bf16 are exact, sums fp32 on the tensor cores (tcgen05; their accumulator drops
+ * the bits below its last place, so an fp32 y takes the sum in parts of at most
+ * 512 terms, and so does a bf16 y of more than 2^18), the epilogue fp32; y and z
+ * are each rounded once.  device_status (nullable): MOE_DEV_TIMEOUT if a device
+ * wait, each limited to two seconds and some, ran out; y is incomplete then.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
  * MOE_ERR_CUDA. */
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* W, const void* bias,
                       const void* residual, void* y, void* z, int32_t* device_status, void* stream);

@@ -14,9 +14,9 @@ def f64(t):
 
 
 def test_a_product_longer_than_the_limit_of_a_wait():
-    """2 * 122880^3 operations take more than two seconds, the limit of one device wait.  Rows repeat every 256, so
+    """2 * 131072^3 operations take more than two seconds, the limit of one device wait.  Rows repeat every 256, so
     256 x 256 values of the definition tell all of them."""
-    n, r = 122880, 256
+    n, r = 131072, 256
     g = torch.Generator(device="cuda").manual_seed(0)
     few = [(torch.randn(r, n, generator=g, device="cuda") / n ** 0.25).bfloat16() for _ in range(2)]
     x, W = (t.repeat(n // r, 1) for t in few)
