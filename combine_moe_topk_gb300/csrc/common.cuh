@@ -261,19 +261,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Bounded wait on an mbarrier phase.  Returns false if `deadline_ns` (on
-// the global timer) passes first; the caller then records MOE_DEV_TIMEOUT.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
-                                                  uint64_t deadline_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63) == 63 && globaltimer_ns() > deadline_ns) return false;
-  }
-}
-
-// The same with the limit counted from this wait's own start (the timer is
-// read only where a wait lasts).
+// Bounded wait on an mbarrier phase.  Returns false if limit_ns pass from the
+// wait's own start; the caller then records MOE_DEV_TIMEOUT.  (The timer is
+// read only where a wait lasts.)
 __device__ __forceinline__ bool mbar_wait_limited(uint64_t* bar, uint32_t parity, long long limit_ns) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t deadline = 0;

@@ -33,8 +33,8 @@
 // waste the tail of a 256-row block, but a 128-row block wastes the same
 // tail rows, and where segments are short -- many experts, few rows each --
 // streaming each expert's weights once bounds the GEMM anyway.)
-// Every mbarrier wait is bounded on the global timer; a time-out records
-// MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
+// Every mbarrier wait is bounded on the global timer, each from its own start;
+// a time-out records MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -71,7 +71,7 @@ struct GemmParams {
   int s;                   // gather mode: token rows of x
   __nv_bfloat16* Y;
   int32_t* status;
-  long long timeout_ns;
+  long long timeout_ns;  // of a single wait
 };
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle (as TMA writes
@@ -238,7 +238,6 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
   // identical static layout in both CTAs: the dynamic buffer starts at the
   // same offset, so the MMA's descriptors address the same tiles in both
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  const uint64_t deadline = globaltimer_ns() + (uint64_t)p.timeout_ns;
 
   for (int x = threadIdx.x; x <= p.e; x += blockDim.x) s_off[x] = __ldg(p.offsets + x);
   for (int x = threadIdx.x; x < p.e; x += blockDim.x) s_cnt[x] = __ldg(p.counts + x);
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       const int b = u / ntn;
       const int r0 = s_off[t.x] + BM2 * (b - s_blk[t.x]) + BM * (int)rank;
       for (int kb = 0; kb < kblocks; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) {
+        if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     // drain: every stage's last fill consumed, so no commit of rank 0 is
     // still on its way to this CTA's barriers when it leaves
     for (int i = 0; i < kPairStages && ok; ++i) {
-      if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline)) ok = false;
+      if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) ok = false;
       if (++stage == kPairStages) {
         stage = 0;
         phase ^= 1u;
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       for (int j = 0; j < kGatherRows / 4; ++j) src[j] = p.x + (size_t)(tok[j] < 0 ? 0 : tok[j]) * p.K + chunk * 8;
       for (int kb = 0; kb < kblocks; ++kb) {
         bool waited = true;
-        if (lane == 0) waited = mbar_wait_bounded(&empty[stage], phase ^ 1u, deadline);
+        if (lane == 0) waited = mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns);
         if (!__shfl_sync(0xffffffffu, waited ? 1 : 0, 0)) {
           ok = false;
           break;
@@ -419,7 +418,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
       for (int kb = 0; kb < kblocks; ++kb) {
-        if (!mbar_wait_bounded(&gathered[stage], phase, deadline)) {
+        if (!mbar_wait_limited(&gathered[stage], phase, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     uint32_t phase = 0, tphase[2] = {0u, 0u};
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
-      if (!mbar_wait_cluster(&tempty[acc], tphase[acc] ^ 1u, deadline)) {
+      if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
         ok = false;
         break;
       }
@@ -447,7 +446,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       tc_fence_after();
       const uint32_t dt = tbase + (uint32_t)(acc * BN);
       for (int kb = 0; kb < kblocks; ++kb) {
-        if (!mbar_wait_cluster(&full[stage], phase, deadline)) {
+        if (!mbar_wait_cluster_limited(&full[stage], phase, p.timeout_ns)) {
           ok = false;
           break;
         }
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       // CTAs' shared memory -- one more commit, to this CTA only, arrives
       // after all of them and after the commits before it (bounded wait)
       mma_commit_pair(&mma_drain, 0x1);
-      mbar_wait_bounded(&mma_drain, 0, globaltimer_ns() + (uint64_t)p.timeout_ns);
+      mbar_wait_limited(&mma_drain, 0, p.timeout_ns);
       atomicOr(&s_err, 1);
     }
   } else if (warp >= 4 && warp < 8) {
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       const int left = s_cnt[t.x] - BM2 * i - BM * (int)rank;
       const int nvalid = left < 0 ? 0 : (left < BM ? left : BM);
       // every lane waits (and acquires) itself; the warp leaves together
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&tfull[acc], tphase[acc], deadline))) {
+      if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
         ok = false;
         break;
       }
@@ -581,7 +580,8 @@ GemmParams params(const int32_t* offsets, const int32_t* counts, int e, int rows
   p.s = 0;
   p.Y = static_cast<__nv_bfloat16*>(Y);
   p.status = status;
-  p.timeout_ns = 2000000000LL;
+  // the longest wait is the epilogue's, for a whole contraction: under 1 us for 128 of K when all is well
+  p.timeout_ns = kWaitNs + 20000LL * (K / 128);
   return p;
 }
 

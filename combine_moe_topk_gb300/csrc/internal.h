@@ -158,6 +158,8 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
                                  int e, int rows, int s, int K, int N, const void* x, const void* W,
                                  void* Y, int32_t* status, const DeviceInfo& di, cudaStream_t st);
 
+constexpr long long kWaitNs = 2000000000LL;  // the limit of one device wait in the products
+
 // --- layer norm ------------------------------------------------------------
 // dtype / w_dtype: 0 = f32, 1 = bf16.  w, b, mean, rstd may be NULL.  ld*:
 // elements between rows of the inputs (outputs are contiguous).

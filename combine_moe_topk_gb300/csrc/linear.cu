@@ -702,7 +702,7 @@ constexpr int kLongSum = 1 << 18;
 // below the first, so the contracted axis is gone through twice.  Tiles that
 // reach past the first term's end read into the second: rows of D that are not
 // stored, or terms that meet B's zeros.  (As a second product with the first
-// one's result for its residual: 16384 x 4096 x 128, dx and dW, 309 us; this way 125.)
+// one's result for its residual: 16384 x 4096 x 128, dx and dW, 309 us; this way 114.)
 template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -1314,7 +1314,6 @@ constexpr int kKinds = 3;
 constexpr int kKindCG[kKinds] = {2, 1, 1};
 constexpr int kKindBN[kKinds] = {256, 128, 64};
 constexpr int kPlanSms = 152;  // plans are made for a whole GB300
-constexpr long long kWaitNs = 2000000000LL;  // the limit of a device wait
 
 // The shape and split of least estimated time, in units of a K block of the
 // widest tile (0.65 us).  Measured: a K block of a 128 x 128 tile takes 0.70 of

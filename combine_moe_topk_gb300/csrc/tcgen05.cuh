@@ -99,15 +99,8 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
   return ok != 0;
 }
 
-// Bounded waits with cluster-scope acquire, for barriers that receive
-// arrivals from the other CTA of the pair: until a point in time, or for
-// limit_ns from the wait's own start.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 63) == 63 && globaltimer_ns() > deadline_ns) return false;
-  }
-}
+// The same bounded wait with cluster-scope acquire, for barriers that receive
+// arrivals from the other CTA of the pair.
 __device__ __forceinline__ bool mbar_wait_cluster_limited(uint64_t* bar, uint32_t parity, long long limit_ns) {
   uint64_t deadline = 0;
   for (uint32_t it = 0;; ++it) {
