@@ -46,7 +46,7 @@ def _status(t: torch.Tensor) -> torch.Tensor | None:
             return None  # it would belong to the graph; a run before the capture makes it
         word = torch.zeros(1, dtype=torch.int32, device=t.device)
         torch.cuda.current_stream(t.device).synchronize()  # it is written from any stream
-        _words[t.get_device()] = word
+        word = _words.setdefault(t.get_device(), word)  # another thread may have been first
     return word
 
 
