@@ -29,7 +29,8 @@ MOE_DEV_NONFINITE, MOE_DEV_BAD_ROUTE, MOE_DEV_TIMEOUT, MOE_DEV_ROWS_EXCEEDED = 0
 KERNELS = ["topk_gate", "layout", "dispatch", "combine", "combine_bwd", "dispatch_bwd", "topk_gate_bwd",
            "grouped_gemm", "dispatch_gemm", "rank_slots", "combine_gate_bwd", "gate_layout", "ep_pack", "ep_unpack",
            "ep_dispatch", "ep_combine", "layernorm", "layernorm_bwd", "balance", "balance_bwd", "linear",
-           "linear_bwd"]
+           "linear_bwd", "gated", "gated_bwd", "grouped_gated", "grouped_gated_bwd", "grouped_gemm_bwd", "grad_norm",
+           "grad_clip"]
 KERNEL_ID = {n: i for i, n in enumerate(KERNELS)}
 
 # every entry point the header declares (checked by the CPU test-suite)
@@ -42,7 +43,10 @@ EXPORTS = [
     "moe_topk_gate_layout", "moe_ep_pack", "moe_ep_dispatch", "moe_ep_combine", "moe_ep_unpack_dgate",
     "moe_layernorm", "moe_layernorm_bwd", "moe_layernorm_bwd_workspace", "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_balance_loss_workspace", "moe_linear", "moe_linear_bwd", "moe_linear_bwd_workspace",
-    "moe_linear_bwd_workspace_for",
+    "moe_linear_bwd_workspace_for", "moe_gated_linear", "moe_gated_linear_bwd", "moe_gated_linear_bwd_workspace",
+    "moe_grouped_gated", "moe_dispatch_grouped_gated", "moe_grouped_gated_bwd", "moe_grouped_gated_bwd_workspace",
+    "moe_grouped_gemm_bwd", "moe_tensor_list_create", "moe_tensor_list_destroy", "moe_grad_norm_workspace",
+    "moe_grad_norm", "moe_grad_clip", "moe_clip_grad_norm",
 ]
 
 
@@ -78,6 +82,20 @@ class LinearDesc(ctypes.Structure):
 class LinearBwdDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("s", "K", "N", "act", "dy_dtype", "dx_dtype", "dw_dtype")] + [
         (n, ctypes.c_int64) for n in ("lddy", "ldx", "ldw", "ldz")]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("s", "K", "N", "act", "bias_dtype")] + [
+        (n, ctypes.c_int64) for n in ("ldx", "ldw")]
+
+
+class GatedBwdDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("s", "K", "N", "act", "dh_dtype", "dx_dtype", "dw_dtype")] + [
+        (n, ctypes.c_int64) for n in ("lddh", "ldx", "ldw", "ldz")]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -125,17 +143,33 @@ def lib() -> ctypes.CDLL:
             "moe_balance_loss_bwd": [P] * 8 + [I, I, I, P, P],
             "moe_linear": [ctypes.POINTER(LinearDesc)] + [P] * 8,
             "moe_linear_bwd": [ctypes.POINTER(LinearBwdDesc)] + [P] * 8 + [Z, P, P],
+            "moe_gated_linear": [ctypes.POINTER(GatedDesc)] + [P] * 7,
+            "moe_gated_linear_bwd": [ctypes.POINTER(GatedBwdDesc)] + [P] * 8 + [Z, P, P],
+            "moe_grouped_gated": [P, I, I, I, I] + [P] * 5,
+            "moe_dispatch_grouped_gated": [P, I, I, I, I, I] + [P] * 5,
+            "moe_grouped_gated_bwd": [P, I, I, I, I] + [P] * 7 + [Z, P],
+            "moe_grouped_gemm_bwd": [P, I, I, I] + [P] * 6,
+            "moe_tensor_list_create": [ctypes.POINTER(Tensor), I, ctypes.POINTER(P)],
+            "moe_tensor_list_destroy": [P],
+            "moe_grad_norm": [P, P, P, Z, P, P],
+            "moe_grad_clip": [P, P, P, F, P],
+            "moe_clip_grad_norm": [P, P, F, P, P, Z, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = I
-        for name in ("moe_layernorm_bwd_workspace", "moe_balance_loss_workspace", "moe_linear_bwd_workspace"):
+        for name in ("moe_layernorm_bwd_workspace", "moe_balance_loss_workspace", "moe_linear_bwd_workspace",
+                     "moe_grouped_gated_bwd_workspace"):
             f = getattr(L, name)
             f.argtypes = [I, I]
             f.restype = Z
         L.moe_linear_bwd_workspace_for.argtypes = [ctypes.POINTER(LinearBwdDesc), I, I, I]
         L.moe_linear_bwd_workspace_for.restype = Z
+        L.moe_gated_linear_bwd_workspace.argtypes = [ctypes.POINTER(GatedBwdDesc), I, I, I]
+        L.moe_gated_linear_bwd_workspace.restype = Z
+        L.moe_grad_norm_workspace.argtypes = [I]
+        L.moe_grad_norm_workspace.restype = Z
         L.moe_capacity.argtypes = [ctypes.c_double, I, I, I]
         L.moe_capacity.restype = I
         L.moe_status_string.argtypes = [I]
@@ -851,3 +885,291 @@ def moe_linear_bwd(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.
     if rc:
         _check(rc, "moe_linear_bwd")
     return dx, dW, db
+
+
+# ------------------------- gated experts: products, gradients, clipping --
+
+def _check_gated(where: str, x: torch.Tensor, W: torch.Tensor, act: str):
+    s, K = _rows2(x, "x")
+    N2, KW = _rows2(W, "W")
+    if KW != K or N2 % 2:
+        raise MoEError(1, where, "W must be [2N, K], the gate's rows first")
+    if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise MoEError(3, where, "x and W must be bf16")
+    if act not in ACT:
+        raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
+    return s, K, N2 // 2
+
+
+def moe_gated_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "silu",
+                     save_z: bool = False, h: torch.Tensor | None = None, device_status: torch.Tensor | None = None):
+    """h bf16 [s,N] = act(x Wg^T + bg) * (x Wu^T + bu): x bf16 [s,K], W bf16
+    [2N,K] = [Wg; Wu] (rows may be strided; K and N multiples of 8), bias [2N]
+    f32 or bf16.  save_z: return (h, z), z bf16 [s,2N] both projections, for
+    moe_gated_linear_bwd."""
+    s, K, N = _check_gated("moe_gated_linear", x, W, act)
+    new = _new(x)
+    if bias is not None and bias.shape != (2 * N,):
+        raise MoEError(1, "moe_gated_linear", "bias must be [2N]")
+    if h is None:
+        h = new(torch.bfloat16, s, N)
+    elif h.shape != (s, N) or h.dtype != torch.bfloat16:
+        raise MoEError(1, "moe_gated_linear", "h must be bf16 [s, N]")
+    z = new(torch.bfloat16, s, 2 * N) if save_z else None
+    px, ldx = _rows_ptr(x)
+    pw, ldw = _rows_ptr(W)
+    d = GatedDesc(s, K, N, ACT[act], 0 if bias is None else _DTYPE.get(bias.dtype, -1), ldx, ldw)
+    rc = lib().moe_gated_linear(d, px, pw, _addr(bias), _addr(h), _addr(z),
+                                _status_addr(device_status, "moe_gated_linear"), _raw_stream(x))
+    if rc:
+        _check(rc, "moe_gated_linear")
+    return (h, z) if save_z else h
+
+
+def moe_gated_linear_bwd(dh: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: torch.Tensor, act: str = "silu",
+                         need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                         dx_dtype: torch.dtype = torch.bfloat16, dw_dtype: torch.dtype = torch.bfloat16,
+                         device_status: torch.Tensor | None = None):
+    """(dh [s,N] f32 or bf16, x bf16 [s,K], W bf16 [2N,K], z bf16 [s,2N]) ->
+    (dx [s,K], dW [2N,K], db f32 [2N]), None for those not needed."""
+    s, K, N = _check_gated("moe_gated_linear_bwd", x, W, act)
+    new = _new(x)
+    if dh.shape != (s, N):
+        raise MoEError(1, "moe_gated_linear_bwd", "dh must be [s, N]")
+    if z.shape != (s, 2 * N) or z.dtype != torch.bfloat16:
+        raise MoEError(1, "moe_gated_linear_bwd", "z must be bf16 [s, 2N]")
+    dx = new(dx_dtype, s, K) if need_dx else None
+    dW = new(dw_dtype, 2 * N, K) if need_dw else None
+    db = new(torch.float32, 2 * N) if need_db else None
+    L = lib()
+    pdh, lddh = _rows_ptr(dh)
+    px, ldx = _rows_ptr(x)
+    pw, ldw = _rows_ptr(W)
+    pz, ldz = _rows_ptr(z)
+    d = GatedBwdDesc(s, K, N, ACT[act], _DTYPE.get(dh.dtype, -1), _DTYPE.get(dx_dtype, -1), _DTYPE.get(dw_dtype, -1),
+                     lddh, ldx, ldw, ldz)
+    nbytes = L.moe_gated_linear_bwd_workspace(d, need_dx, need_dw, need_db)
+    ws = new(torch.uint8, nbytes) if nbytes else None
+    rc = L.moe_gated_linear_bwd(d, pdh, px, pw, pz, _addr(dx), _addr(dW), _addr(db), _addr(ws), nbytes,
+                                _status_addr(device_status, "moe_gated_linear_bwd"), _raw_stream(x))
+    if rc:
+        _check(rc, "moe_gated_linear_bwd")
+    return dx, dW, db
+
+
+def _check_experts(where: str, h: Handle, x: torch.Tensor, W: torch.Tensor, gated: bool, act: str = "none"):
+    """(rows of x, K, N) of an expert product's operands."""
+    s, K = _rows2(x, "x")
+    if W.dim() != 3 or W.shape[0] != h.e or W.shape[2] != K or (gated and W.shape[1] % 2):
+        raise MoEError(1, where, "W must be [e, 2N, K], the gate's rows first" if gated else "W must be [e, N, K]")
+    if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+        raise MoEError(3, where, "x and W must be bf16")
+    if act not in ACT:
+        raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
+    return s, K, W.shape[1] // 2 if gated else W.shape[1]
+
+
+def _bf16(where: str, t: torch.Tensor | None, name: str, *shape):
+    if t is not None and (t.shape != shape or t.dtype != torch.bfloat16):
+        raise MoEError(1, where, f"{name} must be bf16 {list(shape)}")
+
+
+def _gated_rows(where: str, call, h: Handle, x, W, act, H, Z, save_z, gather: bool):
+    s, K, N = _check_experts(where, h, x, W, True, act)
+    new, rows = _new(x), h.rows
+    if s != (h.s if gather else rows):
+        raise MoEError(4, where, "x has another number of rows than the handle's")
+    _bf16(where, H, "H", rows, N)
+    _bf16(where, Z, "Z", rows, 2 * N)
+    if H is None:
+        H = new(torch.bfloat16, rows, N)
+    if not save_z:
+        Z = None
+    elif Z is None:
+        Z = new(torch.bfloat16, rows, 2 * N)
+    sizes = (s, rows, K, N) if gather else (rows, K, N)
+    rc = call(h.raw, *sizes, ACT[act], _addr(x), _addr(W), _addr(H), _addr(Z), _raw_stream(x))
+    if rc:
+        _check(rc, where)
+    return (H, Z) if save_z else H
+
+
+def moe_grouped_gated(h: Handle, X: torch.Tensor, W: torch.Tensor, act: str = "silu", save_z: bool = False,
+                      H: torch.Tensor | None = None, Z: torch.Tensor | None = None):
+    """X bf16 [rows,K], W bf16 [e,2N,K] (each expert's gate rows first) -> H
+    bf16 [rows,N] = act(X Wg[x]^T) * (X Wu[x]^T) per expert segment; save_z:
+    (H, Z), Z bf16 [rows,2N] for moe_grouped_gated_bwd.  Rows no route owns
+    are not written."""
+    return _gated_rows("moe_grouped_gated", lib().moe_grouped_gated, h, X, W, act, H, Z, save_z, False)
+
+
+def moe_dispatch_grouped_gated(h: Handle, x: torch.Tensor, W: torch.Tensor, act: str = "silu", save_z: bool = False,
+                               H: torch.Tensor | None = None, Z: torch.Tensor | None = None):
+    """The same on the token rows x bf16 [s,K] gathered through the handle, without a dispatched buffer."""
+    return _gated_rows("moe_dispatch_grouped_gated", lib().moe_dispatch_grouped_gated, h, x, W, act, H, Z, save_z, True)
+
+
+def _grouped_bwd_args(where: str, h: Handle, D, X, W, need_dx, need_dw, dX, dW, gated: bool, act: str = "none"):
+    rows, K, N = _check_experts(where, h, X, W, gated, act)
+    _bf16(where, D, "the result's gradient", rows, N)
+    _bf16(where, dX, "dX", rows, K)
+    _bf16(where, dW, "dW", *W.shape)
+    new = _new(X)
+    if dX is None and need_dx:
+        dX = new(torch.bfloat16, rows, K)
+    if dW is None and need_dw:
+        dW = new(torch.bfloat16, W.shape[0] * W.shape[1], K).view(W.shape)
+    return rows, K, N, dX if need_dx else None, dW if need_dw else None
+
+
+def moe_grouped_gemm_bwd(h: Handle, dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, need_dx: bool = True,
+                         need_dw: bool = True, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None):
+    """Backward of moe_grouped_gemm: (dY bf16 [rows,N], X bf16 [rows,K], W bf16
+    [e,N,K]) -> (dX [rows,K], dW [e,N,K]), None for those not needed.  Rows of
+    dX that no route owns are not written."""
+    rows, K, N, dX, dW = _grouped_bwd_args("moe_grouped_gemm_bwd", h, dY, X, W, need_dx, need_dw, dX, dW, False)
+    rc = lib().moe_grouped_gemm_bwd(h.raw, rows, K, N, _addr(dY), _addr(X), _addr(W), _addr(dX), _addr(dW), _raw_stream(X))
+    if rc:
+        _check(rc, "moe_grouped_gemm_bwd")
+    return dX, dW
+
+
+def moe_grouped_gated_bwd(h: Handle, dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor, Z: torch.Tensor,
+                          act: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                          dX: torch.Tensor | None = None, dW: torch.Tensor | None = None):
+    """Backward of moe_grouped_gated (X = moe_dispatch's output also for the
+    gathering form): (dH bf16 [rows,N], X bf16 [rows,K], W bf16 [e,2N,K], Z bf16
+    [rows,2N]) -> (dX [rows,K], dW [e,2N,K]), None for those not needed."""
+    where = "moe_grouped_gated_bwd"
+    rows, K, N, dX, dW = _grouped_bwd_args(where, h, dH, X, W, need_dx, need_dw, dX, dW, True, act)
+    _bf16(where, Z, "Z", rows, 2 * N)
+    L = lib()
+    nbytes = L.moe_grouped_gated_bwd_workspace(rows, N) if need_dx or need_dw else 0
+    ws = _new(X)(torch.uint8, nbytes) if nbytes else None
+    rc = L.moe_grouped_gated_bwd(h.raw, rows, K, N, ACT[act], _addr(dH), _addr(X), _addr(W), _addr(Z), _addr(dX), _addr(dW),
+                                 _addr(ws), nbytes, _raw_stream(X))
+    if rc:
+        _check(rc, where)
+    return dX, dW
+
+
+class GradList:
+    """Tensors whose norm is taken and which are clipped together, checked once:
+    f32 or bf16 on one device, each without gaps or overlaps in memory (any
+    order of its axes).  It keeps the tensors alive; a program whose gradients
+    stay in place makes it once."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+        self.device = None
+        spec = (Tensor * max(1, len(tensors)))()
+        for i, t in enumerate(tensors):
+            if t.layout != torch.strided or not _dense(t):
+                raise ValueError(f"tensor {i}: gradients must be dense tensors without gaps or overlaps in memory")
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise MoEError(1, "GradList", "the tensors are on different devices")
+            spec[i].data, spec[i].numel, spec[i].dtype = t.data_ptr(), t.numel(), _DTYPE.get(t.dtype, -1)
+        self._raw = raw = ctypes.c_void_p()
+        if self.device is not None and self.device.type == "cuda":
+            with torch.cuda.device(self.device):
+                rc = lib().moe_tensor_list_create(spec, len(tensors), ctypes.byref(raw))
+        else:  # no tensors, or host tensors, which the library rejects
+            rc = lib().moe_tensor_list_create(spec, len(tensors), ctypes.byref(raw))
+        if rc:
+            _check(rc, "moe_tensor_list_create")
+        if self.device is None:
+            self.device = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+
+    def __len__(self):
+        return len(self.tensors)
+
+    @property
+    def raw(self):
+        return self._raw
+
+    def __del__(self):
+        raw = getattr(self, "_raw", None)
+        if raw and _lib is not None:
+            _lib.moe_tensor_list_destroy(raw)
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """The elements fill a stretch of memory, in some order of the axes."""
+    if t.is_contiguous():
+        return True
+    expect = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != expect:
+            return False
+        expect *= size
+    return True
+
+
+def _grads(grads) -> GradList:
+    return grads if isinstance(grads, GradList) else GradList(grads)
+
+
+def _clip_lists(where: str, grads, out):
+    g = _grads(grads)
+    o = None if out is None else _grads(out)
+    if o is not None:
+        for a, b in zip(g.tensors, o.tensors):
+            if a.shape != b.shape or a.stride() != b.stride():
+                raise MoEError(1, where, "out must have the gradients' shapes and strides")
+    return g, o
+
+
+def _on(device: torch.device):
+    return torch.cuda.device(device)
+
+
+def moe_grad_norm(grads, norm: torch.Tensor | None = None, device_status: torch.Tensor | None = None) -> torch.Tensor:
+    """f32 [1]: the 2-norm of all elements of all tensors (a sequence or a
+    GradList).  A NaN or an infinity reaches it (and device_status)."""
+    g = _grads(grads)
+    L = lib()
+    with _on(g.device):
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=g.device)
+        elif norm.shape != (1,) or norm.dtype != torch.float32:
+            raise MoEError(1, "moe_grad_norm", "norm must be float32 [1]")
+        nbytes = L.moe_grad_norm_workspace(len(g))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        rc = L.moe_grad_norm(g.raw, _addr(norm), _addr(ws), nbytes, _status_addr(device_status, "moe_grad_norm"),
+                             _raw_stream(norm))
+    if rc:
+        _check(rc, "moe_grad_norm")
+    return norm
+
+
+def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
+    """Scale the gradients by min(1, max_norm / (norm + 1e-6)) in place, or into the tensors of `out`; norm f32 [1] on
+    the device (joined over ranks, say).  A norm that is not finite leaves them unscaled."""
+    g, o = _clip_lists("moe_grad_clip", grads, out)
+    if norm.shape != (1,) or norm.dtype != torch.float32:
+        raise MoEError(1, "moe_grad_clip", "norm must be float32 [1]")
+    with _on(g.device):
+        rc = lib().moe_grad_clip(g.raw, None if o is None else o.raw, _addr(norm), max_norm, _raw_stream(norm))
+    if rc:
+        _check(rc, "moe_grad_clip")
+
+
+def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                       device_status: torch.Tensor | None = None) -> torch.Tensor:
+    """moe_grad_norm and moe_grad_clip in two kernels; returns the norm before clipping, f32 [1]."""
+    g, o = _clip_lists("moe_clip_grad_norm", grads, out)
+    L = lib()
+    with _on(g.device):
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=g.device)
+        elif norm.shape != (1,) or norm.dtype != torch.float32:
+            raise MoEError(1, "moe_clip_grad_norm", "norm must be float32 [1]")
+        nbytes = L.moe_grad_norm_workspace(len(g))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
+        rc = L.moe_clip_grad_norm(g.raw, None if o is None else o.raw, max_norm, _addr(norm), _addr(ws), nbytes,
+                                  _status_addr(device_status, "moe_clip_grad_norm"), _raw_stream(norm))
+    if rc:
+        _check(rc, "moe_clip_grad_norm")
+    return norm

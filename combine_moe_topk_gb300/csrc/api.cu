@@ -11,9 +11,12 @@
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <unordered_set>
+#include <vector>
 
 #include "../../include/moe_gb300.h"
 #include "internal.h"
@@ -34,12 +37,18 @@ struct moe_handle_s {
   int absent;          // expert id -1 = an absent route
 };
 
+struct moe_tensor_list_s {
+  int device;  // -1: no tensors
+  std::vector<moe::GradTensor> t;
+};
+
 namespace {
 
 thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches[MOE_KERNEL_COUNT];
 std::mutex g_mu;
 std::unordered_set<const moe_handle_s*> g_live;  // handles not yet destroyed
+std::unordered_set<const moe_tensor_list_s*> g_lists;
 int g_hold_tile = -1;                            // test hook, see moe_debug_hold_layout_tile
 long long g_hold_timeout_ns = 0;
 
@@ -1193,6 +1202,309 @@ moe_status moe_linear_bwd(const moe_linear_bwd_desc* d, const void* dy, const vo
   moe::LinearBwdArgs a = {dy, x, W, z, dx, dW, db, workspace, device_status, d->lddy, d->ldx, d->ldw, d->ldz, d->s, d->K,
                           d->N, d->act, d->dy_dtype == MOE_F32, d->dx_dtype == MOE_F32, d->dw_dtype == MOE_F32};
   return gemm_result(moe::launch_linear_bwd(a, *di, st), "linear_bwd launch", MOE_KERNEL_LINEAR_BWD);
+}
+
+namespace {
+
+moe_status check_gated(int s, int K, int N, int act) {
+  if (s < 0 || K < 8 || K % 8 != 0 || N < 8 || N % 8 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "need s >= 0 and K and N positive multiples of 8");
+  if (s > (1 << 30) || N > (1 << 29)) return fail(MOE_ERR_INVALID_ARG, "s must be <= 2^30 and N <= 2^29");
+  if (K > (1 << 18)) return fail(MOE_ERR_INVALID_ARG, "K must be <= 2^18");
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID_ARG, "unknown activation");
+  return MOE_OK;
+}
+
+// Strides of rows that are read in 16-byte pieces.
+moe_status check_ld8(int64_t ld, int m, const char* name) {
+  MOE_TRY(check_ld(ld, m, name));
+  if (ld % 8 != 0) return fail(MOE_ERR_INVALID_ARG, std::string(name) + " must be a multiple of 8 (rows of whole 16 bytes)");
+  return MOE_OK;
+}
+
+moe_status check_grouped_gated(moe_handle h, int rows, int K, int N, int act) {
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID_ARG, "unknown activation");
+  if (K > (1 << 18)) return fail(MOE_ERR_INVALID_ARG, "K must be <= 2^18");
+  if (N > (1 << 29)) return fail(MOE_ERR_INVALID_ARG, "N must be <= 2^29");
+  if (2LL * h->e * N > 2147483647LL) return fail(MOE_ERR_INVALID_ARG, "2 * e * N must be < 2^31");
+  return check_gemm(h, rows, K, N, nullptr, "", 0, nullptr, nullptr);  // the sizes
+}
+
+}  // namespace
+
+moe_status moe_gated_linear(const moe_gated_desc* d, const void* x, const void* W, const void* bias, void* h, void* z,
+                            int32_t* device_status, void* stream) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+  MOE_TRY(check_gated(d->s, d->K, d->N, d->act));
+  MOE_TRY(check_ld8(d->ldx, d->K, "ldx"));
+  MOE_TRY(check_ld8(d->ldw, d->K, "ldw"));
+  if (bias) MOE_TRY(check_dtype((moe_dtype)d->bias_dtype, "bias_dtype"));
+  MOE_TRY(check_status_ptr(device_status));
+  if (d->s == 0) return MOE_OK;
+  int dev = 0;
+  MOE_TRY(check_ptrs({{x, "x", false}, {W, "W", false}, {bias, "bias", true}, {h, "h", false}, {z, "z", true}}, &dev));
+  MOE_TRY(check_device_ptr(device_status, "device_status", dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
+  moe::GatedArgs a = {x, W, bias, h, z, device_status, d->ldx, d->ldw, d->s, d->K, d->N, d->act, d->bias_dtype == MOE_F32};
+  return gemm_result(moe::launch_gated(a, *di, static_cast<cudaStream_t>(stream)), "gated_linear launch", MOE_KERNEL_GATED);
+}
+
+size_t moe_gated_linear_bwd_workspace(const moe_gated_bwd_desc* d, int dx, int dW, int db) {
+  if (!d || d->s < 1 || d->N < 1) return 0;
+  return moe::gated_bwd_workspace(d->s, d->N, dx || dW, (dx && d->dx_dtype == MOE_F32) || (dW && d->dw_dtype == MOE_F32),
+                                  db != 0);
+}
+
+moe_status moe_gated_linear_bwd(const moe_gated_bwd_desc* d, const void* dh, const void* x, const void* W, const void* z,
+                                void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
+                                int32_t* device_status, void* stream) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "desc is NULL");
+  MOE_TRY(check_gated(d->s, d->K, d->N, d->act));
+  MOE_TRY(check_dtype((moe_dtype)d->dh_dtype, "dh_dtype"));
+  MOE_TRY(check_ld8(d->lddh, d->N, "lddh"));
+  MOE_TRY(check_ld8(d->ldz, 2 * d->N, "ldz"));
+  if (dW) MOE_TRY(check_ld8(d->ldx, d->K, "ldx"));
+  if (dx) MOE_TRY(check_ld8(d->ldw, d->K, "ldw"));
+  if (dx) MOE_TRY(check_dtype((moe_dtype)d->dx_dtype, "dx_dtype"));
+  if (dW) MOE_TRY(check_dtype((moe_dtype)d->dw_dtype, "dw_dtype"));
+  MOE_TRY(check_status_ptr(device_status));
+  const bool none = d->s == 0;
+  if (!dx && !dW && !db) return MOE_OK;
+  if (none && !dW && !db) return MOE_OK;
+  const size_t need = moe_gated_linear_bwd_workspace(d, dx != nullptr, dW != nullptr, db != nullptr);
+  MOE_TRY(check_workspace(workspace, workspace_bytes, need));
+  int dev = 0;
+  MOE_TRY(check_ptrs({{dh, "dh", none}, {x, "x", none || !dW}, {W, "W", none || !dx}, {z, "z", none}, {dx, "dx", true},
+                      {dW, "dW", true}, {db, "db", true}, {workspace, "workspace", need == 0}}, &dev));
+  MOE_TRY(check_device_ptr(device_status, "device_status", dev));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(dev, &di));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (none) {  // sums over no tokens
+    cudaError_t err = cudaSuccess;
+    if (dW) err = cudaMemsetAsync(dW, 0, 2 * (size_t)d->N * d->K * (d->dw_dtype == MOE_F32 ? 4 : 2), st);
+    if (err == cudaSuccess && db) err = cudaMemsetAsync(db, 0, 2 * (size_t)d->N * 4, st);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "gated_linear_bwd zeroing");
+  }
+  moe::GatedBwdArgs a = {dh, x, W, z, dx, dW, db, workspace, device_status, d->lddh, d->ldx, d->ldw, d->ldz, d->s, d->K,
+                         d->N, d->act, d->dh_dtype == MOE_F32, d->dx_dtype == MOE_F32, d->dw_dtype == MOE_F32};
+  return gemm_result(moe::launch_gated_bwd(a, *di, st), "gated_linear_bwd launch", MOE_KERNEL_GATED_BWD);
+}
+
+moe_status moe_grouped_gated(moe_handle h, int rows, int K, int N, int act, const void* X, const void* W, void* H, void* Z,
+                             void* stream) {
+  MOE_TRY(built_handle(h));
+  MOE_TRY(check_grouped_gated(h, rows, K, N, act));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(check_gemm(h, rows, K, N, X, "X", rows, W, H));
+  MOE_TRY(check_ptr(Z, "Z", true));
+  MOE_TRY(check_device_ptr(Z, "Z", h->device));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(h->device, &di));
+  return gemm_result(moe::launch_grouped_gated(h->out.offsets, h->out.counts, h->e, rows, K, N, act, X, W, H, Z,
+                                               h->out.status, *di, static_cast<cudaStream_t>(stream)),
+                     "grouped_gated launch", MOE_KERNEL_GROUPED_GATED);
+}
+
+moe_status moe_dispatch_grouped_gated(moe_handle h, int s, int rows, int K, int N, int act, const void* x, const void* W,
+                                      void* H, void* Z, void* stream) {
+  MOE_TRY(built_handle(h));
+  MOE_TRY(check_shape(h, s, rows));
+  MOE_TRY(check_grouped_gated(h, rows, K, N, act));
+  if (rows == 0 || s == 0) return MOE_OK;
+  MOE_TRY(check_gemm(h, rows, K, N, x, "x", s, W, H));
+  MOE_TRY(check_ptr(Z, "Z", true));
+  MOE_TRY(check_device_ptr(Z, "Z", h->device));
+  const moe::DeviceInfo* di = nullptr;
+  MOE_TRY(device_state(h->device, &di));
+  return gemm_result(moe::launch_dispatch_gated(h->out.offsets, h->out.counts, h->out.inv_row, h->e, rows, s, K, N, act, x, W,
+                                                H, Z, h->out.status, *di, static_cast<cudaStream_t>(stream)),
+                     "dispatch_grouped_gated launch", MOE_KERNEL_GROUPED_GATED);
+}
+
+namespace {
+
+// The pointers of a grouped product's backward pass (D the gradient of its
+// result), and the zeros of no rows; *done: nothing is left to do.
+moe_status grouped_bwd_begin(moe_handle h, int rows, int K, int wide, const void* D, const char* name, const void* X,
+                             const void* W, void* dX, void* dW, cudaStream_t st, const moe::DeviceInfo** di, bool* done) {
+  *done = !dX && !dW;
+  if (*done || (rows == 0 && !dW)) {
+    *done = true;
+    return MOE_OK;
+  }
+  const bool none = rows == 0;
+  MOE_TRY(handle_device(h));
+  int dev = 0;
+  MOE_TRY(check_ptrs({{D, name, none}, {X, "X", none || !dW}, {W, "W", none || !dX}, {dX, "dX", true}, {dW, "dW", true}}, &dev));
+  MOE_TRY(device_state(h->device, di));
+  if (none) {
+    *done = true;
+    cudaError_t err = cudaMemsetAsync(dW, 0, (size_t)h->e * wide * K * 2, st);
+    if (err != cudaSuccess) return cuda_fail(err, "zeroing dW");
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_grouped_gemm_bwd(moe_handle h, int rows, int K, int N, const void* dY, const void* X, const void* W, void* dX,
+                                void* dW, void* stream) {
+  MOE_TRY(built_handle(h));
+  MOE_TRY(check_gemm(h, rows, K, N, nullptr, "", 0, nullptr, nullptr));
+  const moe::DeviceInfo* di = nullptr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  bool done = false;
+  MOE_TRY(grouped_bwd_begin(h, rows, K, N, dY, "dY", X, W, dX, dW, st, &di, &done));
+  if (done) return MOE_OK;
+  return gemm_result(moe::launch_grouped_bwd(h->out.offsets, h->out.counts, h->e, rows, K, N, dY, X, W, dX, dW, h->out.status,
+                                             *di, st),
+                     "grouped_gemm_bwd launch", MOE_KERNEL_GROUPED_GEMM_BWD);
+}
+
+size_t moe_grouped_gated_bwd_workspace(int rows, int N) { return rows < 1 || N < 1 ? 0 : (size_t)rows * 2 * N * 2; }
+
+moe_status moe_grouped_gated_bwd(moe_handle h, int rows, int K, int N, int act, const void* dH, const void* X, const void* W,
+                                 const void* Z, void* dX, void* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  MOE_TRY(built_handle(h));
+  MOE_TRY(check_grouped_gated(h, rows, K, N, act));
+  const moe::DeviceInfo* di = nullptr;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows > 0 && (dX || dW)) {
+    MOE_TRY(check_workspace(workspace, workspace_bytes, moe_grouped_gated_bwd_workspace(rows, N)));
+    MOE_TRY(check_ptr(Z, "Z"));
+    MOE_TRY(check_device_ptr(Z, "Z", h->device));
+    MOE_TRY(check_device_ptr(workspace, "workspace", h->device));
+  }
+  bool done = false;
+  MOE_TRY(grouped_bwd_begin(h, rows, K, 2 * N, dH, "dH", X, W, dX, dW, st, &di, &done));
+  if (done) return MOE_OK;
+  cudaError_t err = moe::launch_grouped_dz(h->out.offsets, h->out.counts, h->e, rows, N, act, dH, Z, workspace, *di, st);
+  if (err == cudaSuccess)
+    err = moe::launch_grouped_bwd(h->out.offsets, h->out.counts, h->e, rows, K, 2 * N, workspace, X, W, dX, dW, h->out.status,
+                                  *di, st);
+  return gemm_result(err, "grouped_gated_bwd launch", MOE_KERNEL_GROUPED_GATED_BWD);
+}
+
+// ---- lists of gradients ---------------------------------------------------------
+
+moe_status moe_tensor_list_create(const moe_tensor* tensors, int count, moe_tensor_list* out) {
+  if (!out) return fail(MOE_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (count < 0 || (count > 0 && !tensors)) return fail(MOE_ERR_INVALID_ARG, "need count >= 0 and tensors");
+  long long chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_tensor& t = tensors[i];
+    const std::string name = "tensor " + std::to_string(i);
+    MOE_TRY(check_dtype((moe_dtype)t.dtype, name.c_str()));
+    if (t.numel < 0 || t.numel > (int64_t)1 << 42) return fail(MOE_ERR_INVALID_ARG, name + ": numel must be in [0, 2^42]");
+    if (t.numel > 0 && !t.data) return fail(MOE_ERR_INVALID_ARG, name + " is NULL");
+    if (reinterpret_cast<uintptr_t>(t.data) % (t.dtype == MOE_F32 ? 4 : 2))
+      return fail(MOE_ERR_INVALID_ARG, name + " is not aligned to its elements");
+    chunks += moe::grad_chunks({t.data, t.numel, t.dtype == MOE_F32});
+    if (chunks > 2147483647LL) return fail(MOE_ERR_INVALID_ARG, "the list holds too many elements");
+  }
+  int dev = 0;
+  if (count > 0) MOE_TRY(current_device(&dev));
+  for (int i = 0; i < count; ++i)
+    if (tensors[i].numel > 0) MOE_TRY(check_device_ptr(tensors[i].data, ("tensor " + std::to_string(i)).c_str(), dev));
+  std::unique_ptr<moe_tensor_list_s> list(new (std::nothrow) moe_tensor_list_s);
+  if (!list) return fail(MOE_ERR_OOM, "no host memory for the list");
+  list->device = count > 0 ? dev : -1;
+  try {
+    list->t.reserve(count);
+    for (int i = 0; i < count; ++i) list->t.push_back({tensors[i].data, tensors[i].numel, tensors[i].dtype == MOE_F32});
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_lists.insert(list.get());
+  } catch (const std::bad_alloc&) {
+    return fail(MOE_ERR_OOM, "no host memory for the list");
+  }
+  *out = list.release();
+  return MOE_OK;
+}
+
+moe_status moe_tensor_list_destroy(moe_tensor_list list) {
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!list || !g_lists.erase(list)) return fail(MOE_ERR_HANDLE_MISMATCH, "the list is unknown or destroyed");
+  }
+  delete list;
+  return MOE_OK;
+}
+
+size_t moe_grad_norm_workspace(int count) { return moe::grad_norm_workspace(count); }
+
+namespace {
+
+moe_status live_list(moe_tensor_list list, const char* name) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!list || !g_lists.count(list)) return fail(MOE_ERR_HANDLE_MISMATCH, std::string(name) + " is unknown or destroyed");
+  return MOE_OK;
+}
+
+// The lists, the device, the norm's place, and the workspace where there is one.
+moe_status check_grads(moe_tensor_list grads, moe_tensor_list out, const float* norm, float max_norm) {
+  MOE_TRY(live_list(grads, "grads"));
+  if (!(max_norm >= 0.f)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be >= 0");
+  if (out) {
+    MOE_TRY(live_list(out, "out"));
+    if (out->t.size() != grads->t.size()) return fail(MOE_ERR_INVALID_ARG, "out holds another number of tensors");
+    for (size_t i = 0; i < out->t.size(); ++i)
+      if (out->t[i].n != grads->t[i].n || out->t[i].f32 != grads->t[i].f32)
+        return fail(MOE_ERR_INVALID_ARG, "out: tensor " + std::to_string(i) + " has another size or type");
+  }
+  if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
+  if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(MOE_ERR_INVALID_ARG, "norm is not 4-byte aligned");
+  int dev = 0;
+  MOE_TRY(current_device(&dev));
+  if ((grads->device >= 0 && dev != grads->device) || (out && out->device >= 0 && dev != out->device))
+    return fail(MOE_ERR_INVALID_ARG, "the current device is not the list's device");
+  return check_device_ptr(norm, "norm", dev);
+}
+
+moe_status check_norm_call(moe_tensor_list grads, const void* workspace, size_t bytes, const int32_t* device_status) {
+  MOE_TRY(check_status_ptr(device_status));
+  MOE_TRY(check_workspace(workspace, bytes, moe::grad_norm_workspace((int)grads->t.size())));
+  int dev = 0;
+  MOE_TRY(current_device(&dev));
+  MOE_TRY(check_device_ptr(workspace, "workspace", dev));
+  return check_device_ptr(device_status, "device_status", dev);
+}
+
+}  // namespace
+
+moe_status moe_grad_norm(moe_tensor_list grads, float* norm, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                         void* stream) {
+  MOE_TRY(check_grads(grads, nullptr, norm, 0.f));
+  MOE_TRY(check_norm_call(grads, workspace, workspace_bytes, device_status));
+  cudaError_t err = moe::launch_grad_norm(grads->t.data(), (int)grads->t.size(), norm, workspace, device_status,
+                                          static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "grad_norm launch");
+  g_launches[MOE_KERNEL_GRAD_NORM]++;
+  return MOE_OK;
+}
+
+moe_status moe_grad_clip(moe_tensor_list grads, moe_tensor_list out, const float* norm, float max_norm, void* stream) {
+  MOE_TRY(check_grads(grads, out, norm, max_norm));
+  cudaError_t err = moe::launch_grad_clip(grads->t.data(), out ? out->t.data() : nullptr, (int)grads->t.size(),
+                                          const_cast<float*>(norm), max_norm, nullptr, nullptr,
+                                          static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "grad_clip launch");
+  g_launches[MOE_KERNEL_GRAD_CLIP]++;
+  return MOE_OK;
+}
+
+moe_status moe_clip_grad_norm(moe_tensor_list grads, moe_tensor_list out, float max_norm, float* norm, void* workspace,
+                              size_t workspace_bytes, int32_t* device_status, void* stream) {
+  MOE_TRY(check_grads(grads, out, norm, max_norm));
+  MOE_TRY(check_norm_call(grads, workspace, workspace_bytes, device_status));
+  cudaError_t err = moe::launch_grad_clip(grads->t.data(), out ? out->t.data() : nullptr, (int)grads->t.size(), norm, max_norm,
+                                          workspace, device_status, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "clip_grad_norm launch");
+  g_launches[MOE_KERNEL_GRAD_NORM]++;
+  g_launches[MOE_KERNEL_GRAD_CLIP]++;
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -36,6 +36,7 @@
 // Every mbarrier wait is bounded on the global timer, each from its own start;
 // a time-out records MOE_DEV_TIMEOUT and the roles wind down to the TMEM release.
 #include "common.cuh"
+#include "grouped.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -45,14 +46,13 @@ namespace {
 
 constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kTmemCols = 2 * BN;     // two fp32 accumulators of 128 lanes x 256 columns
-constexpr int kThreads = 256;        // tile-fed form
+constexpr int kGatedWarps = 8;       // epilogue warps of the gated form (4 in the plain one)
 // Warps gathering the fused form's A rows: 8 (16 rows each) measured 1-4 %
 // faster than 4 and 3 % faster than 16 (fewer registers per thread at 768
 // threads); 2 were 20-30 % slower.
 #ifndef MOE_GEMM_GATHER_WARPS
 #define MOE_GEMM_GATHER_WARPS 8
 #endif
-constexpr int kGatherThreads = kThreads + 32 * MOE_GEMM_GATHER_WARPS;  // fused form: + warps gathering A
 constexpr int kGatherRows = BM / MOE_GEMM_GATHER_WARPS;  // A rows per gathering warp
 static_assert(kGatherRows % 4 == 0 && kGatherRows >= 4, "a gathering warp copies 4 rows per instruction");
 constexpr int kMaxE = 256;
@@ -61,6 +61,7 @@ constexpr int kMaxE = 256;
 constexpr int kStageRowBytes = 64 * 2 + 16;
 constexpr int kEpiWarpBytes = 32 * kStageRowBytes;
 constexpr int kEpiBytes = 4 * kEpiWarpBytes;
+static_assert(kGatedWarps * kRowStage <= kEpiBytes, "the gated form's staging tiles fit in the same place");
 
 struct GemmParams {
   const __nv_bfloat16* x;  // gather mode: token rows [s, K]
@@ -72,6 +73,8 @@ struct GemmParams {
   __nv_bfloat16* Y;
   int32_t* status;
   long long timeout_ns;  // of a single wait
+  __nv_bfloat16* Z;      // gated form: [rows, 2N], or NULL
+  int act;
 };
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle (as TMA writes
@@ -139,27 +142,58 @@ __device__ __forceinline__ void store_accumulator(uint32_t tcol, int ew, int lan
   }
 }
 
+// Drain a gated unit's accumulator: columns [0, 128) are the gate's, [128, 256) the
+// same columns of the factor.  Two warps share 32 lanes, each with half of the 128
+// columns of h, 32 at a time:
+//   h = act(g) u,  and z = [g | u] where it is kept.
+__device__ __forceinline__ void store_gated(uint32_t tcol, int ew, int half, int lane, uint8_t* stage, const GemmParams& p,
+                                            int r0, int n0, int nvalid) {
+  const int rows = nvalid - 32 * ew;
+  if (rows <= 0) return;  // the whole warp
+  const long long at = r0 + 32 * ew;
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int j = 64 * half + 32 * c, col = n0 + j, cols = p.N - col;
+    if (cols <= 0) return;
+    uint32_t v[32], w[16];
+    float g[32], u[32];
+    tmem_ld32(tcol + (uint32_t)j, v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] = __uint_as_float(v[i]);
+    tmem_ld32(tcol + (uint32_t)(BN / 2 + j), v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = __uint_as_float(v[i]);
+    if (p.Z) {
+      pack_bf16(g, w);
+      store_rows(stage, w, p.Z + at * 2 * p.N + col, 2LL * p.N, rows, cols, lane);
+      pack_bf16(u, w);
+      store_rows(stage, w, p.Z + at * 2 * p.N + p.N + col, 2LL * p.N, rows, cols, lane);
+    }
+    if (p.act != MOE_ACT_NONE) activate<32>(g, p.act);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) g[i] *= u[i];
+    pack_bf16(g, w);
+    store_rows(stage, w, p.Y + at * p.N + col, p.N, rows, cols, lane);
+  }
+}
+
 // Unit u -> expert x, first row r0 and owned rows of its 128-row block, and
-// the column tile n0.  s_blk[x] = blocks of the experts before x.
+// the column tile n0 (width columns a tile).  s_blk[x] = blocks of the experts before x.
 struct Unit {
   int x, r0, nvalid, n0;
 };
 
 __device__ __forceinline__ Unit decode_unit(int u, int ntn, const int* s_blk, const int* s_off,
-                                            const int* s_cnt, int e) {
+                                            const int* s_cnt, int e, int width) {
   const int b = u / ntn;
-  int lo = 0, hi = e;  // s_blk[lo] <= b < s_blk[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_blk[mid] <= b) lo = mid; else hi = mid;
-  }
+  const int lo = expert_of(b, s_blk, e);
   Unit t;
   const int i = b - s_blk[lo];
   t.x = lo;
   t.r0 = s_off[lo] + BM * i;
   const int left = s_cnt[lo] - BM * i;
   t.nvalid = left < BM ? left : BM;
-  t.n0 = (u - b * ntn) * BN;
+  t.n0 = (u - b * ntn) * width;
   return t;
 }
 
@@ -215,8 +249,19 @@ __device__ __forceinline__ uint32_t mma_idesc_pair() {
   return d;
 }
 
-template <bool kGather>
-__global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
+// Roles of a CTA: four control warps, the epilogue's, then the gathering ones.
+template <bool kGather, bool kGated>
+struct Roles {
+  static constexpr int kEpiWarps = kGated ? kGatedWarps : 4;
+  static constexpr int kMain = 128 + 32 * kEpiWarps;
+  static constexpr int kAll = kMain + (kGather ? 32 * MOE_GEMM_GATHER_WARPS : 0);
+};
+
+// kGated: W is [e, 2N, K], each expert's N gate rows and then its N factor rows; a
+// unit is 256 rows x 128 columns of h, the first CTA holding the gate's 128 rows of
+// W and the second the factor's, so that both land in the same row of TMEM.
+template <bool kGather, bool kGated>
+__global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
     grouped_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                              const __grid_constant__ CUtensorMap tmB, const GemmParams p) {
   constexpr int kPairABytes = kPairKB * kSubA;  // this CTA's 128 rows of A
@@ -233,7 +278,9 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0 or 1 within the pair
-  constexpr int kGatherWarps = (kGatherThreads - kThreads) / 32;
+  constexpr int kEpiWarps = Roles<kGather, kGated>::kEpiWarps, kMain = Roles<kGather, kGated>::kMain;
+  constexpr int kWidth = kGated ? BN / 2 : BN;  // columns of Y (of h) a unit
+  constexpr int kGatherWarps = MOE_GEMM_GATHER_WARPS;
   constexpr int kGatherArrivals = kGatherWarps * 32;  // one per gathering thread and stage
   // identical static layout in both CTAs: the dynamic buffer starts at the
   // same offset, so the MMA's descriptors address the same tiles in both
@@ -252,7 +299,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 2 * 4);  // rank 0: the epilogue warps of both ranks
+      mbar_init(&tempty[i], 2 * kEpiWarps);  // rank 0: the epilogue warps of both ranks
     }
     mbar_init(&mma_drain, 1);
     fence_barrier_init();
@@ -265,22 +312,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   } else if (warp == 3) {
-    // exclusive prefix over experts of their 256-row block counts
-    int carry = 0;
-    for (int x0 = 0; x0 < p.e; x0 += 32) {
-      const int x = x0 + lane;
-      const int c = x < p.e ? s_cnt[x] : 0;
-      const int blocks = c > 0 ? (c + BM2 - 1) / BM2 : 0;
-      int v = blocks;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int w = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += w;
-      }
-      if (x < p.e) s_blk[x] = carry + v - blocks;
-      carry += __shfl_sync(0xffffffffu, v, 31);
-    }
-    if (lane == 0) s_blk[p.e] = carry;
+    prefix_blocks(s_cnt, s_blk, p.e, BM2, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -288,7 +320,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
   tc_fence_after();
   const uint32_t tbase = tmem_base;
 
-  const int ntn = (p.N + BN - 1) / BN;  // the last column tile may be partial
+  const int ntn = (p.N + kWidth - 1) / kWidth;  // the last column tile may be partial
   const int nunits = s_blk[p.e] * ntn;
   const int kblocks = (p.K + BK * kPairKB - 1) / (BK * kPairKB);  // per stage; columns past K read as zeros
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
@@ -299,7 +331,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e);  // rows in units of BM2 below
+      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);  // rows in units of BM2 below
       const int b = u / ntn;
       const int r0 = s_off[t.x] + BM2 * (b - s_blk[t.x]) + BM * (int)rank;
       for (int kb = 0; kb < kblocks; ++kb) {
@@ -314,7 +346,8 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
         for (int q = 0; q < kPairKB; ++q) {
           const int kx = (kb * kPairKB + q) * BK;
           if (!kGather) tma_load_2d_pair(sa + q * kSubA, &tmA, kx, r0, fb);
-          tma_load_2d_pair(sa + kPairABytes + q * kSubB, &tmB, kx, t.x * p.N + t.n0 + (BN / 2) * (int)rank, fb);
+          const int nrow = kGated ? (2 * t.x + (int)rank) * p.N + t.n0 : t.x * p.N + t.n0 + (BN / 2) * (int)rank;
+          tma_load_2d_pair(sa + kPairABytes + q * kSubB, &tmB, kx, nrow, fb);
         }
         if (++stage == kPairStages) {
           stage = 0;
@@ -332,7 +365,7 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       }
     }
     if (!ok) atomicOr(&s_err, 1);
-  } else if (kGather && warp >= kThreads / 32) {
+  } else if (kGather && warp >= kMain / 32) {
     // ---- A gather (fused form, both ranks): this CTA's 128 rows ------------
     // Each lane copies 16 bytes of kGatherRows / 4 rows per K block (8 lanes per 128-byte
     // row, the swizzle as in the one-SM form), then hands its copies of the
@@ -343,13 +376,13 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
     // arrive on its full barrier, rank 1's on its own `gathered` barrier,
     // forwarded below; the waiter on each fences the async proxy.  A unit's
     // row-to-token indices are loaded while the previous unit is gathered.
-    const int gw = warp - kThreads / 32, chunk = lane & 7;
+    const int gw = warp - kMain / 32, chunk = lane & 7;
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
     // token of each of this lane's kGatherRows / 4 rows in unit u; -1 for rows no route owns
     auto unit_tokens = [&](int u, int* tok) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e);
+      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);
       const int i = u / ntn - s_blk[t.x];
       const int r0 = s_off[t.x] + BM2 * i + BM * (int)rank;
       const int left = s_cnt[t.x] - BM2 * i - BM * (int)rank;
@@ -479,15 +512,15 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       mbar_wait_limited(&mma_drain, 0, p.timeout_ns);
       atomicOr(&s_err, 1);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 4 + kEpiWarps) {
     // ---- epilogue (both ranks): own 128 rows ------------------------------
-    const int ew = warp - 4;
+    const int ew = warp & 3;
     const uint32_t te0 = mapa_shared(smem_addr(&tempty[0]), 0), te1 = mapa_shared(smem_addr(&tempty[1]), 0);
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e);
+      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);
       const int b = u / ntn;
       const int i = b - s_blk[t.x];
       const int r0 = s_off[t.x] + BM2 * i + BM * (int)rank;
@@ -500,8 +533,12 @@ __global__ void __launch_bounds__(kGather ? kGatherThreads : kThreads, 1)
       }
       tphase[acc] ^= 1u;
       tc_fence_after();
-      store_accumulator(tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN), ew, lane,
-                        smem + kPairStages * kPairStageBytes + ew * kEpiWarpBytes, p.Y, p.N, r0, t.n0, nvalid);
+      const uint32_t tcol = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN);
+      uint8_t* stage_buf = smem + kPairStages * kPairStageBytes;
+      if constexpr (kGated)
+        store_gated(tcol, ew, (warp - 4) >> 2, lane, stage_buf + (warp - 4) * kRowStage, p, r0, t.n0, nvalid);
+      else
+        store_accumulator(tcol, ew, lane, stage_buf + ew * kEpiWarpBytes, p.Y, p.N, r0, t.n0, nvalid);
       tc_fence_before();
       __syncwarp();  // every lane's TMEM reads are done
       if (lane == 0) {
@@ -537,23 +574,24 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kGather>
+template <bool kGather, bool kGated = false>
 cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const GemmParams& p,
                         const DeviceInfo& di, cudaStream_t st) {
+  constexpr int kWidth = kGated ? BN / 2 : BN;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(grouped_gemm_pair_kernel<kGather>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(grouped_gemm_pair_kernel<kGather, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 kPairSmemBytes);
   });
   if (err != cudaSuccess) return err;
   // pair units: at most ceil(rows / 256) + e blocks of 256 rows, times the column tiles
-  const long long units = (((long long)p.rows + BM2 - 1) / BM2 + p.e) * ((p.N + BN - 1) / BN);
+  const long long units = (((long long)p.rows + BM2 - 1) / BM2 + p.e) * ((p.N + kWidth - 1) / kWidth);
   long long pairs = di.sms / 2;
   if (units < pairs) pairs = units;
   if (pairs < 1) pairs = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kGather ? kGatherThreads : kThreads);
+  cfg.blockDim = dim3(Roles<kGather, kGated>::kAll);
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -563,7 +601,7 @@ cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kGather>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kGather, kGated>, ma, mb, p);
 }
 
 GemmParams params(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N,
@@ -582,6 +620,8 @@ GemmParams params(const int32_t* offsets, const int32_t* counts, int e, int rows
   p.status = status;
   // the longest wait is the epilogue's, for a whole contraction: under 1 us for 128 of K when all is well
   p.timeout_ns = kWaitNs + 20000LL * (K / 128);
+  p.Z = nullptr;
+  p.act = MOE_ACT_NONE;
   return p;
 }
 
@@ -607,6 +647,33 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
   p.s = s;
   if (!make_map(&mb, W, (uint64_t)K, (uint64_t)e * (uint64_t)N, BN / 2)) return cudaErrorInvalidValue;
   return launch_pair<true>(mb, mb, p, di, st);  // A is gathered by threads: no A map
+}
+
+cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, int act,
+                                 const void* X, const void* W, void* H, void* Z, int32_t* status, const DeviceInfo& di,
+                                 cudaStream_t st) {
+  CUtensorMap ma, mb;
+  if (!make_map(&ma, X, (uint64_t)K, (uint64_t)rows, BM) ||
+      !make_map(&mb, W, (uint64_t)K, 2 * (uint64_t)e * (uint64_t)N, BN / 2))
+    return cudaErrorInvalidValue;
+  GemmParams p = params(offsets, counts, e, rows, K, N, H, status);
+  p.Z = static_cast<__nv_bfloat16*>(Z);
+  p.act = act;
+  return launch_pair<false, true>(ma, mb, p, di, st);
+}
+
+cudaError_t launch_dispatch_gated(const int32_t* offsets, const int32_t* counts, const int32_t* inv_row, int e, int rows,
+                                  int s, int K, int N, int act, const void* x, const void* W, void* H, void* Z,
+                                  int32_t* status, const DeviceInfo& di, cudaStream_t st) {
+  CUtensorMap mb;
+  GemmParams p = params(offsets, counts, e, rows, K, N, H, status);
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.inv_row = inv_row;
+  p.s = s;
+  p.Z = static_cast<__nv_bfloat16*>(Z);
+  p.act = act;
+  if (!make_map(&mb, W, (uint64_t)K, 2 * (uint64_t)e * (uint64_t)N, BN / 2)) return cudaErrorInvalidValue;
+  return launch_pair<true, true>(mb, mb, p, di, st);
 }
 
 }  // namespace moe

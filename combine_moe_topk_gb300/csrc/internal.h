@@ -215,4 +215,70 @@ size_t linear_bwd_workspace(int s, int N);  // enough for every call
 size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, bool products, bool f32_results, bool db);
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 
+// Its products alone: dx = dz W, dW = dz^T x (each may be NULL).  two: dz [s][lddz]
+// is followed by what its rounding to bf16 left, for the fp32 results.
+struct ProductsBwdArgs {
+  const void *dz, *x, *W;
+  void *dx, *dW;
+  int32_t* status;
+  long long lddz, ldx, ldw;
+  int s, K, N, dx_f32, dw_f32;
+  bool two;
+};
+cudaError_t launch_products_bwd(const ProductsBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
+
+// --- gated products ------------------------------------------------------------
+// W [2N][ldw]: the gate's rows, then the factor's; h [s][N], z [s][2N] or NULL, bf16.
+struct GatedArgs {
+  const void *x, *W, *bias;
+  void *h, *z;
+  int32_t* status;
+  long long ldx, ldw;
+  int s, K, N, act, bias_f32;
+};
+cudaError_t launch_gated(const GatedArgs& a, const DeviceInfo& di, cudaStream_t st);
+
+struct GatedBwdArgs {
+  const void *dh, *x, *W, *z;
+  void *dx, *dW;
+  float* db;
+  void* workspace;
+  int32_t* status;
+  long long lddh, ldx, ldw, ldz;
+  int s, K, N, act, dh_f32, dx_f32, dw_f32;
+};
+size_t gated_bwd_workspace(int s, int N, bool products, bool f32_results, bool db);
+cudaError_t launch_gated_bwd(const GatedBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
+
+// dz [rows][2N] of the rows that a route owns (others are left as they are).
+cudaError_t launch_grouped_dz(const int32_t* offsets, const int32_t* counts, int e, int rows, int N, int act, const void* dH,
+                              const void* Z, void* dz, const DeviceInfo& di, cudaStream_t st);
+
+// --- the experts' products, gated and backward ---------------------------------
+// H[r] = act(A[r] Wg[x]^T) * (A[r] Wu[x]^T), W [e][2N][K]; Z [rows][2N] or NULL.
+cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, int act,
+                                 const void* X, const void* W, void* H, void* Z, int32_t* status, const DeviceInfo& di,
+                                 cudaStream_t st);
+cudaError_t launch_dispatch_gated(const int32_t* offsets, const int32_t* counts, const int32_t* inv_row, int e, int rows,
+                                  int s, int K, int N, int act, const void* x, const void* W, void* H, void* Z,
+                                  int32_t* status, const DeviceInfo& di, cudaStream_t st);
+// dX[r] = dY[r] W[x] for owned rows; dW[x] = sum over x's rows dY[r]^T X[r] (each may be
+// NULL).  dY [rows][N], X, dX [rows][K], W, dW [e][N][K], bf16.
+cudaError_t launch_grouped_bwd(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, const void* dY,
+                               const void* X, const void* W, void* dX, void* dW, int32_t* status, const DeviceInfo& di,
+                               cudaStream_t st);
+
+// --- gradient norm and clipping --------------------------------------------------
+struct GradTensor {
+  void* p;
+  long long n;  // elements
+  int f32;
+};
+size_t grad_norm_workspace(int count);
+long long grad_chunks(const GradTensor& g);  // at least its chunks, for the check that a list's fit an int
+cudaError_t launch_grad_norm(const GradTensor* g, int count, float* norm, void* workspace, int32_t* status, cudaStream_t st);
+// out == NULL: in place.  workspace == NULL: *norm is given; else the norm is computed into it first.
+cudaError_t launch_grad_clip(const GradTensor* g, const GradTensor* out, int count, float* norm, float max_norm, void* workspace,
+                             int32_t* status, cudaStream_t st);
+
 }  // namespace moe

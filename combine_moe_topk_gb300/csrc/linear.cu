@@ -32,6 +32,7 @@
 #include <math_constants.h>
 
 #include "common.cuh"
+#include "grouped.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -40,119 +41,6 @@ namespace moe {
 namespace {
 
 typedef __nv_bfloat16 bf16;
-
-// ---- activations -------------------------------------------------------------
-
-constexpr float kInvSqrt2Pi = 0.39894228040143268f;  // 1 / sqrt(2 pi)
-constexpr float kTanhA = 0.79788456080286536f;       // sqrt(2 / pi)
-constexpr float kTanhB = 0.044715f;
-
-// 1 / (1 + exp(-v)); exp overflows to inf and the quotient to 0.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
-
-// One value, or two in one instruction.
-template <typename T>
-__device__ __forceinline__ T all_of(float v);
-template <>
-__device__ __forceinline__ float all_of<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float2 all_of<float2>(float v) { return both(v); }
-template <typename F>
-__device__ __forceinline__ float each(float v, F f) { return f(v); }
-template <typename F>
-__device__ __forceinline__ float2 each(float2 v, F f) { return make_float2(f(v.x), f(v.y)); }
-
-// Phi(z) = (1 + erf(z / sqrt 2)) / 2 and e = exp(-z^2 / 2), of one value or two.  For
-// x >= 0, Phi(-x) = e R(x) with R smooth and falling like 1 / x: a polynomial of
-// degree 8 in t = 1 / (1 + 0.305 x), without a constant, fitted for the least
-// largest relative error on [0, 14] (1.6 units of 2^-24; 6.4 with fp32's
-// roundings, to which the exponential adds about 2 z^2).  So the tail keeps its
-// relative precision, where 1 + erf cancels, and one exponential serves gelu's
-// slope too.  (With erff and expf the backward pass' kernel was bound by
-// instructions.)
-template <typename T>
-__device__ __forceinline__ T normal_cdf(T z, T& e) {
-  auto k = [](float v) { return all_of<T>(v); };
-  const T x = each(z, [](float v) { return fabsf(v); });
-  const T t = each(fma2(k(0.305f), x, k(1.f)), [](float v) { return __fdividef(1.f, v); });
-  e = each(mul2(mul2(x, x), k(-0.72134752044448170f)), exp2_approx);  // 2^(-x^2 / 2 log2 e)
-  T q = fma2(k(0.03669917955994606f), t, k(-0.1529882699251175f));
-  q = fma2(q, t, k(0.18571682274341583f));
-  q = fma2(q, t, k(-0.03797676041722298f));
-  q = fma2(q, t, k(0.12102164328098297f));
-  q = fma2(q, t, k(0.10342087596654892f));
-  q = fma2(q, t, k(0.12246681749820709f));
-  q = fma2(q, t, k(0.12163973599672318f));
-  q = mul2(q, mul2(t, e));
-  if constexpr (sizeof(T) == 8) return make_float2(z.x < 0.f ? q.x : 1.f - q.x, z.y < 0.f ? q.y : 1.f - q.y);
-  else return z < 0.f ? q : 1.f - q;
-}
-
-__device__ __forceinline__ float activated(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : (z != z ? z : 0.f);  // NaN stays
-    case MOE_ACT_GELU_TANH: return z * sigmoid(2.f * kTanhA * (z + kTanhB * z * z * z));  // (1 + tanh(u)) / 2 = sigmoid(2u)
-    case MOE_ACT_SILU: return z * sigmoid(z);
-    default: return z;
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void activate(float* f, int act) {
-  switch (act) {  // uniform over the grid; one loop for each, so that the code that runs is short
-    case MOE_ACT_RELU:
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_RELU);
-      break;
-    case MOE_ACT_GELU:
-      if constexpr (N == 1) {
-        float e;
-        f[0] *= normal_cdf(f[0], e);
-      } else {
-        // two values an instruction: 16384 x 128 x 4096, bound by this, 136 -> 113 us
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-          float2 e;
-          const float2 cdf = normal_cdf(make_float2(f[j], f[j + 1]), e);
-          f[j] *= cdf.x;
-          f[j + 1] *= cdf.y;
-        }
-      }
-      break;
-    case MOE_ACT_GELU_TANH:
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_GELU_TANH);
-      break;
-    case MOE_ACT_SILU:
-#pragma unroll
-      for (int j = 0; j < N; ++j) f[j] = activated(f[j], MOE_ACT_SILU);
-      break;
-    default: break;
-  }
-}
-
-__device__ __forceinline__ float slope(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case MOE_ACT_GELU: {
-      float e;
-      const float cdf = normal_cdf(z, e);
-      return fmaf(z * kInvSqrt2Pi, e, cdf);
-    }
-    case MOE_ACT_GELU_TANH: {
-      // s + z s' with s = sigmoid(2u); past 16 the slope is 0 or 1 in fp32, and z's
-      // square there would overflow beside s (1 - s) = 0
-      z = fabsf(z) > 16.f ? copysignf(16.f, z) : z;
-      const float s = sigmoid(2.f * kTanhA * (z + kTanhB * z * z * z));
-      return fmaf(z * s * (1.f - s), 2.f * kTanhA * (1.f + 3.f * kTanhB * z * z), s);
-    }
-    case MOE_ACT_SILU: {
-      const float s = sigmoid(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    default: return 1.f;
-  }
-}
 
 // ---- epilogue ------------------------------------------------------------------
 
@@ -256,75 +144,6 @@ struct Shape {
   static_assert(128 * kPartRow <= kStages * kStage, "a part fits in the ring");
 };
 
-// Matrix descriptor of a tile in shared memory, 128-byte swizzle, base on 1024
-// bytes.  Rows of 128 bytes along the contracted axis: groups of 8 rows 1024
-// bytes apart.  Rows along the other axis (kMN): 8 steps of the contracted axis
-// are 1024 bytes, the next 64 elements of the other axis 8192 bytes on.
-template <bool kMN>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3ffffu) >> 4);
-  d |= (uint64_t)(kMN ? 8192 >> 4 : 1) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-// Descriptor step of one MMA (16 of the contracted axis), in 16-byte units.
-template <bool kMN>
-constexpr uint64_t kstep() { return kMN ? 2048 >> 4 : 32 >> 4; }
-
-template <int CG, int BN, bool AT, bool BT>
-__device__ __forceinline__ uint32_t instr_desc() {
-  uint32_t d = 0;
-  d |= 1u << 4;                             // fp32 accumulator
-  d |= 1u << 7;                             // A bf16
-  d |= 1u << 10;                            // B bf16
-  d |= (AT ? 1u : 0u) << 15;                // A's rows run along m
-  d |= (BT ? 1u : 0u) << 16;                // B's rows run along n
-  d |= (uint32_t)(BN >> 3) << 17;
-  d |= (uint32_t)((128 * CG) >> 4) << 24;
-  return d;
-}
-
-__device__ __forceinline__ void tma_load_2d(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_addr(sdst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
-      : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void load_tile(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
-  if constexpr (CG == 2) tma_load_2d_pair(sdst, map, x, y, mbar);
-  else tma_load_2d(sdst, map, x, y, mbar);
-}
-
-template <int CG>
-__device__ __forceinline__ void mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t idesc, int accumulate) {
-  if constexpr (CG == 2) {
-    mma_bf16_pair(dt, ad, bd, idesc, accumulate);
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
-}
-
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if constexpr (CG == 2) {
-    mma_commit_pair(bar);
-  } else {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-  }
-}
-
 // 32 rows x 32 columns starting at (r0, n0), lane = row, v its columns.  The
 // usual way out (bulk): bias, activation and residual in that layout, then
 // the rounded rows into the warp's staging tile, which a TMA store writes,
@@ -351,6 +170,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
+               : "memory");
+}
+
 __device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* src, int x, int y, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -360,8 +186,8 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* 
   }
 }
 
-// 16 words of each lane's row, 64-byte pieces, columns starting at x.
-__device__ __forceinline__ void put_narrow(Bulk& b, const CUtensorMap* map, const uint32_t* w, int x, int y, int lane) {
+// 16 words of each lane's row into the next 64-byte piece.
+__device__ __forceinline__ uint8_t* fill_narrow(Bulk& b, const uint32_t* w, int lane) {
   uint8_t* dst = b.stage + b.piece * 2048;
   if (lane == 0) bulk_wait_read<1>();  // the store before last, from this piece
   __syncwarp();
@@ -369,8 +195,25 @@ __device__ __forceinline__ void put_narrow(Bulk& b, const CUtensorMap* map, cons
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<uint4*>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
         make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  store_piece(map, dst, x, y, lane);
   b.piece ^= 1;
+  return dst;
+}
+
+// The same stored, columns starting at x.
+__device__ __forceinline__ void put_narrow(Bulk& b, const CUtensorMap* map, const uint32_t* w, int x, int y, int lane) {
+  store_piece(map, fill_narrow(b, w, lane), x, y, lane);
+}
+
+// Half `part` of z's columns (0 the gate's, 1 the factor's).
+__device__ __forceinline__ void put_half_of_z(Bulk& b, const CUtensorMap* map, const uint32_t* w, int x, int part, int y,
+                                              int lane) {
+  uint8_t* src = fill_narrow(b, w, lane);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(map, src, x, part, y);
+    bulk_commit();
+  }
 }
 
 // 16 words as half `half` of a 128-byte piece whose columns start at x; the
@@ -386,14 +229,6 @@ __device__ __forceinline__ void put_half(Bulk& b, const CUtensorMap* map, const 
     *reinterpret_cast<uint4*>(b.stage + lane * 128 + (((4 * half + q) ^ (lane & 7)) << 4)) =
         make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
   if (half == 1 || last) store_piece(map, b.stage, x, y, lane);
-}
-
-__device__ __forceinline__ void pack_bf16(const float (&f)[32], uint32_t (&w)[16]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-    w[j] = *reinterpret_cast<const uint32_t*>(&h);
-  }
 }
 
 // 32 consecutive values of fp32 or bf16 memory, of which the first n (a
@@ -469,6 +304,42 @@ __device__ __forceinline__ void finish_bulk(const Epi& e, Bulk& b, const CUtenso
     if (!kPair || e.narrow) put_narrow(b, tmY, w, n0, r0, lane);
     else put_half(b, tmY, w, c & 1, n0 + 32 >= N, n0 - 32 * (c & 1), r0, lane);
   }
+}
+
+// A gated product's 32 columns: g and u hold the same columns of both halves of z,
+//   h = act(g + bias) * (u + bias of the other half).
+// N is a multiple of 8.
+template <bool kPair>
+__device__ __forceinline__ void finish_gated(const Epi& e, Bulk& b, const CUtensorMap* tmH, const CUtensorMap* tmZ,
+                                             const uint32_t (&g)[32], const uint32_t (&u)[32], int c, int r0, int n0, int M,
+                                             int N, int lane) {
+  if (r0 >= M || n0 >= N) return;  // the whole warp
+  float f[32], v[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    f[j] = __uint_as_float(g[j]);
+    v[j] = __uint_as_float(u[j]);
+  }
+  if (e.bias) {
+    Raw32 bias;
+    load32(bias, e.bias, e.bias_f32, n0, N - n0);
+    add32(bias, e.bias_f32, f);
+    load32(bias, e.bias, e.bias_f32, (long long)N + n0, N - n0);
+    add32(bias, e.bias_f32, v);
+  }
+  uint32_t w[16];
+  if (e.z) {
+    pack_bf16(f, w);
+    put_half_of_z(b, tmZ, w, n0, 0, r0, lane);
+    pack_bf16(v, w);
+    put_half_of_z(b, tmZ, w, n0, 1, r0, lane);
+  }
+  if (e.act != MOE_ACT_NONE) activate<32>(f, e.act);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) f[j] *= v[j];
+  pack_bf16(f, w);
+  if (!kPair || e.narrow) put_narrow(b, tmH, w, n0, r0, lane);
+  else put_half(b, tmH, w, c & 1, n0 + 32 >= N, n0 - 32 * (c & 1), r0, lane);
 }
 
 // The same where rows are not of 16 bytes, so that TMA cannot write them: a
@@ -680,6 +551,68 @@ __device__ __forceinline__ void join_parts(const GemmArgs& p, const Epi& e, cons
   }
 }
 
+// The same for a gated product's tile: BN / 2 columns of h, whose two halves of z lie
+// BN / 2 columns apart in the parts.
+template <int S, int BN>
+__device__ __forceinline__ void join_gated(const GemmArgs& p, const Epi& e, const Unit& t, int split, const uint8_t* parts) {
+  constexpr int kCols = BN / 2, kGroups = kCols / 4, kRounds = (128 / S * kGroups + kThreads - 1) / kThreads;
+  const int per = rows_of_share(t.m0, p.M, S), end = min(min(128, p.M - t.m0), (split + 1) * per);
+  auto row_of = [&](int j) { return split * per + (int)(threadIdx.x + j * kThreads) / kGroups; };
+  auto col_of = [&](int j) { return (int)(threadIdx.x + j * kThreads) % kGroups * 4; };
+  cluster_sync_all();  // every part is in its CTA's shared memory
+  float f[kRounds][2][4];
+  bool there[kRounds];
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    const int row = row_of(j), col = t.n0 + col_of(j);
+    there[j] = row < end && col < p.N;
+    if (!there[j]) continue;
+    uint4 v[2][S];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint8_t* own = parts + row * Shape<1, BN>::kPartRow + (q * kCols + col_of(j)) * 4;
+      v[q][0] = *reinterpret_cast<const uint4*>(own);
+#pragma unroll
+      for (int s = 1; s < S; ++s) v[q][s] = ld_cluster(mapa_shared(smem_addr(own), (split + s) & (S - 1)));
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      Vec<float>::to_float(v[q][0], f[j][q]);
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        float a[4];
+        Vec<float>::to_float(v[q][s], a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[j][q][i] += a[i];
+      }
+    }
+  }
+  cluster_arrive();
+#pragma unroll
+  for (int j = 0; j < kRounds; ++j) {
+    if (!there[j]) continue;
+    const int col = t.n0 + col_of(j);
+    const long long row = t.m0 + row_of(j);
+    if (e.bias) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float b[4];
+        load4(e.bias, e.bias_f32, q * p.N + col, true, 4, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[j][q][i] += b[i];
+      }
+    }
+    if (e.z) {
+      store4(e.z, 0, row * 2 * p.N + col, true, 4, f[j][0]);
+      store4(e.z, 0, row * 2 * p.N + p.N + col, true, 4, f[j][1]);
+    }
+    activate<4>(f[j][0], e.act);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[j][0][i] *= f[j][1][i];
+    store4(e.out, 0, row * p.N + col, true, 4, f[j][0]);
+  }
+}
+
 // kExact (fp32 outputs, and sums of more than kLongSum terms): the tensor cores'
 // accumulator drops the bits below its last place at every step (measured:
 // 4.4e-6 of the result over 4096 terms, against 6e-7 for fp32 additions), so a
@@ -703,7 +636,12 @@ constexpr int kLongSum = 1 << 18;
 // reach past the first term's end read into the second: rows of D that are not
 // stored, or terms that meet B's zeros.  (As a second product with the first
 // one's result for its residual: 16384 x 4096 x 128, dx and dW, 309 us; this way 114.)
-template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice>
+//
+// kGated: B is W's two halves of N rows each (p.N counts columns of h); a tile's
+// first BN / 2 columns are the gate's and the others the same columns of the
+// factor, so that each epilogue thread finds both in its row of TMEM and only h
+// (and z, if kept) leaves the chip.
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice, bool kGated>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ,
@@ -778,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, split, p);
+      const Unit t = unit_of<CG, kGated ? BN / 2 : BN>(u, split, p);
       const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + S::kRowsB * (int)rank;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) {
@@ -800,7 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_tile<CG>(sa + q * kSubA, &tmA, k, m0 + lower, fb);
           }
           uint8_t* sb = sa + kKB * kSubA + q * S::kSubB;
-          if constexpr (BT) {
+          if constexpr (kGated) {  // boxes of BN / 2 rows: the second CTA of a pair holds the factor's
+#pragma unroll
+            for (int g = 0; g < 2 / CG; ++g)
+              load_tile<CG>(sb + g * (BN / 2) * 128, &tmB, k, t.n0 + (CG == 2 ? (int)rank : g) * p.N, fb);
+          } else if constexpr (BT) {
 #pragma unroll
             for (int g = 0; g < S::kRowsB / 64; ++g) load_tile<CG>(sb + g * 8192, &tmB, n0 + 64 * g, k, fb);
           } else {
@@ -830,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, tphase[2] = {0u, 0u};
     bool ok = true;
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, split, p);
+      const Unit t = unit_of<CG, kGated ? BN / 2 : BN>(u, split, p);
       for (int kb0 = t.kb0; kb0 < t.kb1 && ok;) {
         const int kb1 = kExact ? min(t.kb1, kb0 + kExactBlocks) : t.kb1;
         if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
@@ -896,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (int u = worker; u < units && ok; u += workers) {
-      const Unit t = unit_of<CG, BN>(u, split, p);
+      const Unit t = unit_of<CG, kGated ? BN / 2 : BN>(u, split, p);
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew, n0 = t.n0 + half * (BN / 2);
       if constexpr (kSplit) {  // for the rows that this CTA will finish
         const int rows = rows_of_share(t.m0, p.M, p.splits), i = threadIdx.x - 128;
@@ -925,7 +867,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!kSplit && epi.wide) load_residual(epi, res, r0 + lane, n0 + 32 * c, p.M, p.N);
       };
       auto lanes_of = [&]() { return tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + half * (BN / 2)); };
-      if constexpr (kExact) {
+      if constexpr (kGated && !kSplit) {
+        if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
+          ok = false;
+          break;
+        }
+        tphase[acc] ^= 1u;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < BN / 128; ++c) {
+          const int col = half * (BN / 4) + 32 * c;
+          const uint32_t at = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN + col);
+          uint32_t g[32], v[32];
+          tmem_ld32(at, g);
+          tmem_ld32(at + BN / 2, v);
+          if (c == BN / 128 - 1) release();
+          finish_gated<BN == 256>(epi, bulk, &tmY, &tmZ, g, v, c, r0, t.n0 + col, p.M, p.N, lane);
+        }
+        acc ^= 1;
+      } else if constexpr (kExact) {
         uint32_t sum[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -989,11 +949,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if constexpr (kSplit) {
-    const Unit t = unit_of<CG, BN>(worker, split, p);
-    switch (p.splits) {
-      case 2: join_parts<2, BN>(p, epi, t, split, smem); break;
-      case 4: join_parts<4, BN>(p, epi, t, split, smem); break;
-      default: join_parts<8, BN>(p, epi, t, split, smem); break;
+    const Unit t = unit_of<CG, kGated ? BN / 2 : BN>(worker, split, p);
+    if constexpr (kGated) {
+      switch (p.splits) {
+        case 2: join_gated<2, BN>(p, epi, t, split, smem); break;
+        case 4: join_gated<4, BN>(p, epi, t, split, smem); break;
+        default: join_gated<8, BN>(p, epi, t, split, smem); break;
+      }
+    } else {
+      switch (p.splits) {
+        case 2: join_parts<2, BN>(p, epi, t, split, smem); break;
+        case 4: join_parts<4, BN>(p, epi, t, split, smem); break;
+        default: join_parts<8, BN>(p, epi, t, split, smem); break;
+      }
     }
     cluster_wait();  // nobody reads this CTA's part any more
   }
@@ -1293,6 +1261,19 @@ bool make_out_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t o
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// z [M][2][N] as the gated epilogue stores it: 32 rows x 32 columns of one half.
+bool make_z_map(CUtensorMap* map, const void* base, uint64_t N, uint64_t M) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {N, 2, M};
+  cuuint64_t strides[2] = {N * 2, N * 4};
+  cuuint32_t box[3] = {32u, 1u, 32u};
+  cuuint32_t estride[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D bf16 [outer][inner], rows ld elements apart, 128-byte swizzle.
 bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_rows) {
   auto fn = encode_fn();
@@ -1324,7 +1305,7 @@ constexpr int kPlanSms = 152;  // plans are made for a whole GB300
 // four parts of 128 x 128 (11.8; two 14.8, unsplit 20.2, wide 26.7), 1024^3 to
 // 128 x 64 (7.8 against 12.8 and 9.9), 64 x 1024 x 1024 to four parts of that (5.8;
 // unsplit 6.9).
-Plan plan_gemm(int M, int N, int K, int passes, bool exact) {
+Plan plan_gemm(int M, int N, int K, int passes, bool exact, int kinds = kKinds) {
   const double cost[kKinds] = {1.0, 0.70, 0.66}, base[kKinds] = {9.0, 8.0, 6.0};
   // clusters of 2, 4 and 8 CTAs that run at once (sixteen of eight did not: 2048 x
   // 4096 x 128 18.6 us, in four parts 10.2)
@@ -1332,7 +1313,7 @@ Plan plan_gemm(int M, int N, int K, int passes, bool exact) {
   Plan best = {};
   double best_t = 0;
   const int kblocks = (K + 127) / 128 * passes;
-  for (int k = exact ? 1 : 0; k < kKinds; ++k) {  // exact: its running sums need registers, so not the widest
+  for (int k = exact ? 1 : 0; k < kinds; ++k) {  // exact: its running sums need registers, so not the widest
     Plan q;
     q.kind = k;
     q.kblocks = kblocks;
@@ -1358,12 +1339,12 @@ Plan plan_gemm(int M, int N, int K, int passes, bool exact) {
   return best;
 }
 
-template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice>
+template <int CG, int BN, bool AT, bool BT, bool kExact, bool kSplit, bool kTwice, bool kGated = false>
 cudaError_t run_one(const CUtensorMap (&maps)[4], const GemmArgs& p, const DeviceInfo& di, cudaStream_t st) {
   typedef Shape<CG, BN> S;
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    return cudaFuncSetAttribute(gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice, kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   });
   if (err != cudaSuccess) return err;
   const long long units = (long long)p.tiles_m * p.tiles_n;
@@ -1384,7 +1365,7 @@ cudaError_t run_one(const CUtensorMap (&maps)[4], const GemmArgs& p, const Devic
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice>, maps[0], maps[1], maps[2], maps[3], p);
+  return cudaLaunchKernelEx(&cfg, gemm_kernel<CG, BN, AT, BT, kExact, kSplit, kTwice, kGated>, maps[0], maps[1], maps[2], maps[3], p);
 }
 
 template <int CG, int BN, bool AT, bool BT, bool kExact, bool kTwice = false>
@@ -1429,6 +1410,24 @@ cudaError_t product(const void* A, long long lda, const void* B, long long ldb, 
     case 1: return run_gemm<1, 128, AT, BT, false>(maps, p, di, st);
     default: return run_gemm<1, 64, AT, BT, false>(maps, p, di, st);
   }
+}
+
+// h [M,N] = act(A Bg^T) * (A Bu^T), B [2][N][K].
+cudaError_t gated_product(const void* A, long long lda, const void* B, long long ldb, int M, int N, int K, Epi epi,
+                          int32_t* status, const DeviceInfo& di, cudaStream_t st) {
+  const Plan q = plan_gemm(M, 2 * N, K, 1, false, 2);  // the two wider shapes: 32 columns of h a warp
+  CUtensorMap maps[4] = {};
+  epi.wide = 1;
+  epi.narrow = epi.z || q.kind != 0;
+  if (!make_map(&maps[0], A, K, M, lda, 128) || !make_map(&maps[1], B, K, 2 * (uint64_t)N, ldb, kKindBN[q.kind] / 2))
+    return cudaErrorInvalidValue;
+  if (q.splits == 1 && (!make_out_map(&maps[2], epi.out, N, M, false, epi.narrow) || (epi.z && !make_z_map(&maps[3], epi.z, N, M))))
+    return cudaErrorInvalidValue;
+  const long long limit = kWaitNs + 20000LL * q.per_split;
+  GemmArgs p = {M, N, K, q.tiles_m, q.tiles_n, q.splits, q.per_split, q.kblocks, q.kblocks, M, epi, status, limit};
+  if (q.kind == 0) return run_one<2, 256, false, false, false, false, false, true>(maps, p, di, st);
+  return q.splits > 1 ? run_one<1, 128, false, false, false, true, false, true>(maps, p, di, st)
+                      : run_one<1, 128, false, false, false, false, false, true>(maps, p, di, st);
 }
 
 template <bool kHigh>
@@ -1551,21 +1550,36 @@ cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cuda
   }
   const void* dz = own ? ws + q.dz : a.dy;
   const long long ld = own ? lddz : a.lddy;
+  return launch_products_bwd({dz, a.x, a.W, a.dx, a.dW, a.status, ld, a.ldx, a.ldw, a.s, a.K, a.N, a.dx_f32, a.dw_f32, own == 2},
+                             di, st);
+}
+
+cudaError_t launch_products_bwd(const ProductsBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {
   if (a.dx) {
     Epi e = {};
     e.out = a.dx;
     e.out_f32 = a.dx_f32;
-    cudaError_t err = product<false, true>(dz, ld, a.W, a.ldw, a.s, a.K, a.N, own == 2 && f32_dx, e, a.status, di, st);
+    cudaError_t err = product<false, true>(a.dz, a.lddz, a.W, a.ldw, a.s, a.K, a.N, a.two && a.dx_f32, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   if (a.dW) {
     Epi e = {};
     e.out = a.dW;
     e.out_f32 = a.dw_f32;
-    cudaError_t err = product<true, true>(dz, ld, a.x, a.ldx, a.N, a.K, a.s, own == 2 && f32_dw, e, a.status, di, st);
+    cudaError_t err = product<true, true>(a.dz, a.lddz, a.x, a.ldx, a.N, a.K, a.s, a.two && a.dw_f32, e, a.status, di, st);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
+}
+
+cudaError_t launch_gated(const GatedArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  Epi e = {};
+  e.out = a.h;
+  e.z = static_cast<bf16*>(a.z);
+  e.bias = a.bias;
+  e.act = a.act;
+  e.bias_f32 = a.bias_f32;
+  return gated_product(a.x, a.ldx, a.W, a.ldw, a.s, a.N, a.K, e, a.status, di, st);
 }
 
 }  // namespace moe

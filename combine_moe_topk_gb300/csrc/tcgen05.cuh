@@ -117,6 +117,75 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
+// Matrix descriptor of a tile in shared memory, 128-byte swizzle, base on 1024
+// bytes.  Rows of 128 bytes along the contracted axis: groups of 8 rows 1024
+// bytes apart.  Rows along the other axis (kMN): 8 steps of the contracted axis
+// are 1024 bytes, the next 64 elements of the other axis 8192 bytes on.
+template <bool kMN>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3ffffu) >> 4);
+  d |= (uint64_t)(kMN ? 8192 >> 4 : 1) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+// Descriptor step of one MMA (16 of the contracted axis), in 16-byte units.
+template <bool kMN>
+constexpr uint64_t kstep() { return kMN ? 2048 >> 4 : 32 >> 4; }
+
+template <int CG, int BN, bool AT, bool BT>
+__device__ __forceinline__ uint32_t instr_desc() {
+  uint32_t d = 0;
+  d |= 1u << 4;                             // fp32 accumulator
+  d |= 1u << 7;                             // A bf16
+  d |= 1u << 10;                            // B bf16
+  d |= (AT ? 1u : 0u) << 15;                // A's rows run along m
+  d |= (BT ? 1u : 0u) << 16;                // B's rows run along n
+  d |= (uint32_t)(BN >> 3) << 17;
+  d |= (uint32_t)((128 * CG) >> 4) << 24;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_2d(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(sdst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar)
+      : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void load_tile(void* sdst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
+  if constexpr (CG == 2) tma_load_2d_pair(sdst, map, x, y, mbar);
+  else tma_load_2d(sdst, map, x, y, mbar);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma(uint32_t dt, uint64_t ad, uint64_t bd, uint32_t idesc, int accumulate) {
+  if constexpr (CG == 2) {
+    mma_bf16_pair(dt, ad, bd, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(dt),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (CG == 2) {
+    mma_commit_pair(bar);
+  } else {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+  }
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   // a function-local static initialises once, thread-safe
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {

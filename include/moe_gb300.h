@@ -100,7 +100,14 @@ enum {
   MOE_KERNEL_BALANCE_BWD = 19,
   MOE_KERNEL_LINEAR = 20,
   MOE_KERNEL_LINEAR_BWD = 21,
-  MOE_KERNEL_COUNT = 22
+  MOE_KERNEL_GATED = 22,
+  MOE_KERNEL_GATED_BWD = 23,
+  MOE_KERNEL_GROUPED_GATED = 24,
+  MOE_KERNEL_GROUPED_GATED_BWD = 25,
+  MOE_KERNEL_GROUPED_GEMM_BWD = 26,
+  MOE_KERNEL_GRAD_NORM = 27,
+  MOE_KERNEL_GRAD_CLIP = 28,
+  MOE_KERNEL_COUNT = 29
 };
 
 /* Opaque layout handle [P1 "How"; P3 description].  Owned by the library:
@@ -581,6 +588,125 @@ size_t moe_linear_bwd_workspace_for(const moe_linear_bwd_desc* desc, int dx, int
 moe_status moe_linear_bwd(const moe_linear_bwd_desc* desc, const void* dy, const void* x, const void* W,
                           const void* z, void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
                           int32_t* device_status, void* stream);
+
+/* ---- gated experts: products, gradients, clipping -----------------------------
+ * The pages have no counterpart: these train and serve experts whose first
+ * product is gated.  W holds two matrices of N rows each, the gate's Wg first,
+ * then the factor's Wu:
+ *   z = [g | u] = [x Wg^T | x Wu^T] (+ bias),  h = act(g) * u,
+ * act one of MOE_ACT_* (NONE: a bilinear unit).  Operands, h and z are bf16; sums
+ * and the epilogue are fp32, h and z each rounded once.  K and N are multiples
+ * of 8, K at most 2^18 (the tensor cores' accumulator, see moe_linear).  Workspaces and
+ * device_status are as in moe_linear. */
+typedef struct {
+  int32_t s, K, N;        /* x [s,K], W [2N,K], h [s,N]                              */
+  int32_t act;            /* MOE_ACT_*                                               */
+  int32_t bias_dtype;     /* of bias                                                 */
+  int64_t ldx, ldw;       /* elements between rows, multiples of 8                   */
+} moe_gated_desc;
+
+/* h = act(x Wg^T + bias[:N]) * (x Wu^T + bias[N:]) in one kernel.  bias [2N] fp32 or
+ * bf16, nullable; z [s,2N], nullable: what the backward pass needs.  Any s >= 0; up
+ * to 16 rows stream W once.  Errors: MOE_ERR_INVALID_ARG, MOE_ERR_DTYPE,
+ * MOE_ERR_CUDA. */
+moe_status moe_gated_linear(const moe_gated_desc* desc, const void* x, const void* W, const void* bias, void* h, void* z,
+                            int32_t* device_status, void* stream);
+
+typedef struct {
+  int32_t s, K, N;
+  int32_t act;
+  int32_t dh_dtype;       /* MOE_F32 or MOE_BF16                                     */
+  int32_t dx_dtype;       /* of dx                                                   */
+  int32_t dw_dtype;       /* of dW                                                   */
+  int64_t lddh, ldx, ldw, ldz; /* multiples of 8                                     */
+} moe_gated_bwd_desc;
+
+/* Bytes of moe_gated_linear_bwd's workspace for a call that asks for these. */
+size_t moe_gated_linear_bwd_workspace(const moe_gated_bwd_desc* desc, int dx, int dW, int db);
+
+/* Backward of moe_gated_linear:
+ *   dz = [dh u act'(g) | dh act(g)];  dx = dz W;  dW = dz^T x;  db = sum_t dz.
+ * dh [s,N] fp32 or bf16, z [s,2N]; dx [s,K], dW [2N,K] fp32 or bf16, db f32 [2N], each
+ * nullable.  dz is rounded to bf16 for a bf16 result and taken in two bf16 terms
+ * for an fp32 one, as in moe_linear_bwd; db sums it in fp32 before that.  Fixed order of all sums.
+ * With s = 0, dW and db are zeroed. */
+moe_status moe_gated_linear_bwd(const moe_gated_bwd_desc* desc, const void* dh, const void* x, const void* W, const void* z,
+                                void* dx, void* dW, float* db, void* workspace, size_t workspace_bytes,
+                                int32_t* device_status, void* stream);
+
+/* The gated product of the experts over the dispatched rows: for every row r that
+ * a kept route to expert x owns,
+ *   H[r] = act(X[r] Wg[x]^T) * (X[r] Wu[x]^T).
+ * X [rows,K] (the output of moe_dispatch), W [e,2N,K], H [rows,N]; Z [rows,2N],
+ * nullable.  Rows no route owns are neither used nor written, whatever they hold.
+ * Any layout of the handle.  K at least 64.  Time-outs go to the handle's status
+ * word.  Errors as moe_grouped_gemm. */
+moe_status moe_grouped_gated(moe_handle h, int rows, int K, int N, int act, const void* X, const void* W, void* H, void* Z,
+                             void* stream);
+
+/* The same on the token rows x [s,K], gathered through the handle, without a
+ * dispatched buffer; same bits. */
+moe_status moe_dispatch_grouped_gated(moe_handle h, int s, int rows, int K, int N, int act, const void* x, const void* W,
+                                      void* H, void* Z, void* stream);
+
+/* Backward of moe_grouped_gemm (Y[r] = X[r] W[x]^T) on the same handle:
+ *   dX[r] = dY[r] W[x] for rows that a route owns (others are not written),
+ *   dW[x] = sum over the rows r of expert x of dY[r]^T X[r], 0 without rows.
+ * dY [rows,N], X and dX [rows,K], W and dW [e,N,K], bf16; dX and dW nullable.  fp32 sums
+ * in a fixed order, rounded once.  (Of an expert with more than 2^18 rows the
+ * accumulator may lose up to count / 16 units of 2^-24 of a sum of one sign.)  rows = 0: dW
+ * is zeroed.  Errors as moe_grouped_gemm. */
+moe_status moe_grouped_gemm_bwd(moe_handle h, int rows, int K, int N, const void* dY, const void* X, const void* W, void* dX,
+                                void* dW, void* stream);
+
+/* Bytes of moe_grouped_gated_bwd's workspace: dz. */
+size_t moe_grouped_gated_bwd_workspace(int rows, int N);
+
+/* Backward of moe_grouped_gated and of its gathering form (X is then the output of
+ * moe_dispatch, and dX goes through moe_dispatch_bwd):
+ *   dz[r] = [dH u act'(g) | dH act(g)][r], rounded to bf16;
+ *   dX[r] = dz[r] W[x];  dW[x] = sum over x's rows of dz[r]^T X[r].
+ * dH [rows,N], Z [rows,2N], X and dX [rows,K], W and dW [e,2N,K]; the rest as
+ * moe_grouped_gemm_bwd. */
+moe_status moe_grouped_gated_bwd(moe_handle h, int rows, int K, int N, int act, const void* dH, const void* X, const void* W,
+                                 const void* Z, void* dX, void* dW, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the gradients' global norm, and clipping -----------------------------------
+ * A list of tensors, checked once: device memory of the current device, fp32 or
+ * bf16, contiguous, aligned to their elements (16 bytes are not needed), any
+ * number of elements including none.  The list keeps the addresses, not the
+ * memory: it must be there while calls with the list run. */
+typedef struct {
+  void* data;
+  int64_t numel;
+  int32_t dtype; /* MOE_F32 or MOE_BF16 */
+} moe_tensor;
+typedef struct moe_tensor_list_s* moe_tensor_list;
+
+/* Errors: MOE_ERR_INVALID_ARG (a pointer, an alignment, sizes), MOE_ERR_DTYPE,
+ * MOE_ERR_OOM (host memory). */
+moe_status moe_tensor_list_create(const moe_tensor* tensors, int count, moe_tensor_list* out);
+moe_status moe_tensor_list_destroy(moe_tensor_list list);
+
+/* Bytes of workspace of the two calls below that compute a norm. */
+size_t moe_grad_norm_workspace(int count);
+
+/* norm[0] = sqrt(sum of g^2 over all tensors), f32 in device memory.  Squares are
+ * summed in fp32 within 32 elements and in 64 bits beyond, scaled where they
+ * would leave fp32's range; fixed order.  A NaN or infinity reaches the norm (which is
+ * infinite past fp32's range too) and sets MOE_DEV_NONFINITE in device_status (nullable).  An empty list: 0. */
+moe_status moe_grad_norm(moe_tensor_list grads, float* norm, void* workspace, size_t workspace_bytes, int32_t* device_status,
+                         void* stream);
+
+/* With coef = min(1, max_norm / (norm[0] + 1e-6)), every gradient times coef, rounded
+ * once, to the tensor of the same place in `out` (same sizes and types, no overlap; NULL: in
+ * place; then nothing is written where coef is 1).  norm is given, e.g. joined over ranks.  A norm that is not
+ * finite leaves the gradients unscaled (`out` gets copies).  max_norm >= 0. */
+moe_status moe_grad_clip(moe_tensor_list grads, moe_tensor_list out, const float* norm, float max_norm, void* stream);
+
+/* moe_grad_norm and moe_grad_clip in two kernels; norm[0] is written. */
+moe_status moe_clip_grad_norm(moe_tensor_list grads, moe_tensor_list out, float max_norm, float* norm, void* workspace,
+                              size_t workspace_bytes, int32_t* device_status, void* stream);
 
 /* Fill *info with the handle's sizes and device pointers (valid until the
  * handle is destroyed). */
