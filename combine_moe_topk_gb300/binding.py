@@ -1062,6 +1062,8 @@ class GradList:
     def __init__(self, tensors):
         self.tensors = tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
         self.device = None
+        # compared with another list's in one go
+        self.layout = repr([(tuple(t.shape), t.stride()) for t in tensors])
         spec = (Tensor * max(1, len(tensors)))()
         for i, t in enumerate(tensors):
             if t.layout != torch.strided or not _dense(t):
@@ -1114,43 +1116,50 @@ def _grads(grads) -> GradList:
 def _clip_lists(where: str, grads, out):
     g = _grads(grads)
     o = None if out is None else _grads(out)
-    if o is not None:
-        for a, b in zip(g.tensors, o.tensors):
-            if a.shape != b.shape or a.stride() != b.stride():
-                raise MoEError(1, where, "out must have the gradients' shapes and strides")
+    if o is not None and g.layout != o.layout:
+        raise MoEError(1, where, "out must have the gradients' shapes and strides")
     return g, o
 
 
-def _on(device: torch.device):
-    return torch.cuda.device(device)
+def _check_norm(where: str, norm: torch.Tensor):
+    if norm.shape != (1,) or norm.dtype != torch.float32:
+        raise MoEError(1, where, "norm must be float32 [1]")
+
+
+def _norm_call(where: str, g: GradList, norm, device_status, call):
+    """call(norm, workspace, its bytes, status, stream) on the list's device."""
+    if g.device is None:
+        raise RuntimeError("no CUDA device")
+    if g.device.type == "cuda" and g.device.index != torch.cuda.current_device():
+        with torch.cuda.device(g.device):
+            return _norm_call(where, g, norm, device_status, call)
+    new = _new_here if _strided is not None and not _modes() else \
+        lambda dtype, n: torch.empty(n, dtype=dtype, device=g.device)
+    if norm is None:
+        norm = new(torch.float32, 1)
+    else:
+        _check_norm(where, norm)
+    nbytes = lib().moe_grad_norm_workspace(len(g))
+    ws = new(torch.uint8, nbytes)
+    rc = call(_addr(norm), ws.data_ptr(), nbytes, _status_addr(device_status, where), _raw_stream(norm))
+    if rc:
+        _check(rc, where)
+    return norm
 
 
 def moe_grad_norm(grads, norm: torch.Tensor | None = None, device_status: torch.Tensor | None = None) -> torch.Tensor:
     """f32 [1]: the 2-norm of all elements of all tensors (a sequence or a
     GradList).  A NaN or an infinity reaches it (and device_status)."""
     g = _grads(grads)
-    L = lib()
-    with _on(g.device):
-        if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=g.device)
-        elif norm.shape != (1,) or norm.dtype != torch.float32:
-            raise MoEError(1, "moe_grad_norm", "norm must be float32 [1]")
-        nbytes = L.moe_grad_norm_workspace(len(g))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
-        rc = L.moe_grad_norm(g.raw, _addr(norm), _addr(ws), nbytes, _status_addr(device_status, "moe_grad_norm"),
-                             _raw_stream(norm))
-    if rc:
-        _check(rc, "moe_grad_norm")
-    return norm
+    return _norm_call("moe_grad_norm", g, norm, device_status, lambda *a: lib().moe_grad_norm(g.raw, *a))
 
 
 def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
     """Scale the gradients by min(1, max_norm / (norm + 1e-6)) in place, or into the tensors of `out`; norm f32 [1] on
     the device (joined over ranks, say).  A norm that is not finite leaves them unscaled."""
     g, o = _clip_lists("moe_grad_clip", grads, out)
-    if norm.shape != (1,) or norm.dtype != torch.float32:
-        raise MoEError(1, "moe_grad_clip", "norm must be float32 [1]")
-    with _on(g.device):
+    _check_norm("moe_grad_clip", norm)
+    with torch.cuda.device(g.device):
         rc = lib().moe_grad_clip(g.raw, None if o is None else o.raw, _addr(norm), max_norm, _raw_stream(norm))
     if rc:
         _check(rc, "moe_grad_clip")
@@ -1160,16 +1169,6 @@ def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | No
                        device_status: torch.Tensor | None = None) -> torch.Tensor:
     """moe_grad_norm and moe_grad_clip in two kernels; returns the norm before clipping, f32 [1]."""
     g, o = _clip_lists("moe_clip_grad_norm", grads, out)
-    L = lib()
-    with _on(g.device):
-        if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=g.device)
-        elif norm.shape != (1,) or norm.dtype != torch.float32:
-            raise MoEError(1, "moe_clip_grad_norm", "norm must be float32 [1]")
-        nbytes = L.moe_grad_norm_workspace(len(g))
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=g.device)
-        rc = L.moe_clip_grad_norm(g.raw, None if o is None else o.raw, max_norm, _addr(norm), _addr(ws), nbytes,
-                                  _status_addr(device_status, "moe_clip_grad_norm"), _raw_stream(norm))
-    if rc:
-        _check(rc, "moe_clip_grad_norm")
-    return norm
+    ro = None if o is None else o.raw
+    return _norm_call("moe_clip_grad_norm", g, norm, device_status,
+                      lambda *a: lib().moe_clip_grad_norm(g.raw, ro, max_norm, *a))

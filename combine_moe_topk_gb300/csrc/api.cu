@@ -1403,7 +1403,7 @@ moe_status moe_tensor_list_create(const moe_tensor* tensors, int count, moe_tens
     if (reinterpret_cast<uintptr_t>(t.data) % (t.dtype == MOE_F32 ? 4 : 2))
       return fail(MOE_ERR_INVALID_ARG, name + " is not aligned to its elements");
     chunks += moe::grad_chunks({t.data, t.numel, t.dtype == MOE_F32});
-    if (chunks > 2147483647LL) return fail(MOE_ERR_INVALID_ARG, "the list holds too many elements");
+    if (chunks > 1LL << 30) return fail(MOE_ERR_INVALID_ARG, "the list holds too many elements");
   }
   int dev = 0;
   if (count > 0) MOE_TRY(current_device(&dev));
