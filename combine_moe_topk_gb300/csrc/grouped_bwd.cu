@@ -49,7 +49,11 @@ constexpr int kStageK = 64 * kKB;
 constexpr int kSub = 128 * 64 * 2;        // 16 KB: 128 rows (or columns) x 64
 constexpr int kStage = kKB * 2 * kSub;    // A and B
 constexpr int kStages = 3;
-constexpr int kSmem = kStages * kStage + kEpiWarps * kRowStage + 1024;
+// a warp's staging tile: 32 rows x 64 columns (dW), 32 x 32 (dX)
+template <bool kWeights>
+constexpr int kPiece = kWeights ? 32 * 128 : kRowStage;
+template <bool kWeights>
+constexpr int kSmem = kStages * kStage + kEpiWarps * kPiece<kWeights> + 1024;
 constexpr int kTile = 256;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 256;
@@ -71,16 +75,26 @@ struct Unit {
   int count;      // rows of the expert
 };
 
+// The r-th unit of a pair.  dW's units are in order of falling length (their
+// experts' rows), and every other round of them is dealt out in reverse, so that
+// skewed routing leaves no pair with much more to do than another.
 template <bool kWeights>
-__device__ __forceinline__ Unit unit_of(int u, const Args& p, const int* s_blk, const int* s_cnt) {
+__device__ __forceinline__ int pick(int r, int pair, int pairs) {
+  return r * pairs + (kWeights && (r & 1) ? pairs - 1 - pair : pair);
+}
+
+// order: dW's experts by falling count; dX: blk, row blocks of the experts before x.
+template <bool kWeights>
+__device__ __forceinline__ Unit unit_of(int u, const Args& p, const int* s_blk, const uint8_t* order, const int* s_cnt) {
   const int tn = (p.cols + kTile - 1) / kTile;
   Unit t;
   if constexpr (kWeights) {
     // an expert's tiles one after another, in bands of 8 rows of tiles, so that
     // those in flight share their operands in L2
     const int tm = (p.M + kTile - 1) / kTile;
-    t.x = u / (tm * tn);
-    const int r = u - t.x * tm * tn, band = r / (8 * tn), rows = min(8, tm - band * 8), q = r - band * 8 * tn, n = q / rows;
+    const int place = u / (tm * tn);
+    t.x = order[place];
+    const int r = u - place * tm * tn, band = r / (8 * tn), rows = min(8, tm - band * 8), q = r - band * 8 * tn, n = q / rows;
     t.m0 = (band * 8 + q - n * rows) * kTile;
     t.n0 = n * kTile;
     t.count = s_cnt[t.x];
@@ -121,13 +135,14 @@ __device__ __forceinline__ bool is_cut(const Unit& t, int kb) { return kb == t.b
 template <bool kWeights>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_bwd_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ Args p) {
+                       const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
   // full: the copies of both CTAs (two arrivals of the first CTA's producer, or one
   // of each CTA's zeroing warp); tail: this CTA's copies of a cut block
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], tail[kStages], tfull[2], tempty[2], drain;
   __shared__ uint32_t tmem_base;
-  __shared__ int s_off[kMaxE + 1], s_cnt[kMaxE], s_blk[kMaxE + 1];
+  __shared__ int s_cnt[kMaxE], s_off[kWeights ? 1 : kMaxE], s_blk[kWeights ? 1 : kMaxE + 1];
+  __shared__ uint8_t s_order[kWeights ? kMaxE : 1];
   __shared__ int s_err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -157,11 +172,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dependency_wait();  // from here on memory of earlier kernels is read
   for (int x = threadIdx.x; x < p.e; x += blockDim.x) {
-    s_off[x] = ld_plain(p.offsets + x);
+    if (!kWeights) s_off[x] = ld_plain(p.offsets + x);
     s_cnt[x] = ld_plain(p.counts + x);
   }
   __syncthreads();
-  if (!kWeights && warp == 3) prefix_blocks(s_cnt, s_blk, p.e, kTile, lane);
+  if constexpr (kWeights) {
+    for (int x = threadIdx.x; x < p.e; x += blockDim.x) {
+      const int n = s_cnt[x];
+      int place = 0;
+      for (int y = 0; y < p.e; ++y) place += s_cnt[y] > n || (s_cnt[y] == n && y < x);
+      s_order[place] = (uint8_t)x;
+    }
+  } else if (warp == 3) {
+    prefix_blocks(s_cnt, s_blk, p.e, kTile, lane);
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist before any remote signal
@@ -176,9 +200,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- TMA producer ------------------------------------------------------
     Ring r;
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of<kWeights>(u, p, s_blk, s_cnt);
-      const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + 128 * (int)rank, first = s_off[t.x];
+    for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
+      const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
+      const int m0 = t.m0 + 128 * (int)rank, n0 = t.n0 + 128 * (int)rank;
+      const int first = kWeights ? ld_plain(p.offsets + t.x) : s_off[t.x];
       for (int kb = 0; kb < t.blocks; ++kb) {
         if (!mbar_wait_limited(&empty[r.stage], r.phase ^ 1u, p.timeout_ns)) {
           ok = false;
@@ -229,8 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of<kWeights>(u, p, s_blk, s_cnt);
+    for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
+      const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
       if (t.blocks == 0) continue;
       if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
         ok = false;
@@ -274,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int pos = 0;  // ring position of the unit's first block
     uint32_t phases = 0;  // of each stage's tail barrier
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of<kWeights>(u, p, s_blk, s_cnt);
+    for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
+      const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
       if (t.blocks == 0) continue;
       const int stage = (pos + t.blocks - 1) % kStages;
       pos = (pos + t.blocks) % kStages;
@@ -300,16 +325,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ---- epilogue --------------------------------------------------------------
     const int ew = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* stage_buf = smem + kStages * kStage + (warp - 4) * kRowStage;
+    uint8_t* stage_buf = smem + kStages * kStage + (warp - 4) * kPiece<kWeights>;
     const uint32_t te[2] = {mapa_shared(smem_addr(&tempty[0]), 0), mapa_shared(smem_addr(&tempty[1]), 0)};
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Unit t = unit_of<kWeights>(u, p, s_blk, s_cnt);
+    for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
+      const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew;
       const int rows = (kWeights ? p.M : t.count) - r0;
-      const long long first = kWeights ? (long long)t.x * p.M + r0 : (long long)s_off[t.x] + r0;
       const bool zeros = t.blocks == 0;
       if (!zeros) {
         if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
@@ -319,23 +343,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         tphase[acc] ^= 1u;
         tc_fence_after();
       }
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int col = t.n0 + 128 * half + 32 * c;
-        if (rows <= 0 || col >= p.cols) break;  // the whole warp
-        uint32_t w[16];
+      const uint32_t lanes = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * kTile + 128 * half);
+      auto words = [&](int c, uint32_t (&w)[16]) {  // 32 columns of this lane's row
         if (zeros) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = 0u;
-        } else {
-          uint32_t v[32];
-          float f[32];
-          tmem_ld32(tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * kTile + 128 * half + 32 * c), v);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-          pack_bf16(f, w);
+          return;
         }
-        store_rows(stage_buf, w, p.out + first * p.cols + col, p.cols, rows, p.cols - col, lane);
+        uint32_t v[32];
+        float f[32];
+        tmem_ld32(lanes + (uint32_t)(32 * c), v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        pack_bf16(f, w);
+      };
+      if constexpr (kWeights) {
+        // 64 columns at a time through the staging tile, out by TMA, clipped at the
+        // expert's edge (16-byte stores by lanes: 128 experts of 2816 x 704 and 174
+        // rows, where little else is done, 217 us)
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int col = t.n0 + 128 * half + 64 * c;
+          if (rows <= 0 || col >= p.cols) break;  // the whole warp
+          uint32_t w[2][16];
+          words(2 * c, w[0]);
+          words(2 * c + 1, w[1]);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4*>(stage_buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(w[q >> 2][4 * (q & 3)], w[q >> 2][4 * (q & 3) + 1], w[q >> 2][4 * (q & 3) + 2], w[q >> 2][4 * (q & 3) + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmOut, stage_buf, col, r0, t.x);
+            bulk_commit();
+          }
+        }
+      } else {
+        const long long first = (long long)s_off[t.x] + r0;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col = t.n0 + 128 * half + 32 * c;
+          if (rows <= 0 || col >= p.cols) break;  // the whole warp
+          uint32_t w[16];
+          words(c, w);
+          store_rows(stage_buf, w, p.out + first * p.cols + col, p.cols, rows, p.cols - col, lane);
+        }
       }
       if (zeros) continue;
       tc_fence_before();
@@ -346,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       acc ^= 1;
     }
+    if (kWeights && lane == 0) bulk_wait_all();  // the stores have read the staging tile and are written
     if (!ok && lane == 0) atomicOr(&s_err, 1);
   }
 
@@ -377,13 +433,13 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 [e][N][K]; boxes of 64 x 64 of one expert.
-bool make_weight_map(CUtensorMap* map, const void* base, uint64_t K, uint64_t N, uint64_t e) {
+// bf16 [e][N][K]; boxes of 64 columns x rows of one expert.
+bool make_weight_map(CUtensorMap* map, const void* base, uint64_t K, uint64_t N, uint64_t e, uint32_t rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {K, N, e};
   cuuint64_t strides[2] = {K * 2, K * N * 2};
-  cuuint32_t box[3] = {64, 64, 1};
+  cuuint32_t box[3] = {64, rows, 1};
   cuuint32_t estride[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estride,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -391,11 +447,11 @@ bool make_weight_map(CUtensorMap* map, const void* base, uint64_t K, uint64_t N,
 }
 
 template <bool kWeights>
-cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, const Args& p, long long units, const DeviceInfo& di,
+cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& out, const Args& p, long long units, const DeviceInfo& di,
                 cudaStream_t st) {
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(grouped_bwd_kernel<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return cudaFuncSetAttribute(grouped_bwd_kernel<kWeights>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<kWeights>);
   });
   if (err != cudaSuccess) return err;
   long long pairs = di.sms / 2;
@@ -404,7 +460,7 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, const Args& p, lon
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = kSmem<kWeights>;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -415,7 +471,7 @@ cudaError_t run(const CUtensorMap& ma, const CUtensorMap& mb, const Args& p, lon
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_bwd_kernel<kWeights>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, grouped_bwd_kernel<kWeights>, ma, mb, out, p);
 }
 
 }  // namespace
@@ -426,16 +482,18 @@ cudaError_t launch_grouped_bwd(const int32_t* offsets, const int32_t* counts, in
   const long long tn = (K + kTile - 1) / kTile;
   CUtensorMap ma, mb;
   if (dX) {
-    if (!make_map(&ma, dY, N, rows, 128) || !make_weight_map(&mb, W, K, N, e)) return cudaErrorInvalidValue;
+    if (!make_map(&ma, dY, N, rows, 128) || !make_weight_map(&mb, W, K, N, e, 64)) return cudaErrorInvalidValue;
     // the longest wait is the epilogue's, for a whole contraction: under 1 us for 128 of it when all is well
     const Args p = {offsets, counts, e, N, K, static_cast<bf16*>(dX), status, kWaitNs + 20000LL * (N / kStageK)};
-    cudaError_t err = run<false>(ma, mb, p, (((long long)rows + kTile - 1) / kTile + e) * tn, di, st);
+    cudaError_t err = run<false>(ma, mb, ma, p, (((long long)rows + kTile - 1) / kTile + e) * tn, di, st);
     if (err != cudaSuccess) return err;
   }
   if (dW) {
-    if (!make_map(&ma, dY, N, rows, 64) || !make_map(&mb, X, K, rows, 64)) return cudaErrorInvalidValue;
+    CUtensorMap out;
+    if (!make_map(&ma, dY, N, rows, 64) || !make_map(&mb, X, K, rows, 64) || !make_weight_map(&out, dW, K, N, e, 32))
+      return cudaErrorInvalidValue;
     const Args p = {offsets, counts, e, N, K, static_cast<bf16*>(dW), status, kWaitNs + 20000LL * (rows / kStageK)};
-    cudaError_t err = run<true>(ma, mb, p, e * ((long long)(N + kTile - 1) / kTile) * tn, di, st);
+    cudaError_t err = run<true>(ma, mb, out, p, e * ((long long)(N + kTile - 1) / kTile) * tn, di, st);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;

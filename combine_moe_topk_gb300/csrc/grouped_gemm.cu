@@ -177,23 +177,25 @@ __device__ __forceinline__ void store_gated(uint32_t tcol, int ew, int half, int
   }
 }
 
-// Unit u -> expert x, first row r0 and owned rows of its 128-row block, and
-// the column tile n0 (width columns a tile).  s_blk[x] = blocks of the experts before x.
+// Unit u -> expert x, the row block i of its segment and the column tile n0.
+// blk[x] = row blocks of the experts before x.  An expert's units go in bands of
+// kBand row blocks, the block fastest, so that the pairs that run at the same time
+// share columns of W and rows of A in L2.  Gated, bands of 8: 16384 rows of 8
+// experts, 4096 x 4096, 625 us (671 with 1).  The plain product keeps bands of 1, one
+// block's column tiles one after another: bands of 8 made no difference but to the
+// fused form on 131072 skewed rows, 4096 x 4096 (2780 us, 2875 with 8).
 struct Unit {
-  int x, r0, nvalid, n0;
+  int x, i, n0;
 };
 
-__device__ __forceinline__ Unit decode_unit(int u, int ntn, const int* s_blk, const int* s_off,
-                                            const int* s_cnt, int e, int width) {
-  const int b = u / ntn;
-  const int lo = expert_of(b, s_blk, e);
+template <int kBand>
+__device__ __forceinline__ Unit decode_unit(int u, int ntn, const int* blk, int e, int width) {
   Unit t;
-  const int i = b - s_blk[lo];
-  t.x = lo;
-  t.r0 = s_off[lo] + BM * i;
-  const int left = s_cnt[lo] - BM * i;
-  t.nvalid = left < BM ? left : BM;
-  t.n0 = (u - b * ntn) * width;
+  t.x = expert_of(u / ntn, blk, e);
+  const int r = u - blk[t.x] * ntn, band = r / (kBand * ntn), first = band * kBand;
+  const int rows = min(kBand, blk[t.x + 1] - blk[t.x] - first), q = r - first * ntn, n = q / rows;
+  t.i = first + q - n * rows;
+  t.n0 = n * width;
   return t;
 }
 
@@ -331,9 +333,8 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);  // rows in units of BM2 below
-      const int b = u / ntn;
-      const int r0 = s_off[t.x] + BM2 * (b - s_blk[t.x]) + BM * (int)rank;
+      const Unit t = decode_unit<kGated ? 8 : 1>(u, ntn, s_blk, p.e, kWidth);
+      const int r0 = s_off[t.x] + BM2 * t.i + BM * (int)rank;
       for (int kb = 0; kb < kblocks; ++kb) {
         if (!mbar_wait_limited(&empty[stage], phase ^ 1u, p.timeout_ns)) {
           ok = false;
@@ -382,10 +383,9 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
     bool ok = true;
     // token of each of this lane's kGatherRows / 4 rows in unit u; -1 for rows no route owns
     auto unit_tokens = [&](int u, int* tok) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);
-      const int i = u / ntn - s_blk[t.x];
-      const int r0 = s_off[t.x] + BM2 * i + BM * (int)rank;
-      const int left = s_cnt[t.x] - BM2 * i - BM * (int)rank;
+      const Unit t = decode_unit<kGated ? 8 : 1>(u, ntn, s_blk, p.e, kWidth);
+      const int r0 = s_off[t.x] + BM2 * t.i + BM * (int)rank;
+      const int left = s_cnt[t.x] - BM2 * t.i - BM * (int)rank;
 #pragma unroll
       for (int j = 0; j < kGatherRows / 4; ++j) {
         const int rr = kGatherRows * gw + 4 * j + (lane >> 3);
@@ -520,11 +520,9 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
     for (int u = pair; u < nunits && ok; u += npairs) {
-      const Unit t = decode_unit(u, ntn, s_blk, s_off, s_cnt, p.e, kWidth);
-      const int b = u / ntn;
-      const int i = b - s_blk[t.x];
-      const int r0 = s_off[t.x] + BM2 * i + BM * (int)rank;
-      const int left = s_cnt[t.x] - BM2 * i - BM * (int)rank;
+      const Unit t = decode_unit<kGated ? 8 : 1>(u, ntn, s_blk, p.e, kWidth);
+      const int r0 = s_off[t.x] + BM2 * t.i + BM * (int)rank;
+      const int left = s_cnt[t.x] - BM2 * t.i - BM * (int)rank;
       const int nvalid = left < 0 ? 0 : (left < BM ? left : BM);
       // every lane waits (and acquires) itself; the warp leaves together
       if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
@@ -649,9 +647,20 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
   return launch_pair<true>(mb, mb, p, di, st);  // A is gathered by threads: no A map
 }
 
+// Whether an expert product streams the weights through warp-level MMA, 16 rows at a
+// time (few_gated_kernel), or goes by tiles of 256 rows.  The host knows the rows of
+// all experts together.  Measured, tiles / streamed: 64 experts of 2048 x 1408, 1.5
+// rows an expert 109.5 / 94.1 us, 6 134.7 / 129.1, 12 135.3 / 145.3; 8 experts of
+// 4096 x 4096, 4 rows 104.9 / 82.8, 8 104.9 / 88.4, 16 105.7 / 130.5; 128 experts of
+// 4096 x 512, 8 rows 183.9 / 177.3, 16 185.2 / 255.7.  (Uneven routing adds at most a
+// pass for every 16 rows.)
+static bool few_rows(int rows, int e) { return rows <= kFewRows || rows <= 8LL * e; }
+
 cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, int act,
                                  const void* X, const void* W, void* H, void* Z, int32_t* status, const DeviceInfo& di,
                                  cudaStream_t st) {
+  if (few_rows(rows, e))
+    return launch_few_grouped(offsets, counts, nullptr, e, rows, 0, K, N, act, X, W, H, Z, status, di, st);
   CUtensorMap ma, mb;
   if (!make_map(&ma, X, (uint64_t)K, (uint64_t)rows, BM) ||
       !make_map(&mb, W, (uint64_t)K, 2 * (uint64_t)e * (uint64_t)N, BN / 2))
@@ -665,6 +674,8 @@ cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, 
 cudaError_t launch_dispatch_gated(const int32_t* offsets, const int32_t* counts, const int32_t* inv_row, int e, int rows,
                                   int s, int K, int N, int act, const void* x, const void* W, void* H, void* Z,
                                   int32_t* status, const DeviceInfo& di, cudaStream_t st) {
+  if (few_rows(rows, e))
+    return launch_few_grouped(offsets, counts, inv_row, e, rows, s, K, N, act, x, W, H, Z, status, di, st);
   CUtensorMap mb;
   GemmParams p = params(offsets, counts, e, rows, K, N, H, status);
   p.x = static_cast<const __nv_bfloat16*>(x);

@@ -237,6 +237,12 @@ struct GatedArgs {
   int s, K, N, act, bias_f32;
 };
 cudaError_t launch_gated(const GatedArgs& a, const DeviceInfo& di, cudaStream_t st);
+constexpr int kFewRows = 16;  // up to so many rows the products stream W through warp-level MMA
+cudaError_t launch_few_gated(const GatedArgs& a, const DeviceInfo& di, cudaStream_t st);
+// The same for few rows an expert; inv_row NULL: x is the dispatched rows, else s token rows.
+cudaError_t launch_few_grouped(const int32_t* offsets, const int32_t* counts, const int32_t* inv_row, int e, int rows, int s,
+                               int K, int N, int act, const void* x, const void* W, void* H, void* Z, int32_t* status,
+                               const DeviceInfo& di, cudaStream_t st);
 
 struct GatedBwdArgs {
   const void *dh, *x, *W, *z;

@@ -170,13 +170,6 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(smem_addr(src))
-               : "memory");
-}
-
 __device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* src, int x, int y, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
@@ -978,15 +971,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- few rows -------------------------------------------------------------------
 
-constexpr int kFewRows = 16;
-
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 struct FewArgs {
   const bf16* x;
   const bf16* W;
@@ -1573,6 +1557,7 @@ cudaError_t launch_products_bwd(const ProductsBwdArgs& a, const DeviceInfo& di, 
 }
 
 cudaError_t launch_gated(const GatedArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  if (a.s <= kFewRows) return launch_few_gated(a, di, st);
   Epi e = {};
   e.out = a.h;
   e.z = static_cast<bf16*>(a.z);
