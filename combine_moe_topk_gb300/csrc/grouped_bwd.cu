@@ -210,13 +210,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         uint32_t fb;
+        // the second half of a last block of at most 64 rows is not needed
+        const bool both = !kWeights || t.count - kb * kStageK > 64;
         if (kWeights && is_cut(t, kb)) {
           fb = smem_addr(&tail[r.stage]);
-          mbar_arrive_expect_tx(&tail[r.stage], kStage);
+          mbar_arrive_expect_tx(&tail[r.stage], both ? kStage : kStage / 2);
         } else {
           fb = mapa_shared(smem_addr(&full[r.stage]), 0);
           if (rank == 0) {
-            mbar_arrive_expect_tx(&full[r.stage], 2 * kStage);
+            mbar_arrive_expect_tx(&full[r.stage], both ? 2 * kStage : kStage);
             mbar_arrive(&full[r.stage]);
           }
         }
@@ -224,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < kKB; ++q) {
           const int k = kb * kStageK + 64 * q;
+          if (q == 1 && !both) break;
           uint8_t* sb = sa + (kKB + q) * kSub;
           if constexpr (kWeights) {
 #pragma unroll
@@ -330,6 +333,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t tphase[2] = {0u, 0u};
     bool ok = true;
+    auto release = [&]() {  // this warp's reads of the accumulator are done
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_accumulator(te[acc]);
+      }
+    };
     for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
       const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew;
@@ -360,20 +371,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kWeights) {
         // 64 columns at a time through the staging tile, out by TMA, clipped at the
         // expert's edge (16-byte stores by lanes: 128 experts of 2816 x 704 and 174
-        // rows, where little else is done, 217 us)
-#pragma unroll 1
+        // rows, where little else is done, 217 us); the accumulator goes back as soon
+        // as it is read
+        uint32_t w[4][16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) words(c, w[c]);
+        if (!zeros) release();
+#pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = t.n0 + 128 * half + 64 * c;
           if (rows <= 0 || col >= p.cols) break;  // the whole warp
-          uint32_t w[2][16];
-          words(2 * c, w[0]);
-          words(2 * c + 1, w[1]);
           if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4*>(stage_buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-                make_uint4(w[q >> 2][4 * (q & 3)], w[q >> 2][4 * (q & 3) + 1], w[q >> 2][4 * (q & 3) + 2], w[q >> 2][4 * (q & 3) + 3]);
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t* v = w[2 * c + (q >> 2)] + 4 * (q & 3);
+            *reinterpret_cast<uint4*>(stage_buf + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -391,15 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           words(c, w);
           store_rows(stage_buf, w, p.out + first * p.cols + col, p.cols, rows, p.cols - col, lane);
         }
+        if (!zeros) release();
       }
-      if (zeros) continue;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_cluster(te[acc]);
-      }
-      acc ^= 1;
+      if (!zeros) acc ^= 1;
     }
     if (kWeights && lane == 0) bulk_wait_all();  // the stores have read the staging tile and are written
     if (!ok && lane == 0) atomicOr(&s_err, 1);

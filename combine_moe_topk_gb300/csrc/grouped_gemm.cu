@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
       __syncwarp();  // every lane's TMEM reads are done
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_cluster(acc ? te1 : te0);
+        else mbar_arrive_accumulator(acc ? te1 : te0);
       }
       acc ^= 1;
     }

@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         if (CG == 1 || rank == 0) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_cluster(te[acc]);
+        else mbar_arrive_accumulator(te[acc]);
       }
     };
     for (int u = worker; u < units && ok; u += workers) {

@@ -201,6 +201,15 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   }
 }
 
+// The same for an epilogue that hands an accumulator back to the MMA's CTA: what must
+// be over are its tcgen05.ld, and tcgen05.wait::ld has seen to that.  So release
+// stays at the CTA's scope: a release at cluster scope also waits for the warp's
+// stores to be seen there, which cost more than a microsecond a tile (dW of 128
+// experts, 2816 x 768 from 128 rows: 167 -> 126 us).
+__device__ __forceinline__ void mbar_arrive_accumulator(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   // a function-local static initialises once, thread-safe
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
