@@ -1,8 +1,8 @@
 """Autograd wrappers and the activation-checkpoint handle recorder.
 
-Gate, dispatch and combine on a layout handle, and the operators around
-them: layer norm, dense products with their epilogue, the balance loss
-(``block.py`` strings all of them together).
+Gate, dispatch, combine and the experts' products on a layout handle, and the
+operators around them: layer norm, dense and gated products, the balance
+loss, gradient clipping (``block.py`` strings all of them together).
 
 DeepSpeed #8213 "Add an opt-in DeepEP transport for the AutoEP expert
 all-to-all", description: the backward of a combine is a dispatch and the
@@ -247,6 +247,99 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, a
     """y [s, N] = act(x W^T + bias) + residual, bf16 (or fp32) out."""
     return LinearFn.apply(_strided(x, 8), _strided(W, 8), _rows(bias), _strided(residual), act, out_dtype,
                           torch.is_grad_enabled())
+
+
+class GatedLinearFn(torch.autograd.Function):
+    """h = act(x Wg^T + bg) * (x Wu^T + bu); z, both projections, is kept where a gradient can be asked for."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, W: torch.Tensor, bias, act: str, grad: bool):
+        save_z = grad and any(ctx.needs_input_grad[:3])
+        out = B.moe_gated_linear(x, W, bias, act, save_z=save_z, device_status=_status(x))
+        h, z = out if save_z else (out, None)
+        ctx.save_for_backward(x, W, z)
+        ctx.act = act
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return h
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dh: torch.Tensor):
+        x, W, z = ctx.saved_tensors
+        dx, dW, db = B.moe_gated_linear_bwd(_strided(dh, 8), x, W, z, ctx.act, *ctx.needs_input_grad[:3],
+                                            device_status=_status(x))
+        return dx, dW, db if db is None else db.to(ctx.bias_dtype), None, None
+
+
+def gated_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: str = "silu") -> torch.Tensor:
+    """h bf16 [s, N] of x [s, K] and W [2N, K], the gate's rows first (bias [2N])."""
+    return GatedLinearFn.apply(_strided(x, 8), _strided(W, 8), _rows(bias), act, torch.is_grad_enabled())
+
+
+class GroupedGemmFn(torch.autograd.Function):
+    """Y[r] = X[r] W[x]^T over the experts' row segments of a handle."""
+
+    @staticmethod
+    def forward(ctx, X: torch.Tensor, W: torch.Tensor, handle: B.Handle):
+        ctx.handle = handle
+        ctx.save_for_backward(X, W)
+        return B.moe_grouped_gemm(handle, X, W)
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dY: torch.Tensor):
+        X, W = ctx.saved_tensors
+        need_x, need_w, _ = ctx.needs_input_grad
+        dX, dW = B.moe_grouped_gemm_bwd(ctx.handle, _rows(dY), X, W, need_x, need_w)
+        return dX, dW, None
+
+
+def grouped_gemm(X: torch.Tensor, W: torch.Tensor, handle: B.Handle) -> torch.Tensor:
+    """Y bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, N, K]."""
+    return GroupedGemmFn.apply(_rows(X), _rows(W), handle)
+
+
+class GroupedGatedFn(torch.autograd.Function):
+    """H[r] = act(X[r] Wg[x]^T) * (X[r] Wu[x]^T) over the experts' row segments.  gather: from the token rows x, without a
+    dispatched buffer; the backward pass then dispatches them again."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str, gather: bool, grad: bool):
+        save_z = grad and any(ctx.needs_input_grad[:2])
+        call = B.moe_dispatch_grouped_gated if gather else B.moe_grouped_gated
+        out = call(handle, x, W, act, save_z=save_z)
+        H, Z = out if save_z else (out, None)
+        ctx.save_for_backward(x, W, Z)
+        ctx.handle, ctx.act, ctx.gather = handle, act, gather
+        return H
+
+    @staticmethod
+    @first_order
+    def backward(ctx, dH: torch.Tensor):
+        x, W, Z = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad[:2]
+        X = B.moe_dispatch(ctx.handle, x) if ctx.gather else x
+        dX, dW = B.moe_grouped_gated_bwd(ctx.handle, _rows(dH), X, W, Z, ctx.act, need_x, need_w)
+        if ctx.gather and need_x:
+            dX = B.moe_dispatch_bwd(ctx.handle, dX)
+        return dX, dW, None, None, None, None
+
+
+def grouped_gated(X: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str = "silu") -> torch.Tensor:
+    """H bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, 2N, K], each expert's gate rows first."""
+    return GroupedGatedFn.apply(_rows(X), _rows(W), handle, act, False, torch.is_grad_enabled())
+
+
+def dispatch_grouped_gated(x: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str = "silu") -> torch.Tensor:
+    """The same on the token rows x [s, K]: as grouped_gated(dispatch(x)), whose buffer is neither written nor kept."""
+    return GroupedGatedFn.apply(_rows(x), _rows(W), handle, act, True, torch.is_grad_enabled())
+
+
+def clip_grad_norm(parameters, max_norm: float) -> torch.Tensor:
+    """Scale the parameters' gradients in place so that their common 2-norm is at most max_norm; returns the norm before
+    that, f32 [1] on the device.  A norm that is not finite leaves them as they are and is reported by ``status``."""
+    grads = [p.grad for p in ([parameters] if isinstance(parameters, torch.Tensor) else parameters) if p.grad is not None]
+    return B.moe_clip_grad_norm(grads, max_norm, device_status=_status(grads[0]) if grads else None)
 
 
 class BalanceLossFn(torch.autograd.Function):

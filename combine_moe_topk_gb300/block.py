@@ -1,4 +1,6 @@
-"""A trainable mixture-of-experts block from the library's calls:
+"""Trainable mixture-of-experts blocks from the library's calls.
+
+MoEBlock, experts of two dense products in capacity slots:
 
     h      = layernorm(x)
     logits = h Wr^T                               (fp32, the router's projection)
@@ -9,12 +11,19 @@
 A capacity layout puts expert j's rows at [j c, (j + 1) c), known on the host,
 so each expert's two products are calls of ``linear`` on its slice.
 
-``python -m combine_moe_topk_gb300.block`` trains it for some steps on a
-synthetic target (needs a GPU).
+GatedMoEBlock, gated experts without capacity, each step of theirs one call
+over all of them:
+
+    X = dispatch(h);  H = act(X Wg^T) * (X Wu^T);  Y = H Wd^T   (each expert's own W, over its rows)
+    y = (act(h Sg^T) * (h Su^T)) Sd^T + x + combine(Y, g)       (the shared expert, gated too)
+
+``python -m combine_moe_topk_gb300.block [gated]`` trains one for some steps
+on a synthetic target (needs a GPU).
 """
 from __future__ import annotations
 
 import math
+import sys
 
 import torch
 
@@ -72,10 +81,46 @@ class MoEBlock(torch.nn.Module):
         return y, self.weights[0] * loss[0] + self.weights[1] * loss[1], counts
 
 
-def main(steps: int = 20):
+class GatedMoEBlock(torch.nn.Module):
+    """x bf16 [s, m] -> (y bf16 [s, m], auxiliary loss, counts i32 [num_seqs, e]); no route is dropped.
+    gather: the experts' first product takes the token rows itself (less memory, one more dispatch backward)."""
+
+    def __init__(self, m: int, e: int, k: int, d_expert: int, d_shared: int, act: str = "silu", balance: float = 1e-2,
+                 z_loss: float = 1e-3, gather: bool = False, seed: int = 0, device="cuda"):
+        super().__init__()
+        self.e, self.k, self.act, self.gather = e, k, act, gather
+        self.weights = (balance, z_loss)
+        g = torch.Generator().manual_seed(seed)
+
+        def mat(*shape):
+            w = torch.randn(*shape, generator=g) / math.sqrt(shape[-1])
+            return torch.nn.Parameter(w.to(device=device, dtype=torch.bfloat16))
+
+        self.norm_w = torch.nn.Parameter(torch.ones(m, device=device))
+        self.norm_b = torch.nn.Parameter(torch.zeros(m, device=device))
+        self.router = mat(e, m)
+        self.up, self.down = mat(e, 2 * d_expert, m), mat(e, m, d_expert)  # up: an expert's gate rows, then the factor's
+        self.shared_up, self.shared_down = mat(2 * d_shared, m), mat(m, d_shared)
+
+    def forward(self, x: torch.Tensor, valid: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None):
+        h = A.layernorm(x, self.norm_w, self.norm_b)
+        logits = A.linear(h, self.router, out_dtype=torch.float32)
+        idx, gate = A.topk_gate(logits, self.k)
+        loss, counts, _ = A.balance_loss(logits, idx, valid, seq_offsets)
+        handle = B.moe_dispatch_layout(idx, self.e, 0)
+        if self.gather:
+            H = A.dispatch_grouped_gated(h, self.up, handle, self.act)
+        else:
+            H = A.grouped_gated(A.dispatch(h, handle), self.up, handle, self.act)
+        routed = A.combine(A.grouped_gemm(H, self.down, handle), gate, handle)
+        y = A.linear(A.gated_linear(h, self.shared_up, act=self.act), self.shared_down, residual=x) + routed
+        return y, self.weights[0] * loss[0] + self.weights[1] * loss[1], counts
+
+
+def main(steps: int = 20, gated: bool = False):
     torch.manual_seed(0)
     s, m = 1024, 512
-    block = MoEBlock(m, e=8, k=2, d_expert=1024, d_shared=1024)
+    block = GatedMoEBlock(m, e=8, k=2, d_expert=704, d_shared=704) if gated else MoEBlock(m, e=8, k=2, d_expert=1024, d_shared=1024)
     x = torch.randn(s, m, device="cuda").bfloat16()
     target = torch.randn(s, m, device="cuda")
     opt = torch.optim.Adam(block.parameters(), lr=3e-3)
@@ -84,11 +129,13 @@ def main(steps: int = 20):
         loss = (y.float() - target).square().mean() + aux
         opt.zero_grad()
         loss.backward()
+        norm = A.clip_grad_norm(block.parameters(), 1.0) if gated else None
         opt.step()
         if A.status():
             raise RuntimeError("a kernel of this step reported a time-out, a NaN or a bad route")
-        print(f"step {step}: loss {loss.item():.4f} (auxiliary {aux.item():.4f}), routes per expert {counts[0].tolist()}")
+        print(f"step {step}: loss {loss.item():.4f} (auxiliary {aux.item():.4f}), routes per expert {counts[0].tolist()}" +
+              (f", gradient norm {norm.item():.4f}" if gated else ""))
 
 
 if __name__ == "__main__":
-    main()
+    main(gated="gated" in sys.argv[1:])

@@ -209,3 +209,18 @@ class ExpertParallelMoE:
         dX = expert_bwd(recv, dY)
         dx = source_reduce(h, send, all_to_all(dest_dispatch_bwd(recv, dX), plan, self.group, back=True))
         return dx, dgate
+
+
+def clip_grad_norm(sharded, replicated, max_norm: float, group=None) -> torch.Tensor:
+    """Clip an expert-parallel model's gradients, in place, to one norm over all ranks: ``sharded`` are this rank's own
+    (its experts'), ``replicated`` those that every rank holds alike (counted once).  Returns the norm before that, f32
+    [1], the same on every rank; one all-reduce of one number.  Squares travel in 64 bits, so that they stay in range."""
+    import torch.distributed as dist
+
+    sharded, replicated = B.GradList(sharded), B.GradList(replicated)
+    own = B.moe_grad_norm(sharded).double().square()
+    dist.all_reduce(own, group=group)
+    norm = (own + B.moe_grad_norm(replicated).double().square()).sqrt().float()
+    B.moe_grad_clip(sharded, norm, max_norm)
+    B.moe_grad_clip(replicated, norm, max_norm)
+    return norm
