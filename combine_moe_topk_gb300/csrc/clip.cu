@@ -6,12 +6,16 @@
 // Bound by memory: every gradient is read once for the norm and, where it is
 // clipped, read again and written.  The tensors travel in the kernels'
 // parameters (up to 1024 a launch), so a call copies no table to the device and
-// can be captured.  Each is cut into chunks of 16 KB; a block takes every
-// gridDim-th of all chunks (with a contiguous range for each block, 608 places of
-// memory at once, the norm of 1.2 G bf16 took 559 us), and the second pass goes
-// backwards, so that what the first read last is still in L2.
+// can be captured.  Each is cut into chunks of 32 KB; a block takes every
+// gridDim-th of all chunks (with a contiguous range for each block the norm of
+// 1.2 G bf16 took 559 us, 1183 with the clipping), and the second pass goes
+// backwards, so that what the first read last is still in L2.  1.2 G bf16, to other
+// tensors: 1077 us, against 1066 for three passes at the copy's rate; 301 odd pieces
+// of 110 MB together 63 us.  Eight 16-byte pieces a thread in two blocks an SM: four
+// in four took 1111 us, eight in four 1441.
 //
-// The squares of a thread's 32 (16) elements of a chunk are added in fp32, the
+// The squares of a thread's 64 (32) elements of a chunk are added in fp32, half of
+// them at a time, the
 // chunks' sums in two fp32 terms (the second what the first's additions rounded
 // off; in 64 bits, which this GPU adds at a 64th of the rate, the norm of 1.2 G bf16 took 562 us),
 // everything beyond a thread in 64 bits.  Beside them runs the largest magnitude: where a
@@ -31,9 +35,9 @@ namespace {
 typedef __nv_bfloat16 bf16;
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                             // 16-byte pieces a thread of a chunk
-constexpr int kChunkBytes = kThreads * kUnroll * 16;   // 16 KB
-constexpr int kPerSm = 4;                              // blocks: 64 KB of loads in flight an SM
+constexpr int kUnroll = 8;                             // 16-byte pieces a thread of a chunk
+constexpr int kChunkBytes = kThreads * kUnroll * 16;   // 32 KB
+constexpr int kPerSm = 2;                              // blocks: 64 KB of loads in flight an SM
 constexpr int kMaxBlocks = kPerSm * 152;
 constexpr int kLarge = 1024, kSmall = 64;              // tensors a launch
 constexpr float kEps = 1e-6f;
@@ -110,10 +114,10 @@ __device__ __forceinline__ float squares(const T* p, long long n, int c, float s
     v[i] = k < s.pieces ? ld_stream(at + k) : make_uint4(0, 0, 0, 0);
   }
   meanwhile();
-  float sum = 0.f;
-  auto add = [&](float f) {
+  float half[2] = {0.f, 0.f};
+  auto add = [&](float f, int i) {
     if (kScaled) f *= scale;
-    sum = fmaf(f, f, sum);
+    half[i & 1] = fmaf(f, f, half[i & 1]);
     top = fmaxf(top, fabsf(f));
   };
 #pragma unroll
@@ -121,11 +125,11 @@ __device__ __forceinline__ float squares(const T* p, long long n, int c, float s
     float f[kElems];
     Vec<T>::to_float(v[i], f);
 #pragma unroll
-    for (int j = 0; j < kElems; ++j) add(f[j]);
+    for (int j = 0; j < kElems; ++j) add(f[j], i);
   }
-  if ((int)threadIdx.x < s.lead) add(one(p + threadIdx.x));
-  if ((int)threadIdx.x < s.trail) add(one(p + s.first + (long long)s.pieces * kElems + threadIdx.x));
-  return sum;
+  if ((int)threadIdx.x < s.lead) add(one(p + threadIdx.x), 0);
+  if ((int)threadIdx.x < s.trail) add(one(p + s.first + (long long)s.pieces * kElems + threadIdx.x), 1);
+  return half[0] + half[1];
 }
 
 // The block's chunks: this thread's sum of squares (of scaled values) and largest magnitude.
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_norm_kernel(const __gri
   float top = 0.f;
   double sum = sum_range<C, false>(t, 1.f, top);
   top = block_max(top, reinterpret_cast<float*>(red));
-  // 32 squares of 2^60 stay in range; below 2^-50 squares would lose bits
+  // 64 squares of 2^60 stay in range; below 2^-50 squares would lose bits
   if (top < CUDART_INF_F && (top > 1.152921504606847e18f || (top > 0.f && top < 8.8817841970012523e-16f))) {
     const int e = ilogbf(top);
     const int by = e < -100 ? 100 : -e;  // e goes down to -149, 2^149 is out of range

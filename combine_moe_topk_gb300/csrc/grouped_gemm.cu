@@ -288,8 +288,6 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
   // same offset, so the MMA's descriptors address the same tiles in both
   uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
 
-  for (int x = threadIdx.x; x <= p.e; x += blockDim.x) s_off[x] = __ldg(p.offsets + x);
-  for (int x = threadIdx.x; x < p.e; x += blockDim.x) s_cnt[x] = __ldg(p.counts + x);
   if (threadIdx.x == 0) {
     s_err = 0;
     for (int i = 0; i < kPairStages; ++i) {
@@ -313,9 +311,12 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
                  "r"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else if (warp == 3) {
-    prefix_blocks(s_cnt, s_blk, p.e, BM2, lane);
   }
+  grid_dependency_wait();  // all set-up is done: from here on memory of earlier kernels is read
+  for (int x = threadIdx.x; x <= p.e; x += blockDim.x) s_off[x] = ld_plain(p.offsets + x);
+  for (int x = threadIdx.x; x < p.e; x += blockDim.x) s_cnt[x] = ld_plain(p.counts + x);
+  __syncthreads();
+  if (warp == 3) prefix_blocks(s_cnt, s_blk, p.e, BM2, lane);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both ranks' barriers are initialised before any remote signal
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
         const int rr = kGatherRows * gw + 4 * j + (lane >> 3);
         tok[j] = -1;
         if (rr < left) {
-          const int v = __ldg(p.inv_row + r0 + rr);
+          const int v = ld_plain(p.inv_row + r0 + rr);
           tok[j] = (unsigned)v < (unsigned)p.s ? v : 0;
         }
       }
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
     if (!ok) atomicOr(&s_err, 1);
   }
 
+  grid_dependents_launch();
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // both ranks done with TMEM and with each other's barriers
@@ -592,13 +594,15 @@ cudaError_t launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm
   cfg.blockDim = dim3(Roles<kGather, kGated>::kAll);
   cfg.dynamicSmemBytes = kPairSmemBytes;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, grouped_gemm_pair_kernel<kGather, kGated>, ma, mb, p);
 }
 
