@@ -46,7 +46,10 @@ namespace {
 
 constexpr int BM = 128, BN = 256, BK = 64;
 constexpr int kTmemCols = 2 * BN;     // two fp32 accumulators of 128 lanes x 256 columns
-constexpr int kGatedWarps = 8;       // epilogue warps of the gated form (4 in the plain one)
+// Epilogue warps of the gated form (4 in the plain one).  Its fused form has 4 too: with
+// 8 beside the gathering warps 96 registers a thread do not do (16384 rows x 4096 x
+// 2048, z kept: 357 us, 348 with 4).
+constexpr int kGatedWarps = 8;
 // Warps gathering the fused form's A rows: 8 (16 rows each) measured 1-4 %
 // faster than 4 and 3 % faster than 16 (fewer registers per thread at 768
 // threads); 2 were 20-30 % slower.
@@ -143,17 +146,19 @@ __device__ __forceinline__ void store_accumulator(uint32_t tcol, int ew, int lan
 }
 
 // Drain a gated unit's accumulator: columns [0, 128) are the gate's, [128, 256) the
-// same columns of the factor.  Two warps share 32 lanes, each with half of the 128
-// columns of h, 32 at a time:
+// same columns of the factor.  Two warps (one) share 32 lanes, each with half (all)
+// of the 128 columns of h, 32 at a time:
 //   h = act(g) u,  and z = [g | u] where it is kept.
-__device__ __forceinline__ void store_gated(uint32_t tcol, int ew, int half, int lane, uint8_t* stage, const GemmParams& p,
+template <int kWarps>
+__device__ __forceinline__ void store_gated(uint32_t tcol, int ew, int part, int lane, uint8_t* stage, const GemmParams& p,
                                             int r0, int n0, int nvalid) {
+  constexpr int kChunks = 16 / kWarps;  // of 32 columns, this warp's share
   const int rows = nvalid - 32 * ew;
   if (rows <= 0) return;  // the whole warp
   const long long at = r0 + 32 * ew;
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    const int j = 64 * half + 32 * c, col = n0 + j, cols = p.N - col;
+  for (int c = 0; c < kChunks; ++c) {
+    const int j = 32 * (kChunks * part + c), col = n0 + j, cols = p.N - col;
     if (cols <= 0) return;
     uint32_t v[32], w[16];
     float g[32], u[32];
@@ -254,7 +259,7 @@ __device__ __forceinline__ uint32_t mma_idesc_pair() {
 // Roles of a CTA: four control warps, the epilogue's, then the gathering ones.
 template <bool kGather, bool kGated>
 struct Roles {
-  static constexpr int kEpiWarps = kGated ? kGatedWarps : 4;
+  static constexpr int kEpiWarps = kGated && !kGather ? kGatedWarps : 4;
   static constexpr int kMain = 128 + 32 * kEpiWarps;
   static constexpr int kAll = kMain + (kGather ? 32 * MOE_GEMM_GATHER_WARPS : 0);
 };
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(Roles<kGather, kGated>::kAll, 1)
       const uint32_t tcol = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * BN);
       uint8_t* stage_buf = smem + kPairStages * kPairStageBytes;
       if constexpr (kGated)
-        store_gated(tcol, ew, (warp - 4) >> 2, lane, stage_buf + (warp - 4) * kRowStage, p, r0, t.n0, nvalid);
+        store_gated<kEpiWarps>(tcol, ew, (warp - 4) >> 2, lane, stage_buf + (warp - 4) * kRowStage, p, r0, t.n0, nvalid);
       else
         store_accumulator(tcol, ew, lane, stage_buf + ew * kEpiWarpBytes, p.Y, p.N, r0, t.n0, nvalid);
       tc_fence_before();
