@@ -8,6 +8,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <initializer_list>
@@ -38,8 +39,13 @@ struct moe_handle_s {
 };
 
 struct moe_tensor_list_s {
+  struct Range {
+    uintptr_t begin, end;
+    int i;
+  };
   int device;  // -1: no tensors
   std::vector<moe::GradTensor> t;
+  std::vector<Range> ranges;  // of memory, by address
 };
 
 namespace {
@@ -1414,7 +1420,18 @@ moe_status moe_tensor_list_create(const moe_tensor* tensors, int count, moe_tens
   list->device = count > 0 ? dev : -1;
   try {
     list->t.reserve(count);
-    for (int i = 0; i < count; ++i) list->t.push_back({tensors[i].data, tensors[i].numel, tensors[i].dtype == MOE_F32});
+    for (int i = 0; i < count; ++i) {
+      const moe_tensor& t = tensors[i];
+      list->t.push_back({t.data, t.numel, t.dtype == MOE_F32});
+      const uintptr_t at = reinterpret_cast<uintptr_t>(t.data);
+      if (t.numel > 0) list->ranges.push_back({at, at + (uintptr_t)t.numel * (t.dtype == MOE_F32 ? 4 : 2), i});
+    }
+    std::sort(list->ranges.begin(), list->ranges.end(),
+              [](const moe_tensor_list_s::Range& a, const moe_tensor_list_s::Range& b) { return a.begin < b.begin; });
+    for (size_t i = 1; i < list->ranges.size(); ++i)
+      if (list->ranges[i].begin < list->ranges[i - 1].end)
+        return fail(MOE_ERR_INVALID_ARG, "tensors " + std::to_string(list->ranges[i - 1].i) + " and " +
+                                             std::to_string(list->ranges[i].i) + " overlap");
     std::lock_guard<std::mutex> lk(g_mu);
     g_lists.insert(list.get());
   } catch (const std::bad_alloc&) {
@@ -1453,6 +1470,13 @@ moe_status check_grads(moe_tensor_list grads, moe_tensor_list out, const float* 
     for (size_t i = 0; i < out->t.size(); ++i)
       if (out->t[i].n != grads->t[i].n || out->t[i].f32 != grads->t[i].f32)
         return fail(MOE_ERR_INVALID_ARG, "out: tensor " + std::to_string(i) + " has another size or type");
+    // only a tensor's own place in out may share its memory, and then all of it
+    for (size_t i = 0, j = 0; i < grads->ranges.size() && j < out->ranges.size();) {
+      const moe_tensor_list_s::Range &a = grads->ranges[i], &b = out->ranges[j];
+      if (a.begin < b.end && b.begin < a.end && !(a.i == b.i && a.begin == b.begin))
+        return fail(MOE_ERR_INVALID_ARG, "out: tensor " + std::to_string(b.i) + " overlaps gradient " + std::to_string(a.i));
+      if (a.end <= b.end) ++i; else ++j;
+    }
   }
   if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm is NULL");
   if (reinterpret_cast<uintptr_t>(norm) & 3u) return fail(MOE_ERR_INVALID_ARG, "norm is not 4-byte aligned");

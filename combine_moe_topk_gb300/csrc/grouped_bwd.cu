@@ -22,7 +22,8 @@
 // there would survive a zero in one), between the copy and the MMA.  Such a
 // block's copies count on a barrier of each CTA (`tail`); a warp of each waits for
 // it, writes the zeros, and arrives in the TMA's place on the barrier that the MMA
-// waits for.  An expert without rows gets zeros.
+// waits for (the second CTA's word through the async proxy).  An expert without rows
+// gets zeros.
 //
 //   warp 0 lane 0   TMA producer (both CTAs)
 //   warp 1 lane 0   MMA issuer (the first CTA)
@@ -137,9 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     grouped_bwd_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Args p) {
   extern __shared__ uint8_t smem_raw[];
-  // full: the copies of both CTAs (two arrivals of the first CTA's producer, or one
-  // of each CTA's zeroing warp); tail: this CTA's copies of a cut block
+  // full: the copies of both CTAs (two arrivals of the first CTA's producer; of a cut
+  // block its zeroing warp's two, and 16 bytes from the second CTA's); tail: this
+  // CTA's copies of a cut block
   __shared__ __align__(8) uint64_t full[kStages], empty[kStages], tail[kStages], tfull[2], tempty[2], drain;
+  __shared__ __align__(16) uint8_t s_signal[16];  // source and target of the second CTA's word
   __shared__ uint32_t tmem_base;
   __shared__ int s_cnt[kMaxE], s_off[kWeights ? 1 : kMaxE], s_blk[kWeights ? 1 : kMaxE + 1];
   __shared__ uint8_t s_order[kWeights ? kMaxE : 1];
@@ -322,7 +325,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_addr(&full[stage]), 0));
+      if (lane == 0) {
+        // the second CTA's word travels through the async proxy, behind its zeros (an
+        // arrival with release at cluster scope instead: 128 experts of 2816 x 704 and
+        // 174 rows 149 us)
+        if (rank == 0) {
+          mbar_arrive_expect_tx(&full[stage], 16);
+          mbar_arrive(&full[stage]);
+        } else {
+          bulk_signal_s2s(mapa_shared(smem_addr(s_signal), 0), s_signal, mapa_shared(smem_addr(&full[stage]), 0));
+        }
+      }
     }
     if (!ok && lane == 0) atomicOr(&s_err, 1);
   } else if (warp >= 4) {

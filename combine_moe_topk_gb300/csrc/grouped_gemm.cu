@@ -236,16 +236,6 @@ constexpr int kPairRingBytes = kPairStages * kPairKB * (kSubA + kSubB);  // 192 
 constexpr int kPairSmemBytes = kPairRingBytes + kEpiBytes + 1024;
 constexpr int BM2 = 2 * BM;                     // rows of a pair block
 
-// 16 bytes from this CTA's shared memory to `dst` in another CTA of the
-// cluster, the bytes counted on the mbarrier `mbar` there: a signal that
-// travels through the async proxy (no cluster-scope release fence).
-__device__ __forceinline__ void bulk_signal_s2s(uint32_t dst, const void* src, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
-      "r"(smem_addr(src)), "r"(mbar)
-      : "memory");
-}
-
 __device__ __forceinline__ uint32_t mma_idesc_pair() {
   uint32_t d = 0;
   d |= 1u << 4;                        // accumulator format: f32

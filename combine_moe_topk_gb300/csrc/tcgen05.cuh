@@ -113,10 +113,6 @@ __device__ __forceinline__ bool mbar_wait_cluster_limited(uint64_t* bar, uint32_
   }
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
-}
-
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -201,11 +197,21 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   }
 }
 
-// The same for an epilogue that hands an accumulator back to the MMA's CTA: what must
+// 16 bytes from this CTA's shared memory to `dst` in another CTA of the
+// cluster, the bytes counted on the mbarrier `mbar` there: a signal that
+// travels through the async proxy (no cluster-scope release fence).
+__device__ __forceinline__ void bulk_signal_s2s(uint32_t dst, const void* src, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+      "r"(smem_addr(src)), "r"(mbar)
+      : "memory");
+}
+
+// An epilogue warp hands an accumulator back on a barrier of the MMA's CTA.  What must
 // be over are its tcgen05.ld, and tcgen05.wait::ld has seen to that.  So release
-// stays at the CTA's scope: a release at cluster scope also waits for the warp's
-// stores to be seen there, which cost more than a microsecond a tile (dW of 128
-// experts, 2816 x 768 from 128 rows: 167 -> 126 us).
+// stays at the CTA's scope: at cluster scope it also waits for the warp's stores to be
+// seen there, which cost more than a microsecond a tile (dW of 128 experts, 2816 x
+// 768 from 128 rows: 167 -> 126 us).
 __device__ __forceinline__ void mbar_arrive_accumulator(uint32_t mbar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }

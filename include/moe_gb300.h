@@ -674,8 +674,9 @@ moe_status moe_grouped_gated_bwd(moe_handle h, int rows, int K, int N, int act, 
 /* ---- the gradients' global norm, and clipping -----------------------------------
  * A list of tensors, checked once: device memory of the current device, fp32 or
  * bf16, contiguous, aligned to their elements (16 bytes are not needed), any
- * number of elements including none.  The list keeps the addresses, not the
- * memory: it must be there while calls with the list run. */
+ * number of elements including none, none sharing memory with another.  The list
+ * keeps the addresses, not the memory: it must be there while calls with the list
+ * run. */
 typedef struct {
   void* data;
   int64_t numel;
@@ -692,15 +693,15 @@ moe_status moe_tensor_list_destroy(moe_tensor_list list);
 size_t moe_grad_norm_workspace(int count);
 
 /* norm[0] = sqrt(sum of g^2 over all tensors), f32 in device memory.  Squares are
- * summed in fp32 within 32 elements and in 64 bits beyond, scaled where they
+ * summed in fp32 within 32 elements, in twice that up to a thread, in 64 bits beyond, scaled where they
  * would leave fp32's range; fixed order.  A NaN or infinity reaches the norm (which is
  * infinite past fp32's range too) and sets MOE_DEV_NONFINITE in device_status (nullable).  An empty list: 0. */
 moe_status moe_grad_norm(moe_tensor_list grads, float* norm, void* workspace, size_t workspace_bytes, int32_t* device_status,
                          void* stream);
 
 /* With coef = min(1, max_norm / (norm[0] + 1e-6)), every gradient times coef, rounded
- * once, to the tensor of the same place in `out` (same sizes and types, no overlap; NULL: in
- * place; then nothing is written where coef is 1).  norm is given, e.g. joined over ranks.  A norm that is not
+ * once, to the tensor of the same place in `out` (same sizes and types; its own tensor or one that
+ * overlaps none; NULL: in place; then nothing is written where coef is 1).  norm is given, e.g. joined over ranks.  A norm that is not
  * finite leaves the gradients unscaled (`out` gets copies).  max_norm >= 0. */
 moe_status moe_grad_clip(moe_tensor_list grads, moe_tensor_list out, const float* norm, float max_norm, void* stream);
 

@@ -149,3 +149,34 @@ def test_a_list_kept_and_captured():
         assert torch.equal(norm, B.moe_clip_grad_norm(kept, 1.0, out=out))
         for a, c in zip(have, out.tensors):
             assert torch.equal(a, c)
+
+
+def test_tensors_that_share_memory_are_refused():
+    t = torch.randn(100, device="cuda")
+    for bad in ([t, t], [t[:60], t[59:]], [t[50:], t[:51]]):
+        with pytest.raises(B.MoEError, match="overlap"):
+            B.GradList(bad)
+    B.GradList([t[:0], t[:50], t[50:50], t[50:]])  # pieces side by side, and empty ones
+    a, b = t[:50], t[50:]
+    with pytest.raises(B.MoEError, match="overlaps"):
+        B.moe_clip_grad_norm([a, b], 1.0, out=[b, a])
+    with pytest.raises(B.MoEError, match="overlaps"):
+        B.moe_clip_grad_norm([t[:40], t[60:]], 1.0, out=[torch.empty_like(t[:40]), t[10:50]])
+    before = t.clone()
+    norm = B.moe_clip_grad_norm([a, b], 1.0, out=[a, b])  # their own places
+    assert torch.allclose(t, before / float(norm), rtol=1e-5)
+    with pytest.raises(B.MoEError):
+        B.moe_clip_grad_norm([a], 1.0, out=[a, b])
+    with pytest.raises(B.MoEError):
+        B.moe_clip_grad_norm([a], 1.0, out=[torch.empty(50, device="cuda", dtype=torch.bfloat16)])
+
+
+def test_more_than_2_31_elements():
+    n = 2 ** 31 + 4099
+    g = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    g[-1] = 8.0
+    norm = float(B.moe_clip_grad_norm([g[3:]], 1.0))  # off 16 bytes
+    want = (0.25 * (n - 4) + 64.0) ** 0.5
+    assert abs(norm - want) <= 18 * U * want
+    assert float(g[2]) == 0.5 and abs(float(g[-1]) - 8.0 / want) <= 2.0 ** -8 * 8.0 / want
+    assert (g[3:-1] == torch.tensor(0.5 / (want + 1e-6)).bfloat16().item()).all()

@@ -174,3 +174,18 @@ def test_calls_in_a_captured_graph():
         torch.cuda.synchronize()
         for a, c in zip([t.clone() for t in out], step()):
             assert torch.equal(a, c)
+
+
+def test_results_of_more_than_2_31_elements():
+    s, K, N = 66000, 64, 16384  # z: 2.16e9 elements
+    x, W, b, _, _ = make(s, K, N, seed=11)
+    h, z = B.moe_gated_linear(x, W, b, "silu", save_z=True)
+    check_fwd(x[-40:].contiguous(), W, b, "silu", h[-40:], z[-40:])
+    check_fwd(x[:40].contiguous(), W, b, "silu", h[:40], z[:40])
+    # its backward pass: rows are apart from one another in dx, and db sums them all
+    dh = torch.zeros_like(h)
+    dh[-30:] = torch.randn(30, N, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    dx, dW, db = B.moe_gated_linear_bwd(dh, x, W, z)
+    assert not dx[:-30].any()
+    t = slice(s - 30, s)
+    check_bwd(dh[t], x[t].contiguous(), W, z[t], "silu", (dx[t], dW, db))
