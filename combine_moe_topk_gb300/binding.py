@@ -1073,6 +1073,7 @@ class GradList:
             elif t.device != self.device:
                 raise MoEError(1, "GradList", "the tensors are on different devices")
             spec[i].data, spec[i].numel, spec[i].dtype = t.data_ptr(), t.numel(), _DTYPE.get(t.dtype, -1)
+        self.workspace = lib().moe_grad_norm_workspace(len(tensors))
         self._raw = raw = ctypes.c_void_p()
         if self.device is not None and self.device.type == "cuda":
             with torch.cuda.device(self.device):
@@ -1139,9 +1140,8 @@ def _norm_call(where: str, g: GradList, norm, device_status, call):
         norm = new(torch.float32, 1)
     else:
         _check_norm(where, norm)
-    nbytes = lib().moe_grad_norm_workspace(len(g))
-    ws = new(torch.uint8, nbytes)
-    rc = call(_addr(norm), ws.data_ptr(), nbytes, _status_addr(device_status, where), _raw_stream(norm))
+    ws = new(torch.uint8, g.workspace)
+    rc = call(_addr(norm), ws.data_ptr(), g.workspace, _status_addr(device_status, where), _raw_stream(norm))
     if rc:
         _check(rc, where)
     return norm

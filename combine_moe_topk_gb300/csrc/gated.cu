@@ -6,7 +6,8 @@
 //   dx = dz W,  dW = dz^T x   (the products of linear.cu over 2N columns)
 //
 // dz is rounded to bf16 for the tensor cores; db sums it before that.  Memory bound: 10
-// bytes an element of h in bf16.
+// bytes an element of h in bf16 (6001 x 4096, gelu_tanh with column sums 38.0 us, 6.5
+// TB/s; 131072 skewed rows x 512, silu, 96 us, 7.0 TB/s).
 #include <math_constants.h>
 
 #include "common.cuh"
@@ -38,6 +39,9 @@ typedef __nv_bfloat16 bf16;
 // consecutive elements to two MMAs as their k pairs, and the accumulator, which
 // drops the bits below its last place, is emptied into an fp32 sum after every
 // chunk.  The warps' sums are added in order through shared memory every 16 columns.
+// One row, 4096 x 4096: 14.1 us (by tiles 24.4), x 14336: 36.9 us, 6.4 TB/s; 8 tokens
+// through 64 experts of 2048 x 1408, six each, 34 of them chosen: 63.9 us (by tiles
+// 75.0), 6.1 TB/s.
 // A wait that runs out sets the status and everyone runs on without waiting, so
 // that the barriers stay matched.
 constexpr int kFewK = 2048;                    // of the contracted axis a stage
@@ -68,12 +72,15 @@ __device__ __forceinline__ float bias_at(const FewArgs& p, int i) {
                     : __bfloat162float(ld_plain(static_cast<const bf16*>(p.bias) + i));
 }
 
+// kExperts: blocks of the experts' segments; else one block of p.s rows, known
+// without a look at memory.
+template <bool kExperts>
 __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant__ FewArgs p) {
   constexpr int kBlocks = kFewK / 32 / 8;  // 32-wide blocks of a stage and warp
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ __align__(8) uint64_t full[kFewStages], empty[kFewStages];
   __shared__ float red[8][16][2 * kFewCols + 1];
-  __shared__ int s_cnt[kMaxE], s_off[kMaxE], s_blk[kMaxE + 1];
+  __shared__ int s_cnt[kExperts ? kMaxE : 1], s_off[kExperts ? kMaxE : 1], s_blk[kExperts ? kMaxE + 1 : 1];
   __shared__ int s_err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -84,15 +91,18 @@ __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant
     }
     fence_barrier_init();
   }
+  __syncthreads();
   grid_dependency_wait();
-  for (int x = threadIdx.x; x < p.e; x += blockDim.x) {
-    s_cnt[x] = p.counts ? ld_plain(p.counts + x) : p.s;
-    s_off[x] = p.counts ? ld_plain(p.offsets + x) : 0;
+  if constexpr (kExperts) {
+    for (int x = threadIdx.x; x < p.e; x += blockDim.x) {
+      s_cnt[x] = ld_plain(p.counts + x);
+      s_off[x] = ld_plain(p.offsets + x);
+    }
+    __syncthreads();
+    if (warp == 0) prefix_blocks(s_cnt, s_blk, p.e, 16, lane);
+    __syncthreads();
   }
-  __syncthreads();
-  if (warp == 0) prefix_blocks(s_cnt, s_blk, p.e, 16, lane);
-  __syncthreads();
-  const long long all = (long long)s_blk[p.e] * p.N;
+  const long long all = kExperts ? (long long)s_blk[p.e] * p.N : p.N;
   const long long f0 = all * blockIdx.x / gridDim.x, f1 = all * (blockIdx.x + 1) / gridDim.x;
   const int chunks = (p.K + kFewK - 1) / kFewK;
   int stage = 0;
@@ -111,13 +121,19 @@ __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant
   };
   auto group_of = [&](long long f) {
     Group g;
-    const int b = (int)(f / p.N);
+    const int b = kExperts ? (int)(f / p.N) : 0;
     g.c0 = (int)(f - (long long)b * p.N);
     g.cols = (int)min((long long)min(kFewCols, p.N - g.c0), f1 - f);
-    g.x = expert_of(b, s_blk, p.e);
-    const int first = 16 * (b - s_blk[g.x]);
-    g.rows = min(16, s_cnt[g.x] - first);
-    g.row = (long long)s_off[g.x] + first;
+    if constexpr (kExperts) {
+      g.x = expert_of(b, s_blk, p.e);
+      const int first = 16 * (b - s_blk[g.x]);
+      g.rows = min(16, s_cnt[g.x] - first);
+      g.row = (long long)s_off[g.x] + first;
+    } else {
+      g.x = 0;
+      g.rows = p.s;
+      g.row = 0;
+    }
     return g;
   };
   if (warp == 8) {
@@ -140,7 +156,7 @@ __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant
         for (int q = 0; q < 2; ++q) {
           if (8 * q + lane >= g.rows || lane >= 8) continue;
           long long r = g.row + 8 * q + lane;
-          if (p.inv_row) {
+          if (kExperts && p.inv_row) {
             const int t = ld_plain(p.inv_row + r);
             r = (unsigned)t < (unsigned)p.tokens ? t : 0;
           }
@@ -255,13 +271,14 @@ __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant
   }
 }
 
+template <bool kExperts>
 cudaError_t run_few(const FewArgs& p, long long most, const DeviceInfo& di, cudaStream_t st) {
   static OncePerDevice once;
   cudaError_t err = once.run([] {
-    return cudaFuncSetAttribute(few_gated_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    return cudaFuncSetAttribute(few_gated_kernel<kExperts>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
   });
   if (err != cudaSuccess) return err;
-  return launch_chained(few_gated_kernel, dim3((unsigned)(most < di.sms ? most : di.sms)), dim3(288), kFewSmem, st, p);
+  return launch_chained(few_gated_kernel<kExperts>, dim3((unsigned)(most < di.sms ? most : di.sms)), dim3(288), kFewSmem, st, p);
 }
 
 // ---- dz and the biases' gradients -------------------------------------------------
@@ -297,7 +314,9 @@ __device__ __forceinline__ void store_dz(bf16* at, long long further, bool two, 
 }
 
 // A warp walks rows of 256 columns of h, eight a lane; a block's eight warps add
-// their column sums up through shared memory, each block one partial row.
+// their column sums up through shared memory, each block one partial row.  Four
+// blocks an SM hide the loads (five 52 us at 6001 x 4096, six 58, with the next row's
+// loads under way in three 63, in two 39).
 template <typename T, int kAct, bool kTwo, bool kGrouped>
 __global__ void __launch_bounds__(256, 4) gated_dz_kernel(const DzArgs p) {
   __shared__ float acc[kGrouped ? 1 : 8][2][256 + 8];
@@ -428,7 +447,7 @@ cudaError_t launch_few_gated(const GatedArgs& a, const DeviceInfo& di, cudaStrea
   p.z = static_cast<bf16*>(a.z);
   p.status = a.status;
   p.timeout_ns = kWaitNs;
-  return run_few(p, a.N, di, st);
+  return run_few<false>(p, a.N, di, st);
 }
 
 cudaError_t launch_few_grouped(const int32_t* offsets, const int32_t* counts, const int32_t* inv_row, int e, int rows, int s,
@@ -451,7 +470,7 @@ cudaError_t launch_few_grouped(const int32_t* offsets, const int32_t* counts, co
   p.z = static_cast<bf16*>(Z);
   p.status = status;
   p.timeout_ns = kWaitNs;
-  return run_few(p, (long long)rows * N, di, st);
+  return run_few<true>(p, (long long)rows * N, di, st);
 }
 
 cudaError_t launch_gated_bwd(const GatedBwdArgs& a, const DeviceInfo& di, cudaStream_t st) {

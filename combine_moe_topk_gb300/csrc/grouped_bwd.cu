@@ -25,6 +25,10 @@
 // waits for (the second CTA's word through the async proxy).  An expert without rows
 // gets zeros.
 //
+// Bound by the tensor cores where segments are long (1024 rows, 4096 x 1024: dX 1.69,
+// dW 1.59 PFLOP/s), by memory where they are short (174 rows of 128 experts, 2816 x 704:
+// dX 119 us, 5.6 TB/s; dW 125 us, 5.3 TB/s, against 84 for zeros alone).
+//
 //   warp 0 lane 0   TMA producer (both CTAs)
 //   warp 1 lane 0   MMA issuer (the first CTA)
 //   warp 2          TMEM allocation

@@ -1,6 +1,7 @@
 // grouped_gemm.cu -- the expert-grouped GEMM that consumes the dispatched
 // rows, on the 5th-generation tensor cores (tcgen05, TMEM accumulators,
-// TMA tile loads), and its fused form that gathers the token rows itself.
+// TMA tile loads), its fused form that gathers the token rows itself, and both
+// for gated experts.
 //
 // DeepSpeed #8213 "Add an opt-in DeepEP transport for the AutoEP expert
 // all-to-all", description: the dispatch groups arrivals by expert for the

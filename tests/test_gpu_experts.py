@@ -40,6 +40,9 @@ def layout(s, e, k, kind="dropless", seed=0, counts=None):
         return B.moe_dispatch_layout_ex(idx, e, max(1, s * k // (2 * e)), priority="kmajor")
     if kind == "padded":
         return B.moe_dispatch_layout_ex(idx, e, pad_multiple=24)
+    if kind == "absent":  # as an expert-parallel rank's arrivals: most routes are to other ranks' experts
+        idx[torch.rand(idx.shape, generator=torch.Generator().manual_seed(seed)).cuda() < 0.7] = -1
+        return B.moe_dispatch_layout_ex(idx, e, absent_routes=True)
     if kind == "bound":
         return B.moe_dispatch_layout_ex(idx, e, rows_bound=max(1, s * k * 3 // 4))
     return B.moe_dispatch_layout(idx, e, 0)
@@ -141,7 +144,7 @@ def run_all(h, s, K, N, act, seed=0, check_gather=True):
     assert h.status() & ~B.MOE_DEV_ROWS_EXCEEDED == 0  # a layout with a bound says that it was reached
 
 
-@pytest.mark.parametrize("kind", ["dropless", "capacity", "kmajor", "padded", "bound"])
+@pytest.mark.parametrize("kind", ["dropless", "capacity", "kmajor", "padded", "absent", "bound"])
 @pytest.mark.parametrize("s,e,k,K,N", [(1, 4, 2, 64, 8), (9, 8, 2, 72, 24), (100, 8, 3, 128, 136), (700, 16, 4, 264, 128),
                                        (1500, 4, 2, 512, 264), (900, 60, 6, 136, 72)])
 def test_layouts(kind, s, e, k, K, N):
@@ -177,6 +180,27 @@ def test_no_rows():
     assert dX.shape == (0, 64) and not dW.any()
     dX, dW = B.moe_grouped_gated_bwd(h, z[:, :16].contiguous(), x, W, z)
     assert dX.shape == (0, 64) and not dW.any()
+
+
+def test_two_streams_at_once():
+    """The same handle and weights on two streams: each call has a workspace of its own."""
+    s, e, k, K, N = 2000, 8, 2, 512, 256
+    g = torch.Generator().manual_seed(9)
+    h = layout(s, e, k, seed=9)
+    W = rand(g, e, 2 * N, K, scale=K ** -0.5)
+    sets = [(rand(g, s * k, N), rand(g, s * k, K), rand(g, s * k, 2 * N)) for _ in range(2)]
+    want = [B.moe_grouped_gated_bwd(h, dH, X, W, Z) for dH, X, Z in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(B.moe_grouped_gated_bwd(h, sets[i][0], sets[i][1], W, sets[i][2]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
 
 
 def test_a_training_chain_in_a_captured_graph():
