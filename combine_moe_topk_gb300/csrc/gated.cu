@@ -497,7 +497,7 @@ cudaError_t launch_gated_bwd(const GatedBwdArgs& a, const DeviceInfo& di, cudaSt
   }
   if (!copies) return cudaSuccess;
   return launch_products_bwd({p.dz, a.x, a.W, a.dx, a.dW, a.status, 2LL * a.N, a.ldx, a.ldw, a.s, a.K, 2 * a.N, a.dx_f32,
-                              a.dw_f32, copies == 2}, di, st);
+                              a.dw_f32, copies == 2, true}, di, st);
 }
 
 cudaError_t launch_grouped_dz(const int32_t* offsets, const int32_t* counts, int e, int rows, int N, int act, const void* dH,

@@ -216,14 +216,15 @@ size_t linear_bwd_workspace(int s, int N, int act, bool dy_f32, long long lddy, 
 cudaError_t launch_linear_bwd(const LinearBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 // Its products alone: dx = dz W, dW = dz^T x (each may be NULL).  two: dz [s][lddz]
-// is followed by what its rounding to bf16 left, for the fp32 results.
+// is followed by what its rounding to bf16 left, for the fp32 results.  by_rows: a bf16
+// dx may be made of two products (first_rows).
 struct ProductsBwdArgs {
   const void *dz, *x, *W;
   void *dx, *dW;
   int32_t* status;
   long long lddz, ldx, ldw;
   int s, K, N, dx_f32, dw_f32;
-  bool two;
+  bool two, by_rows;
 };
 cudaError_t launch_products_bwd(const ProductsBwdArgs& a, const DeviceInfo& di, cudaStream_t st);
 

@@ -111,7 +111,8 @@ def test_activations_and_types(act, s):
         assert torch.equal(a, c)
 
 
-@pytest.mark.parametrize("s,K,N", [(4100, 640, 2504), (9000, 72, 520), (300, 264, 4504)])
+# the last: dx of two products, 19 blocks of 256 rows and 40 more
+@pytest.mark.parametrize("s,K,N", [(4100, 640, 2504), (9000, 72, 520), (300, 264, 4504), (4904, 1024, 2048)])
 def test_many_tiles(s, K, N):
     x, W, b, dh, z = make(s, K, N, seed=K)
     h, zz = B.moe_gated_linear(x, W, b, "silu", save_z=True)
