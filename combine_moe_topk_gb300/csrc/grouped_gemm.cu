@@ -649,12 +649,14 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
 
 // Whether an expert product streams the weights through warp-level MMA, 16 rows at a
 // time (few_gated_kernel), or goes by tiles of 256 rows.  The host knows the rows of
-// all experts together.  Measured, tiles / streamed: 64 experts of 2048 x 1408, 1.5
-// rows an expert 109.5 / 94.1 us, 6 134.7 / 129.1, 12 135.3 / 145.3; 8 experts of
-// 4096 x 4096, 4 rows 104.9 / 82.8, 8 104.9 / 88.4, 16 105.7 / 130.5; 128 experts of
-// 4096 x 512, 8 rows 183.9 / 177.3, 16 185.2 / 255.7.  (Uneven routing adds at most a
-// pass for every 16 rows.)
-static bool few_rows(int rows, int e) { return rows <= kFewRows || rows <= 8LL * e; }
+// all experts together, not their spread; where routing is skewed, an expert of many
+// rows is streamed over and over.  Measured, tiles / streamed, even routing and
+// skewed (Zipf 1.2): 64 experts of 2048 x 1408, a row an expert 84.0 / 73.9 and 48.0 /
+// 43.9 us, two 116.8 / 103.7 and 57.5 / 58.5, four 127.9 / 122.7 and 69.4 / 82.1; 8
+// experts of 4096 x 4096, two 91.7 / 75.9 and 76.6 / 58.5, eight 102.0 / 87.7 and 91.4
+// / 93.2; 128 experts of 4096 x 512, two 164.2 / 139.0 and 62.2 / 67.9, four 178.1 /
+// 165.1 and 78.4 / 94.3.
+static bool few_rows(int rows, int e) { return rows <= kFewRows || rows <= 2LL * e; }
 
 cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, int act,
                                  const void* X, const void* W, void* H, void* Z, int32_t* status, const DeviceInfo& di,
