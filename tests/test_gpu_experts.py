@@ -158,6 +158,13 @@ def test_segment_lengths(counts):
     run_all(layout(sum(counts), len(counts), 1, counts=counts), sum(counts), 200, 104, "gelu_tanh", seed=len(counts))
 
 
+# few rows an expert: blocks of 16 of one expert, several chunks of the contracted axis, more columns than SMs and fewer
+@pytest.mark.parametrize("counts,K,N", [([40, 0, 0, 9, 17] + [0] * 40, 200, 72), ([2] * 30, 2600, 136), ([1], 4104, 8),
+                                        ([0, 16], 2048, 512), ([3, 0, 1, 33] + [0] * 20, 64, 2504)])
+def test_few_rows(counts, K, N):
+    run_all(layout(sum(counts), len(counts), 1, counts=counts), sum(counts), K, N, "silu", seed=K)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
 def test_activations(act):
     run_all(layout(333, 6, 2, seed=3), 333, 96, 56, act, seed=5)
