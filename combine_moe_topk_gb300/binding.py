@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import torch
@@ -1061,18 +1062,17 @@ class GradList:
 
     def __init__(self, tensors):
         self.tensors = tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
-        self.device = None
-        # compared with another list's in one go
-        self.layout = repr([(tuple(t.shape), t.stride()) for t in tensors])
-        spec = (Tensor * max(1, len(tensors)))()
+        self.device = tensors[0].device if tensors else None
+        self._layout = None
+        flat = []
         for i, t in enumerate(tensors):
-            if t.layout != torch.strided or not _dense(t):
+            if t.layout != torch.strided or not (t.is_contiguous() or _dense(t)):
                 raise ValueError(f"tensor {i}: gradients must be dense tensors without gaps or overlaps in memory")
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
+            if t.device != self.device:
                 raise MoEError(1, "GradList", "the tensors are on different devices")
-            spec[i].data, spec[i].numel, spec[i].dtype = t.data_ptr(), t.numel(), _DTYPE.get(t.dtype, -1)
+            flat += (t.data_ptr(), t.numel(), _DTYPE.get(t.dtype, -1))
+        spec = (Tensor * max(1, len(tensors))).from_buffer_copy(struct.pack("=" + "Qqi4x" * len(tensors), *flat) if flat else
+                                                                bytes(ctypes.sizeof(Tensor)))
         self.workspace = lib().moe_grad_norm_workspace(len(tensors))
         self._raw = raw = ctypes.c_void_p()
         if self.device is not None and self.device.type == "cuda":
@@ -1092,6 +1092,13 @@ class GradList:
     def raw(self):
         return self._raw
 
+    @property
+    def layout(self) -> str:
+        """All shapes and strides, to be compared with another list's in one go."""
+        if self._layout is None:
+            self._layout = repr([(tuple(t.shape), t.stride()) for t in self.tensors])
+        return self._layout
+
     def __del__(self):
         raw = getattr(self, "_raw", None)
         if raw and _lib is not None:
@@ -1100,7 +1107,7 @@ class GradList:
 
 def _dense(t: torch.Tensor) -> bool:
     """The elements fill a stretch of memory, in some order of the axes."""
-    if t.is_contiguous():
+    if t.numel() == 0:
         return True
     expect = 1
     for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
