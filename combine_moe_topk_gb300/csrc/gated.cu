@@ -39,7 +39,7 @@ typedef __nv_bfloat16 bf16;
 // consecutive elements to two MMAs as their k pairs, and the accumulator, which
 // drops the bits below its last place, is emptied into an fp32 sum after every
 // chunk.  The warps' sums are added in order through shared memory every 16 columns.
-// One row, 4096 x 4096: 14.1 us (by tiles 24.4), x 14336: 36.9 us, 6.4 TB/s; 8 tokens
+// One row, 4096 x 4096: 12.7 us (by tiles 24.4), x 14336: 35.4 us, 6.6 TB/s; 8 tokens
 // through 64 experts of 2048 x 1408, six each, 34 of them chosen: 63.9 us (by tiles
 // 75.0), 6.1 TB/s.
 // A wait that runs out sets the status and everyone runs on without waiting, so
@@ -51,7 +51,13 @@ constexpr int kFewStages = 6;
 constexpr int kFewTiles = 2;                   // 8 columns of h each, between two joins
 constexpr int kFewCols = 8 * kFewTiles;
 constexpr int kFewSmem = kFewStages * kFewStage;
+constexpr int kAhead = 64 * 1024;              // of a shared expert's W, fetched to L2 in advance
 constexpr int kMaxE = 256;
+
+// To L2; p and bytes are multiples of 16.
+__device__ __forceinline__ void prefetch_bulk(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 
 struct FewArgs {
   const bf16* x;     // [s][ldx]: one block's rows, the dispatched rows, or (inv_row) the token rows
@@ -92,6 +98,16 @@ __global__ void __launch_bounds__(288, 1) few_gated_kernel(const __grid_constant
     fence_barrier_init();
   }
   __syncthreads();
+  if (!kExperts && warp == 8) {
+    // While the kernel before still runs, the first of this SM's rows of W travel to
+    // L2 (a prefetch reads nothing: should they be written meanwhile, the copies below
+    // find what was written).  64 KB an SM: one row, 4096 x 4096, 13.9 -> 12.7 us (128 KB
+    // 12.8, 256 KB 13.3); the tiles' kernel gained nothing by the same.
+    const int c0 = (int)((long long)p.N * blockIdx.x / gridDim.x), c1 = (int)((long long)p.N * (blockIdx.x + 1) / gridDim.x);
+    const int bytes = min(p.K * 2, 16384), n = min(c1 - c0, kAhead / (2 * bytes));
+    for (int i = lane; i < 2 * n; i += 32)
+      prefetch_bulk(p.W + ((long long)(i & 1) * p.N + c0 + (i >> 1)) * p.ldw, (uint32_t)bytes);
+  }
   grid_dependency_wait();
   if constexpr (kExperts) {
     for (int x = threadIdx.x; x < p.e; x += blockDim.x) {

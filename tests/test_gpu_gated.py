@@ -190,3 +190,29 @@ def test_results_of_more_than_2_31_elements():
     assert not dx[:-30].any()
     t = slice(s - 30, s)
     check_bwd(dh[t], x[t].contiguous(), W, z[t], "silu", (dx[t], dW, db))
+
+
+@pytest.mark.parametrize("s", [1, 12, 40])
+def test_weights_that_the_kernel_before_has_just_written(s):
+    """The weights' first rows are fetched while the kernel before may still write them: what counts is what it wrote."""
+    K, N = 2048, 1024
+    x = make(s, K, N, seed=s)[0]
+    raw = torch.empty(2 * N, K, dtype=torch.bfloat16, device="cuda")
+
+    def step(wait):
+        W = B.moe_layernorm(raw, None, None, stats=False)  # lets the next kernel start before it ends
+        if wait:
+            torch.cuda.synchronize()
+        return B.moe_gated_linear(x, W)
+
+    raw.normal_()
+    step(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h = step(False)
+    for seed in range(8):
+        raw.copy_(torch.randn(2 * N, K, generator=torch.Generator().manual_seed(seed)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(h, step(True))
