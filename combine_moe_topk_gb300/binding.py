@@ -1063,11 +1063,13 @@ class GradList:
     def __init__(self, tensors):
         self.tensors = tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
         self.device = tensors[0].device if tensors else None
-        self._layout = None
+        self.ordered = True  # every tensor's elements are in the order of its axes
         flat = []
         for i, t in enumerate(tensors):
-            if t.layout != torch.strided or not (t.is_contiguous() or _dense(t)):
-                raise ValueError(f"tensor {i}: gradients must be dense tensors without gaps or overlaps in memory")
+            if t.layout != torch.strided or not t.is_contiguous():
+                if t.layout != torch.strided or not _dense(t):
+                    raise ValueError(f"tensor {i}: gradients must be dense tensors without gaps or overlaps in memory")
+                self.ordered = False
             if t.device != self.device:
                 raise MoEError(1, "GradList", "the tensors are on different devices")
             flat += (t.data_ptr(), t.numel(), _DTYPE.get(t.dtype, -1))
@@ -1091,13 +1093,6 @@ class GradList:
     @property
     def raw(self):
         return self._raw
-
-    @property
-    def layout(self) -> str:
-        """All shapes and strides, to be compared with another list's in one go."""
-        if self._layout is None:
-            self._layout = repr([(tuple(t.shape), t.stride()) for t in self.tensors])
-        return self._layout
 
     def __del__(self):
         raw = getattr(self, "_raw", None)
@@ -1124,8 +1119,10 @@ def _grads(grads) -> GradList:
 def _clip_lists(where: str, grads, out):
     g = _grads(grads)
     o = None if out is None else _grads(out)
-    if o is not None and g.layout != o.layout:
-        raise MoEError(1, where, "out must have the gradients' shapes and strides")
+    if o is not None and not (g.ordered and o.ordered):  # the library compares sizes
+        for a, b in zip(g.tensors, o.tensors):
+            if a.shape != b.shape or a.stride() != b.stride():
+                raise MoEError(1, where, "out must have the gradients' shapes and strides")
     return g, o
 
 

@@ -70,6 +70,8 @@ def test_axes_in_any_order():
     b = torch.randn(3, 5, 7, 2, generator=g).cuda().permute(2, 0, 3, 1)
     check([a, b, torch.randn((), generator=g).cuda()], 0.1)
     check([a, b], 0.1, out=[torch.empty_like(a), torch.empty_like(b)])
+    with pytest.raises(B.MoEError, match="strides"):  # the same sizes in another order
+        B.moe_clip_grad_norm([a, b], 0.1, out=[torch.empty_like(a), torch.empty(b.shape, device="cuda")])
 
 
 # squares that leave fp32's range, up and down, alone and beside ordinary ones
