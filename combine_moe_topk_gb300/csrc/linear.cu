@@ -156,7 +156,8 @@ struct Shape {
 // that is little but its output, 75.7 -> 47 us (44 without the stores, 28
 // without the epilogue: what is left is the tile's hand-over between load,
 // product and epilogue; 38.9 since a gradient's product is compiled without the
-// rest of the epilogue).  Rows of 128 bytes instead of 64 matter to the large
+// rest of the epilogue, 27.9 since accumulators go back without a release at
+// cluster scope).  Rows of 128 bytes instead of 64 matter to the large
 // products (8192 x 4096 x 16384: 566 -> 545 us).
 struct Bulk {
   uint8_t* stage;  // this warp's 4 KB

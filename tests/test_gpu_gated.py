@@ -121,6 +121,12 @@ def test_many_tiles(s, K, N):
     check_bwd(dh, x, W, z, "gelu_tanh", B.moe_gated_linear_bwd(dh, x, W, z, "gelu_tanh"))
 
 
+@pytest.mark.parametrize("s", [1, 40])
+def test_the_longest_contraction(s):
+    x, W, b, _, _ = make(s, 1 << 18, 16, seed=s)
+    check_fwd(x, W, b, "silu", B.moe_gated_linear(x, W, b))
+
+
 @pytest.mark.parametrize("s", [3, 50, 400])
 def test_strided_rows(s):
     x, W, b, dh, z = make(s, 128, 64, seed=s)
