@@ -1171,7 +1171,7 @@ def moe_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None):
 
 def moe_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
                        device_status: torch.Tensor | None = None) -> torch.Tensor:
-    """moe_grad_norm and moe_grad_clip in two kernels; returns the norm before clipping, f32 [1]."""
+    """moe_grad_norm and moe_grad_clip in two kernels at most; returns the norm before clipping, f32 [1]."""
     g, o = _clip_lists("moe_clip_grad_norm", grads, out)
     ro = None if o is None else o.raw
     return _norm_call("moe_clip_grad_norm", g, norm, device_status,

@@ -706,7 +706,8 @@ moe_status moe_grad_norm(moe_tensor_list grads, float* norm, void* workspace, si
  * finite leaves the gradients unscaled (`out` gets copies).  max_norm >= 0. */
 moe_status moe_grad_clip(moe_tensor_list grads, moe_tensor_list out, const float* norm, float max_norm, void* stream);
 
-/* moe_grad_norm and moe_grad_clip in two kernels; norm[0] is written. */
+/* moe_grad_norm and moe_grad_clip in two kernels (a short list: in one); norm[0] is
+ * written. */
 moe_status moe_clip_grad_norm(moe_tensor_list grads, moe_tensor_list out, float max_norm, float* norm, void* workspace,
                               size_t workspace_bytes, int32_t* device_status, void* stream);
 
