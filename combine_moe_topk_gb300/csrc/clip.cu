@@ -40,6 +40,10 @@ constexpr int kPerSm = 2;                              // blocks: 64 KB of loads
 constexpr int kMaxBlocks = kPerSm * 152;
 constexpr int kLarge = 1024, kSmall = 64;              // tensors a launch
 constexpr float kEps = 1e-6f;
+// Largest magnitude whose squares a thread adds unscaled.  A block has at most 2^30 / 304
+// of a list's chunks, under 2^22, and a thread 64 elements of each: 2^28 squares of 2^96.
+constexpr float kTop = 281474976710656.f;               // 2^48
+constexpr float kLow = 8.8817841970012523e-16f;         // 2^-50: below it squares would lose bits
 
 // chunk c of tensor i: first[i] <= c < first[i + 1] (the last ends at `chunks`).
 template <int C>
@@ -180,8 +184,7 @@ __device__ __forceinline__ double sum_block(const Table<C>& t, double* red) {
   float top = 0.f;
   double sum = sum_range<C, false>(t, 1.f, top);
   top = block_max(top, reinterpret_cast<float*>(red));
-  // 64 squares of 2^60 stay in range; below 2^-50 squares would lose bits
-  if (top < CUDART_INF_F && (top > 1.152921504606847e18f || (top > 0.f && top < 8.8817841970012523e-16f))) {
+  if (top < CUDART_INF_F && (top > kTop || (top > 0.f && top < kLow))) {
     const int e = ilogbf(top);
     const int by = e < -100 ? 100 : -e;  // e goes down to -149, 2^149 is out of range
     float unused = 0.f;
