@@ -209,8 +209,10 @@ __device__ __forceinline__ double join(const double* part, int parts, double* re
   return block_sum(v, red);
 }
 
+__device__ __forceinline__ float norm_of(double total) { return (float)sqrt(total); }  // an infinity past fp32's range
+
 __device__ __forceinline__ void report(double total, float* norm, int32_t* status) {
-  const float n = (float)sqrt(total);  // an infinity past fp32's range
+  const float n = norm_of(total);
   *norm = n;
   if (!(n < CUDART_INF_F)) raise_status(status, MOE_DEV_NONFINITE);
 }
@@ -292,12 +294,14 @@ __device__ __forceinline__ void scale_chunk(const T* p, T* q, long long n, int c
   if ((int)threadIdx.x < s.trail) single(s.first + (long long)s.pieces * kElems + threadIdx.x);
 }
 
-// This block's chunks, from the last to the first, clipped to max_norm; n is the norm.
+// This block's chunks, from the last to the first, clipped to max_norm; n is the norm
+// as the caller sees it, so that a norm that was given and one that was just computed
+// lead to the same bits.
 template <int C>
-__device__ __forceinline__ void clip_range(const Table<C>& t, double n, float max_norm) {
+__device__ __forceinline__ void clip_range(const Table<C>& t, float n, float max_norm) {
   // a norm that is not finite says nothing: the gradients stay as they are
-  const bool scales = (float)n < CUDART_INF_F && (double)max_norm < n + (double)kEps;
-  const float coef = scales ? (float)((double)max_norm / (n + (double)kEps)) : 1.f;
+  const bool scales = n < CUDART_INF_F && (double)max_norm < (double)n + (double)kEps;
+  const float coef = scales ? (float)((double)max_norm / ((double)n + (double)kEps)) : 1.f;
   const int last = t.chunks - 1 - (int)blockIdx.x;
   int i = last >= 0 ? tensor_of(t, last, 0) : 0, then = i;
   for (int c = last; c >= 0; c -= (int)gridDim.x, i = then) {
@@ -319,11 +323,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
                      int32_t* status) {
   __shared__ double red[kThreads / 32];
   grid_dependency_wait();
-  double n;
+  float n;
   if (part) {
     const double total = join(part, parts, red);
     if (writes && blockIdx.x == 0 && threadIdx.x == 0) report(total, norm, status);
-    n = sqrt(total);
+    n = norm_of(total);
   } else {
     n = ld_plain(norm);
   }
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) grad_small_kernel(const __grid_const
   cluster_arrive();
   if (blockIdx.x == 0 && threadIdx.x == 0) report(total, norm, status);
   grid_dependents_launch();
-  if (clips) clip_range(t, sqrt(total), max_norm);
+  if (clips) clip_range(t, norm_of(total), max_norm);
   cluster_wait();  // nobody reads this block's sum any more
 }
 

@@ -1,5 +1,6 @@
 """The gradient norm of lists that give a block many chunks, with values whose squares
-only add up past fp32's range.
+only add up past fp32's range, and the coefficient's agreement with the norm that
+is returned.
 
 Equal values, so that the norm has a closed form: v sqrt(n).  Tolerances: the norm as
 in the tests of short lists, (16 + 2) 2^-24; a clipped value is off by the norm's and the
@@ -38,3 +39,14 @@ def test_huge_values_beside_ordinary_ones():
     norm = float(B.moe_grad_norm([g]))
     want = float(g.double().square().sum().sqrt())
     assert abs(norm - want) <= 18 * U * want
+
+
+@pytest.mark.parametrize("n", [40, 5000, 60_000, 3_000_000])
+def test_both_ways_to_clip_give_the_same_bits(n):
+    """The coefficient is that of the norm which is returned, computed in one call or given to another."""
+    for seed in range(12):
+        g = torch.randn(n, generator=torch.Generator().manual_seed(seed)).cuda()
+        one, two = g.clone(), g.clone()
+        norm = B.moe_clip_grad_norm([one], 0.37)
+        B.moe_grad_clip([two], norm, 0.37)
+        assert torch.equal(one, two), seed
