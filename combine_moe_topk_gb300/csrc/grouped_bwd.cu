@@ -25,6 +25,14 @@
 // waits for (the second CTA's word through the async proxy).  An expert without rows
 // gets zeros.
 //
+// The accumulator drops the bits below its last place at every step: n terms of one
+// sign come out about n / 16 units of 2^-24 short.  So a contraction of more than 2^17
+// terms hands it over every 2^17 and the epilogue adds these parts up in fp32
+// (whatever the length, sums are at most 2^-10 short, a quarter of what rounding to
+// bf16 may take; 2^22 terms in one accumulator were 2 % short).  The running sums live in local memory: a
+// part takes some 600 us, so their traffic does not matter, and the registers of
+// the short contractions stay as they were.
+//
 // Bound by the tensor cores where segments are long (1024 rows, 4096 x 1024: dX 1.69,
 // dW 1.59 PFLOP/s), by memory where they are short (174 rows of 128 experts, 2816 x 704:
 // dX 119 us, 5.6 TB/s; dW 125 us, 5.3 TB/s, against 84 for zeros alone).
@@ -62,6 +70,7 @@ constexpr int kSmem = kStages * kStage + kEpiWarps * kPiece<kWeights> + 1024;
 constexpr int kTile = 256;
 constexpr int kTmemCols = 512;
 constexpr int kMaxE = 256;
+constexpr int kPartBlocks = (1 << 17) / kStageK;  // K blocks that one accumulator takes
 
 struct Args {
   const int32_t* offsets;
@@ -266,36 +275,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0, u = pair; u < units && ok; u = pick<kWeights>(++i, pair, pairs)) {
       const Unit t = unit_of<kWeights>(u, p, s_blk, s_order, s_cnt);
-      if (t.blocks == 0) continue;
-      if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
-        ok = false;
-        break;
-      }
-      tphase[acc] ^= 1u;
-      tc_fence_after();
-      const uint32_t dt = tbase + (uint32_t)(acc * kTile);
-      for (int kb = 0; kb < t.blocks; ++kb) {
-        if (!mbar_wait_cluster_limited(&full[r.stage], r.phase, p.timeout_ns)) {
+      for (int kb0 = 0; kb0 < t.blocks && ok; kb0 += kPartBlocks) {
+        if (!mbar_wait_cluster_limited(&tempty[acc], tphase[acc] ^ 1u, p.timeout_ns)) {
           ok = false;
           break;
         }
+        tphase[acc] ^= 1u;
         tc_fence_after();
-        const uint32_t sa = smem_addr(smem + r.stage * kStage);
-        const int left = kWeights ? t.count - kb * kStageK : kStageK;
+        const uint32_t dt = tbase + (uint32_t)(acc * kTile);
+        const int kb1 = min(t.blocks, kb0 + kPartBlocks);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_cluster_limited(&full[r.stage], r.phase, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_addr(smem + r.stage * kStage);
+          const int left = kWeights ? t.count - kb * kStageK : kStageK;
 #pragma unroll
-        for (int q = 0; q < kKB; ++q) {
-          const uint64_t ad = tile_desc<kWeights>(sa + q * kSub), bd = tile_desc<true>(sa + (kKB + q) * kSub);
+          for (int q = 0; q < kKB; ++q) {
+            const uint64_t ad = tile_desc<kWeights>(sa + q * kSub), bd = tile_desc<true>(sa + (kKB + q) * kSub);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (64 * q + 16 * kk < left)
-              mma<2>(dt, ad + kk * kstep<kWeights>(), bd + kk * kstep<true>(), idesc, (kb | q | kk) != 0);
+            for (int kk = 0; kk < 4; ++kk)
+              if (64 * q + 16 * kk < left)
+                mma<2>(dt, ad + kk * kstep<kWeights>(), bd + kk * kstep<true>(), idesc, (kb > kb0) | (q | kk) != 0);
+          }
+          mma_commit_pair(&empty[r.stage]);
+          r.next();
         }
-        mma_commit_pair(&empty[r.stage]);
-        r.next();
+        if (!ok) break;
+        mma_commit_pair(&tfull[acc]);
+        acc ^= 1;
       }
-      if (!ok) break;
-      mma_commit_pair(&tfull[acc]);
-      acc ^= 1;
     }
     if (!ok) {
       // a wait ran out: let the MMAs issued so far finish reading shared memory
@@ -363,15 +374,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = t.m0 + 128 * (int)rank + 32 * ew;
       const int rows = (kWeights ? p.M : t.count) - r0;
       const bool zeros = t.blocks == 0;
-      if (!zeros) {
+      auto filled = [&]() {  // the accumulator is ready; its address for this warp
         if (!__all_sync(0xffffffffu, mbar_wait_limited(&tfull[acc], tphase[acc], p.timeout_ns))) {
           ok = false;
-          break;
+          return;
         }
         tphase[acc] ^= 1u;
         tc_fence_after();
+      };
+      auto lanes_of = [&]() { return tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * kTile + 128 * half); };
+      const bool parts = t.blocks > kPartBlocks;
+      float sum[4][32];  // of the parts but the last
+      if (parts) {
+#pragma unroll 1
+        for (int kb = 0; kb + kPartBlocks < t.blocks && ok; kb += kPartBlocks) {
+          filled();
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(lanes_of() + (uint32_t)(32 * c), v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c][j] = kb ? sum[c][j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+          }
+          release();
+          acc ^= 1;
+        }
+        if (!ok) break;
       }
-      const uint32_t lanes = tbase + ((uint32_t)(32 * ew) << 16) + (uint32_t)(acc * kTile + 128 * half);
+      if (!zeros) filled();
+      if (!ok) break;
+      const uint32_t lanes = lanes_of();
       auto words = [&](int c, uint32_t (&w)[16]) {  // 32 columns of this lane's row
         if (zeros) {
 #pragma unroll
@@ -383,6 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(lanes + (uint32_t)(32 * c), v);
 #pragma unroll
         for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        if (parts) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] += sum[c][j];
+        }
         pack_bf16(f, w);
       };
       if constexpr (kWeights) {

@@ -653,10 +653,9 @@ moe_status moe_dispatch_grouped_gated(moe_handle h, int s, int rows, int K, int 
  *   dX[r] = dY[r] W[x] for rows that a route owns (others are not written),
  *   dW[x] = sum over the rows r of expert x of dY[r]^T X[r], 0 without rows.
  * dY [rows,N], X and dX [rows,K], W and dW [e,N,K], bf16; dX and dW nullable.  fp32 sums
- * in a fixed order, rounded once.  (Of an expert with more than 2^18 rows, and of N
- * past that, the accumulator may lose up to a 16th of the terms in units of 2^-24 of
- * a sum of one sign.)  rows = 0: dW
- * is zeroed.  Errors as moe_grouped_gemm. */
+ * in a fixed order, rounded once, over any number of rows and any N (a sum of one sign
+ * may be up to 2^-10 of itself short, see moe_linear).  rows = 0: dW is zeroed.  Errors
+ * as moe_grouped_gemm. */
 moe_status moe_grouped_gemm_bwd(moe_handle h, int rows, int K, int N, const void* dY, const void* X, const void* W, void* dX,
                                 void* dW, void* stream);
 
