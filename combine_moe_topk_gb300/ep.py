@@ -44,6 +44,7 @@ import dataclasses
 
 import torch
 
+from . import autograd as A
 from . import binding as B
 
 
@@ -213,14 +214,21 @@ class ExpertParallelMoE:
 
 def clip_grad_norm(sharded, replicated, max_norm: float, group=None) -> torch.Tensor:
     """Clip an expert-parallel model's gradients, in place, to one norm over all ranks: ``sharded`` are this rank's own
-    (its experts'), ``replicated`` those that every rank holds alike (counted once).  Returns the norm before that, f32
-    [1], the same on every rank; one all-reduce of one number.  Squares travel in 64 bits, so that they stay in range."""
+    (its experts'), ``replicated`` those that every rank holds alike (the group's first rank counts them).  Returns the
+    norm before that, f32 [1], the same bits on every rank; one all-reduce of one number.  Squares travel in 64 bits, so
+    that they stay in range.  A norm that is not finite leaves the gradients of all ranks as they are, and every rank's
+    ``autograd.status`` reports it."""
     import torch.distributed as dist
 
     sharded, replicated = B.GradList(sharded), B.GradList(replicated)
-    own = B.moe_grad_norm(sharded).double().square()
-    dist.all_reduce(own, group=group)
-    norm = (own + B.moe_grad_norm(replicated).double().square()).sqrt().float()
+    total = B.moe_grad_norm(sharded).double().square()
+    if dist.get_rank(group) == 0:
+        total = total + B.moe_grad_norm(replicated).double().square()
+    dist.all_reduce(total, group=group)
+    norm = total.sqrt().float()
+    word = A._status(norm)
+    if word is not None:
+        B.moe_grad_norm([norm], device_status=word)  # its own norm: sets the bit where it is not finite
     B.moe_grad_clip(sharded, norm, max_norm)
     B.moe_grad_clip(replicated, norm, max_norm)
     return norm
