@@ -40,6 +40,7 @@ group.  A batch of s tokens per rank sends at most s*R rows.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -220,15 +221,19 @@ def clip_grad_norm(sharded, replicated, max_norm: float, group=None) -> torch.Te
     ``autograd.status`` reports it."""
     import torch.distributed as dist
 
-    sharded, replicated = B.GradList(sharded), B.GradList(replicated)
-    total = B.moe_grad_norm(sharded).double().square()
-    if dist.get_rank(group) == 0:
-        total = total + B.moe_grad_norm(replicated).double().square()
-    dist.all_reduce(total, group=group)
-    norm = total.sqrt().float()
-    word = A._status(norm)
-    if word is not None:
-        B.moe_grad_norm([norm], device_status=word)  # its own norm: sets the bit where it is not finite
-    B.moe_grad_clip(sharded, norm, max_norm)
-    B.moe_grad_clip(replicated, norm, max_norm)
+    sharded, replicated = ([g] if isinstance(g, torch.Tensor) else list(g) for g in (sharded, replicated))
+    device = next((t.device for t in (*sharded, *replicated)), None)
+    # a list without tensors belongs to the current device: to that of the other list's
+    with torch.cuda.device(device) if device is not None and device.type == "cuda" else contextlib.nullcontext():
+        sharded, replicated = B.GradList(sharded), B.GradList(replicated)
+        total = B.moe_grad_norm(sharded).double().square()
+        if dist.get_rank(group) == 0:
+            total = total + B.moe_grad_norm(replicated).double().square()
+        dist.all_reduce(total, group=group)
+        norm = total.sqrt().float()
+        word = A._status(norm)
+        if word is not None:
+            B.moe_grad_norm([norm], device_status=word)  # its own norm: sets the bit where it is not finite
+        B.moe_grad_clip(sharded, norm, max_norm)
+        B.moe_grad_clip(replicated, norm, max_norm)
     return norm

@@ -85,3 +85,50 @@ def test_every_rank_clips_to_the_same_norm(case):
     for _, norm, _, before, after in got:
         for b, a in zip(before, after):
             assert all(abs(y - x * (0.5 / (norm + 1e-6))) <= 1e-6 * abs(x) for x, y in zip(b, a))
+
+
+# ---- the calls of the ranks' clipping where a rank holds only one kind of gradients -------
+
+class _Far:
+    """A gradient on a device that is not the current one."""
+    device = torch.device("cuda", 1)
+
+
+@pytest.fixture
+def one_rank(monkeypatch):
+    """A group of one rank; the devices that are made current, and under which device each kernel is called."""
+    at, log = [0], []
+
+    class device:
+        def __init__(self, d):
+            self.to = torch.device(d).index
+
+        def __enter__(self):
+            at.append(self.to)
+
+        def __exit__(self, *exc):
+            at.pop()
+
+    class grad_list(list):
+        def __init__(self, tensors):
+            super().__init__(tensors)
+            self.at = self[0].device.index if self else at[-1]  # without tensors: the current device
+
+    def norm(g, norm=None, device_status=None):
+        log.append(("norm", g.at))
+        return torch.ones(1)
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(B, "GradList", grad_list)
+    monkeypatch.setattr(B, "moe_grad_norm", norm)
+    monkeypatch.setattr(B, "moe_grad_clip", lambda g, norm, max_norm, out=None: log.append(("clip", g.at)))
+    monkeypatch.setattr(A, "_status", lambda t: None)
+    dist.init_process_group("gloo", init_method=f"tcp://127.0.0.1:{32900 + os.getpid() % 1000}", rank=0, world_size=1)
+    yield log
+    dist.destroy_process_group()
+
+
+@pytest.mark.parametrize("sharded,replicated", [([], [_Far()]), ([_Far()], []), ([_Far()], (t for t in [_Far()]))])
+def test_all_kernels_run_on_the_gradients_device(one_rank, sharded, replicated):
+    EP.clip_grad_norm(sharded, replicated, 1.0)
+    assert one_rank == [("norm", 1), ("norm", 1), ("clip", 1), ("clip", 1)]
