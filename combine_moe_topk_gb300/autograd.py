@@ -276,38 +276,48 @@ def gated_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = N
     return GatedLinearFn.apply(_strided(x, 8), _strided(W, 8), _rows(bias), act, torch.is_grad_enabled())
 
 
+def _zeros(handle: B.Handle, t: torch.Tensor, name: str, cols: int) -> dict:
+    """The argument `name`, [rows, cols] zeros, for a call that leaves rows of no route as they are, where a layout has
+    such rows; dispatch and the combine's backward pass zero them too."""
+    if not getattr(handle, "gaps", False):
+        return {}
+    return {name: torch.zeros(handle.rows, cols, dtype=t.dtype, device=t.device)}
+
+
 class GroupedGemmFn(torch.autograd.Function):
-    """Y[r] = X[r] W[x]^T over the experts' row segments of a handle."""
+    """Y[r] = X[r] W[x]^T over the experts' row segments of a handle.  Rows of no route (capacity slots, padding) are zero
+    in Y and in X's gradient: what comes between these calls may sum over all rows (a bias of the hidden rows)."""
 
     @staticmethod
     def forward(ctx, X: torch.Tensor, W: torch.Tensor, handle: B.Handle):
         ctx.handle = handle
         ctx.save_for_backward(X, W)
-        return B.moe_grouped_gemm(handle, X, W)
+        return B.moe_grouped_gemm(handle, X, W, **_zeros(handle, X, "Y", W.shape[1]))
 
     @staticmethod
     @first_order
     def backward(ctx, dY: torch.Tensor):
         X, W = ctx.saved_tensors
         need_x, need_w, _ = ctx.needs_input_grad
-        dX, dW = B.moe_grouped_gemm_bwd(ctx.handle, _rows(dY), X, W, need_x, need_w)
+        zeros = _zeros(ctx.handle, X, "dX", X.shape[1]) if need_x else {}
+        dX, dW = B.moe_grouped_gemm_bwd(ctx.handle, _rows(dY), X, W, need_x, need_w, **zeros)
         return dX, dW, None
 
 
 def grouped_gemm(X: torch.Tensor, W: torch.Tensor, handle: B.Handle) -> torch.Tensor:
-    """Y bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, N, K]."""
+    """Y bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, N, K]; 0 in rows of no route."""
     return GroupedGemmFn.apply(_rows(X), _rows(W), handle)
 
 
 class GroupedGatedFn(torch.autograd.Function):
     """H[r] = act(X[r] Wg[x]^T) * (X[r] Wu[x]^T) over the experts' row segments.  gather: from the token rows x, without a
-    dispatched buffer; the backward pass then dispatches them again."""
+    dispatched buffer; the backward pass then dispatches them again.  Rows of no route are zero, as in GroupedGemmFn."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str, gather: bool, grad: bool):
         save_z = grad and any(ctx.needs_input_grad[:2])
         call = B.moe_dispatch_grouped_gated if gather else B.moe_grouped_gated
-        out = call(handle, x, W, act, save_z=save_z)
+        out = call(handle, x, W, act, save_z=save_z, **_zeros(handle, x, "H", W.shape[1] // 2))
         H, Z = out if save_z else (out, None)
         ctx.save_for_backward(x, W, Z)
         ctx.handle, ctx.act, ctx.gather = handle, act, gather
@@ -319,14 +329,16 @@ class GroupedGatedFn(torch.autograd.Function):
         x, W, Z = ctx.saved_tensors
         need_x, need_w = ctx.needs_input_grad[:2]
         X = B.moe_dispatch(ctx.handle, x) if ctx.gather else x
-        dX, dW = B.moe_grouped_gated_bwd(ctx.handle, _rows(dH), X, W, Z, ctx.act, need_x, need_w)
+        zeros = _zeros(ctx.handle, x, "dX", x.shape[1]) if need_x and not ctx.gather else {}
+        dX, dW = B.moe_grouped_gated_bwd(ctx.handle, _rows(dH), X, W, Z, ctx.act, need_x, need_w, **zeros)
         if ctx.gather and need_x:
             dX = B.moe_dispatch_bwd(ctx.handle, dX)
         return dX, dW, None, None, None, None
 
 
 def grouped_gated(X: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str = "silu") -> torch.Tensor:
-    """H bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, 2N, K], each expert's gate rows first."""
+    """H bf16 [rows, N] of the dispatched rows X [rows, K] and W [e, 2N, K], each expert's gate rows first; 0 in rows of no
+    route."""
     return GroupedGatedFn.apply(_rows(X), _rows(W), handle, act, False, torch.is_grad_enabled())
 
 

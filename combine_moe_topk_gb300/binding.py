@@ -286,9 +286,9 @@ class _DeviceArray:
 
 
 class Handle:
-    """Owns a ``moe_handle``; destroys it when garbage-collected."""
+    """Owns a ``moe_handle``; destroys it when garbage-collected.  ``gaps``: there may be rows that no route owns."""
 
-    def __init__(self, raw: ctypes.c_void_p, device: torch.device):
+    def __init__(self, raw: ctypes.c_void_p, device: torch.device, gaps: bool = False):
         self._raw = raw
         self.device = device
         info = LayoutInfo()
@@ -297,6 +297,7 @@ class Handle:
         self.s, self.e, self.k = info.s, info.e, info.k
         self.capacity, self.R, self.rows = info.capacity, info.R, info.rows
         self.priority, self.pad_multiple = info.priority, info.pad_multiple
+        self.gaps = gaps or self.capacity > 0 or self.pad_multiple > 1
 
     @property
     def raw(self):
@@ -433,7 +434,7 @@ def moe_dispatch_layout_ex(topk_idx: torch.Tensor, e: int, capacity: int = 0, nu
     rc = lib().moe_dispatch_layout_ex(_ptr(topk_idx), s, int(e), k, ctypes.byref(opt), _stream(dev),
                                       ctypes.byref(raw))
     _check(rc, "moe_dispatch_layout_ex")
-    return Handle(raw, dev)
+    return Handle(raw, dev, bool(absent_routes) or rows_bound != 0)
 
 
 def moe_layout_create(s: int, e: int, k: int, capacity: int = 0, num_virtual_ranks: int = 0,
@@ -450,7 +451,7 @@ def moe_layout_create(s: int, e: int, k: int, capacity: int = 0, num_virtual_ran
     with torch.cuda.device(dev):
         rc = lib().moe_layout_create(int(s), int(e), int(k), ctypes.byref(opt), _stream(dev), ctypes.byref(raw))
     _check(rc, "moe_layout_create")
-    return Handle(raw, dev)
+    return Handle(raw, dev, bool(absent_routes) or rows_bound != 0)
 
 
 def moe_layout_rebuild(h: Handle, topk_idx: torch.Tensor) -> Handle:
