@@ -311,7 +311,7 @@ def grouped_gemm(X: torch.Tensor, W: torch.Tensor, handle: B.Handle) -> torch.Te
 
 class GroupedGatedFn(torch.autograd.Function):
     """H[r] = act(X[r] Wg[x]^T) * (X[r] Wu[x]^T) over the experts' row segments.  gather: from the token rows x, without a
-    dispatched buffer; the backward pass then dispatches them again.  Rows of no route are zero, as in GroupedGemmFn."""
+    dispatched buffer; for dW the backward pass dispatches them again.  Rows of no route are zero, as in GroupedGemmFn."""
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, W: torch.Tensor, handle: B.Handle, act: str, gather: bool, grad: bool):
@@ -328,7 +328,7 @@ class GroupedGatedFn(torch.autograd.Function):
     def backward(ctx, dH: torch.Tensor):
         x, W, Z = ctx.saved_tensors
         need_x, need_w = ctx.needs_input_grad[:2]
-        X = B.moe_dispatch(ctx.handle, x) if ctx.gather else x
+        X = x if not ctx.gather else B.moe_dispatch(ctx.handle, x) if need_w else None  # only dW reads them
         zeros = _zeros(ctx.handle, x, "dX", x.shape[1]) if need_x and not ctx.gather else {}
         dX, dW = B.moe_grouped_gated_bwd(ctx.handle, _rows(dH), X, W, Z, ctx.act, need_x, need_w, **zeros)
         if ctx.gather and need_x:

@@ -959,12 +959,12 @@ def moe_gated_linear_bwd(dh: torch.Tensor, x: torch.Tensor, W: torch.Tensor, z: 
     return dx, dW, db
 
 
-def _check_experts(where: str, h: Handle, x: torch.Tensor, W: torch.Tensor, gated: bool, act: str = "none"):
-    """(rows of x, K, N) of an expert product's operands."""
-    s, K = _rows2(x, "x")
+def _check_experts(where: str, h: Handle, x: torch.Tensor | None, W: torch.Tensor, gated: bool, act: str = "none"):
+    """(rows of x, K, N) of an expert product's operands; without x the handle's rows."""
+    s, K = _rows2(x, "x") if x is not None else (h.rows, W.shape[-1])
     if W.dim() != 3 or W.shape[0] != h.e or W.shape[2] != K or (gated and W.shape[1] % 2):
         raise MoEError(1, where, "W must be [e, 2N, K], the gate's rows first" if gated else "W must be [e, N, K]")
-    if x.dtype != torch.bfloat16 or W.dtype != torch.bfloat16:
+    if (x is not None and x.dtype != torch.bfloat16) or W.dtype != torch.bfloat16:
         raise MoEError(3, where, "x and W must be bf16")
     if act not in ACT:
         raise MoEError(1, where, f"act must be one of {', '.join(ACT)}")
@@ -1012,11 +1012,13 @@ def moe_dispatch_grouped_gated(h: Handle, x: torch.Tensor, W: torch.Tensor, act:
 
 
 def _grouped_bwd_args(where: str, h: Handle, D, X, W, need_dx, need_dw, dX, dW, gated: bool, act: str = "none"):
+    if X is None and need_dw:
+        raise MoEError(1, where, "dW needs X")
     rows, K, N = _check_experts(where, h, X, W, gated, act)
     _bf16(where, D, "the result's gradient", rows, N)
     _bf16(where, dX, "dX", rows, K)
     _bf16(where, dW, "dW", *W.shape)
-    new = _new(X)
+    new = _new(W)
     if dX is None and need_dx:
         dX = new(torch.bfloat16, rows, K)
     if dW is None and need_dw:
@@ -1024,32 +1026,33 @@ def _grouped_bwd_args(where: str, h: Handle, D, X, W, need_dx, need_dw, dX, dW, 
     return rows, K, N, dX if need_dx else None, dW if need_dw else None
 
 
-def moe_grouped_gemm_bwd(h: Handle, dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, need_dx: bool = True,
+def moe_grouped_gemm_bwd(h: Handle, dY: torch.Tensor, X: torch.Tensor | None, W: torch.Tensor, need_dx: bool = True,
                          need_dw: bool = True, dX: torch.Tensor | None = None, dW: torch.Tensor | None = None):
     """Backward of moe_grouped_gemm: (dY bf16 [rows,N], X bf16 [rows,K], W bf16
     [e,N,K]) -> (dX [rows,K], dW [e,N,K]), None for those not needed.  Rows of
-    dX that no route owns are not written."""
+    dX that no route owns are not written.  X may be None without dW."""
     rows, K, N, dX, dW = _grouped_bwd_args("moe_grouped_gemm_bwd", h, dY, X, W, need_dx, need_dw, dX, dW, False)
-    rc = lib().moe_grouped_gemm_bwd(h.raw, rows, K, N, _addr(dY), _addr(X), _addr(W), _addr(dX), _addr(dW), _raw_stream(X))
+    rc = lib().moe_grouped_gemm_bwd(h.raw, rows, K, N, _addr(dY), _addr(X), _addr(W), _addr(dX), _addr(dW), _raw_stream(W))
     if rc:
         _check(rc, "moe_grouped_gemm_bwd")
     return dX, dW
 
 
-def moe_grouped_gated_bwd(h: Handle, dH: torch.Tensor, X: torch.Tensor, W: torch.Tensor, Z: torch.Tensor,
+def moe_grouped_gated_bwd(h: Handle, dH: torch.Tensor, X: torch.Tensor | None, W: torch.Tensor, Z: torch.Tensor,
                           act: str = "silu", need_dx: bool = True, need_dw: bool = True,
                           dX: torch.Tensor | None = None, dW: torch.Tensor | None = None):
     """Backward of moe_grouped_gated (X = moe_dispatch's output also for the
     gathering form): (dH bf16 [rows,N], X bf16 [rows,K], W bf16 [e,2N,K], Z bf16
-    [rows,2N]) -> (dX [rows,K], dW [e,2N,K]), None for those not needed."""
+    [rows,2N]) -> (dX [rows,K], dW [e,2N,K]), None for those not needed.  X may
+    be None without dW."""
     where = "moe_grouped_gated_bwd"
     rows, K, N, dX, dW = _grouped_bwd_args(where, h, dH, X, W, need_dx, need_dw, dX, dW, True, act)
     _bf16(where, Z, "Z", rows, 2 * N)
     L = lib()
     nbytes = L.moe_grouped_gated_bwd_workspace(rows, N) if need_dx or need_dw else 0
-    ws = _new(X)(torch.uint8, nbytes) if nbytes else None
+    ws = _new(W)(torch.uint8, nbytes) if nbytes else None
     rc = L.moe_grouped_gated_bwd(h.raw, rows, K, N, ACT[act], _addr(dH), _addr(X), _addr(W), _addr(Z), _addr(dX), _addr(dW),
-                                 _addr(ws), nbytes, _raw_stream(X))
+                                 _addr(ws), nbytes, _raw_stream(W))
     if rc:
         _check(rc, where)
     return dX, dW

@@ -72,3 +72,21 @@ def test_rows_of_no_route_are_zero_through_autograd(kind, gather):
         if not gather:
             assert not X.grad[~owned].any()
         assert torch.isfinite(W.grad).all() and torch.isfinite(Wd.grad).all()
+
+
+@pytest.mark.parametrize("kind", ["dropless", "capacity"])
+def test_frozen_experts_give_the_same_gradient(kind):
+    s, e, k, K, N = 90, 6, 2, 64, 72
+    g = torch.Generator().manual_seed(5)
+    idx = torch.stack([torch.randperm(e, generator=g)[:k] for _ in range(s)]).int().cuda()
+    h = handle(kind, idx, e)
+    x, W = torch.randn(s, K, generator=g).bfloat16().cuda(), torch.randn(e, 2 * N, K, generator=g).bfloat16().cuda()
+    d = torch.randn(h.rows, N, generator=g).bfloat16().cuda()
+    grads, dispatches = [], []
+    for frozen in (True, False):
+        X, w = x.clone().requires_grad_(), W.clone().requires_grad_(not frozen)
+        before = B.moe_launch_count("dispatch")
+        A.dispatch_grouped_gated(X, w, h, "silu").backward(d)
+        grads.append(X.grad)
+        dispatches.append(B.moe_launch_count("dispatch") - before)
+    assert torch.equal(*grads) and dispatches == [0, 1]
