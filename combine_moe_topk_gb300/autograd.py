@@ -277,8 +277,9 @@ def gated_linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = N
 
 
 def _zeros(handle: B.Handle, t: torch.Tensor, name: str, cols: int) -> dict:
-    """The argument `name`, [rows, cols] zeros, for a call that leaves rows of no route as they are, where a layout has
-    such rows; dispatch and the combine's backward pass zero them too."""
+    """The argument `name`, [rows, cols] zeros, for a call that leaves rows of no route as they are, where a layout can have
+    such rows (capacity slots and padding, which dispatch and the combine's backward pass zero too; rows behind the last
+    segment)."""
     if not getattr(handle, "gaps", False):
         return {}
     return {name: torch.zeros(handle.rows, cols, dtype=t.dtype, device=t.device)}

@@ -655,7 +655,11 @@ cudaError_t launch_dispatch_gemm(const int32_t* offsets, const int32_t* counts, 
 // 43.9 us, two 116.8 / 103.7 and 57.5 / 58.5, four 127.9 / 122.7 and 69.4 / 82.1; 8
 // experts of 4096 x 4096, two 91.7 / 75.9 and 76.6 / 58.5, eight 102.0 / 87.7 and 91.4
 // / 93.2; 128 experts of 4096 x 512, two 164.2 / 139.0 and 62.2 / 67.9, four 178.1 /
-// 165.1 and 78.4 / 94.3.
+// 165.1 and 78.4 / 94.3.  The worst case is every row on one expert: at most rows / 16 =
+// e / 8 of its blocks are streamed, an eighth of what even routing streams, mostly from
+// L2.  Two rows an expert, all on one: 64 experts of 2048 x 1408 15.4 / 21.3 us, 256 of
+// them 16.7 / 76.8 (even routing 473.6 / 447.5); 256 of 4096 x 512 24.8 / 53.6 (353.9 /
+// 301.9).
 static bool few_rows(int rows, int e) { return rows <= kFewRows || rows <= 2LL * e; }
 
 cudaError_t launch_grouped_gated(const int32_t* offsets, const int32_t* counts, int e, int rows, int K, int N, int act,

@@ -612,7 +612,7 @@ __device__ __forceinline__ void join_gated(const GemmArgs& p, const Epi& e, cons
 // 4.4e-6 of the result over 4096 terms, against 6e-7 for fp32 additions), so a
 // product hands its sum over every kExactBlocks K blocks, and the epilogue adds
 // these up in registers.  Where all terms have one sign, n of them come out up to
-// n / 16 units of 2^-24 short: at kLongSum 2^-10, a quarter of what rounding to bf16
+// n / 16 units of 2^-23 short: at kLongSum 2^-9, half of what rounding to bf16
 // may take, so a bf16 output keeps the one accumulator up to there (4096 x 4096 from
 // 2^19 terms takes 20.3 ms this way; that way 13.1, and up to 2e-3 short).
 constexpr int kExactBlocks = 4;

@@ -1,7 +1,7 @@
 """The experts' backward products over contractions past 2^17 terms.
 
-The tensor cores' accumulator drops the bits below its last place: n terms of one sign come out
-up to n / 16 units of 2^-24 short.  It is emptied into an fp32 sum every 2^17 terms, so a sum of any
+The tensor cores' accumulator drops the bits below its last place, up to 2^-23 of the sum at every
+step of 16 terms: n terms of one sign come out up to n / 16 units of 2^-23 short.  It is emptied into an fp32 sum every 2^17 terms, so a sum of any
 length of one sign is at most 2^-10 short, to which the result's rounding adds 2^-8 and the fp32
 sums (33 of them at most here) 2^-18."""
 import pytest
